@@ -580,6 +580,184 @@ MOE_API moe_status moe_slot_push(moe_slot* slot, int64_t full_bytes, int64_t inp
                                  int64_t* offset, uint32_t* forward_flags);
 MOE_API moe_status moe_slot_pop(moe_slot* slot, int64_t offset);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around the routed layer: the norms between blocks, the router's choice and
+ * the weight update.  The pages describe the routed layer alone; these calls
+ * are what a training or serving step runs next to it.  They need no
+ * context.  Buffers are the caller's; calls only enqueue on `stream` (no
+ * allocation, no synchronisation), so they can be captured in a CUDA graph.
+ * Results do not depend on the number of SMs or on timing, except that the
+ * parameter gradients of moe_block_norm_backward are summed in an order that
+ * depends on the device's SM count (fixed on one device).
+ * Types: MOE_TYPE_BF16 or MOE_TYPE_FP32; sums, statistics and products of
+ * sums are FP32 (or wider) and each result is rounded once.
+ */
+typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_FP32 = 1 } moe_type;
+
+/*
+ * Norm after a block, its gate, the scaled residual and the norm before the
+ * next block, in one pass over [T, D] rows:
+ *   p = branch * r_o * (post_weight + weight_offset),  r_o = 1/sqrt(mean_d branch^2 + eps)
+ *   y = residual_scale * x + branch_scale * gate * p
+ *   h = y * r_y * (pre_weight + weight_offset),        r_y = 1/sqrt(mean_d y^2 + eps)
+ * Every part may be left out: branch NULL (p = 0: a norm alone, which takes
+ * no gate and no post_weight), post_weight NULL (p = branch), gate NULL with
+ * MOE_GATE_NONE (1), pre_weight NULL (no h), y NULL (not written).  h is
+ * formed from the unrounded y.
+ *   x, y          [T, D] of residual_type; y may be x (in place)
+ *   branch, h     bf16 [T, D]; h may be branch
+ *   post_weight, pre_weight  [D] of weight_type
+ *   gate          of gate_type: MOE_GATE_CHANNEL [D]; MOE_GATE_GROUP
+ *                 [gate_rows, D], row t taking gate row t / (T / gate_rows)
+ *                 (T % gate_rows == 0; gate_rows = T is a gate of every
+ *                 element); MOE_GATE_TOKEN [T]
+ *   stats         float [2, T] or NULL: r_o (if post_weight) and r_y (if
+ *                 pre_weight), which the backward reads
+ * Strides are elements between rows (0: D); other tensors are contiguous.
+ * Pointers are 16-byte aligned; rows are read in 16-byte pieces if D and the
+ * strides are multiples of 8, else element by element.  D <= 16384.
+ * A row of zeros gives zeros (r = 1/sqrt(eps)).  T may be 0.
+ * Errors: MOE_ERR_INVALID_ARG (null cfg, T < 0, D < 1, unknown types or
+ * modes, eps not finite and positive, scales not finite, a stride in (0, D),
+ * parts that do not belong together, null or misaligned pointers),
+ * MOE_ERR_UNSUPPORTED (D > 16384).
+ *
+ * moe_block_norm_backward: from dy (residual_type, y_stride; NULL = 0) and
+ * dh (bf16, h_stride; with pre_weight), the gradients of y and h, and the
+ * forward's x, branch, gate, weights and stats:
+ *   dx            [T, D] of residual_type, contiguous, or NULL
+ *   dbranch       bf16 [T, D] contiguous (with branch)
+ *   dgate         the gate's shape and type (with gate)
+ *   dpost_weight, dpre_weight   float [D] (with the weights)
+ * y is rebuilt from x and branch in FP32, so x must be the forward's input
+ * (not overwritten by an in-place y).  Each parameter's gradient is
+ * overwritten; with T = 0 it is zero.  `workspace`: at least
+ * moe_block_norm_workspace_bytes (16-byte aligned, contents need not be
+ * kept or cleared; MOE_ERR_CAPACITY if too small).  That size depends on the
+ * current device's SM count; 0 for an invalid cfg.
+ */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_GROUP = 2, MOE_GATE_TOKEN = 3 } moe_gate_mode;
+
+typedef struct {
+  int32_t tokens;          /* T */
+  int32_t d_model;         /* D */
+  moe_type residual_type;  /* x, y, dy, dx */
+  moe_type weight_type;    /* post_weight, pre_weight */
+  moe_type gate_type;
+  moe_gate_mode gate_mode;
+  int32_t gate_rows;       /* MOE_GATE_GROUP */
+  float residual_scale, branch_scale, eps, weight_offset;
+  int64_t x_stride, branch_stride, y_stride, h_stride;
+} moe_block_norm_config;
+
+MOE_API moe_status moe_block_norm_forward(const moe_block_norm_config* cfg, const void* x, const void* branch,
+                                          const void* gate, const void* post_weight, const void* pre_weight, void* y,
+                                          void* h, float* stats, cudaStream_t stream);
+MOE_API size_t moe_block_norm_workspace_bytes(const moe_block_norm_config* cfg);
+MOE_API moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void* x, const void* branch,
+                                           const void* gate, const void* post_weight, const void* pre_weight,
+                                           const float* stats, const void* dy, const void* dh, void* dx, void* dbranch,
+                                           void* dgate, float* dpost_weight, float* dpre_weight, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The router's choice: the ids and scores that moe_forward takes, from the
+ * logits [T, E], and the gradient of the logits from moe_backward's d_scores.
+ *   key = logit + select_bias (FP32, one rounding; select_bias float [E] or
+ *   NULL steers the choice and nothing else).  Each token takes the top_k
+ *   largest keys in descending order, equal keys by ascending expert; a key
+ *   of -inf (a masked expert) is never taken, and places left without an
+ *   expert get id -1 and score 0 (inactive routes).
+ *   scores, times `scale`:
+ *     MOE_SCORE_SOFTMAX  the softmax over all experts' logits at the chosen
+ *                        ones; renormalize: over the chosen ones alone
+ *     MOE_SCORE_SIGMOID  sigmoid(logit); renormalize: divided by the chosen
+ *                        ones' sum + 1e-20
+ *   A row with a NaN or +inf logit (or key) has no choice: ids -1, scores NaN.
+ *   logits     [T, E] of logits_type, rows logits_stride elements apart (0: E)
+ *   ids        int32 [T, top_k];  scores  float [T, top_k]
+ * moe_topk_gate_backward: d_logits [T, E] of logits_type (contiguous,
+ * overwritten) from d_scores [T, top_k] at the forward's ids; an id outside
+ * [0, E) takes no gradient; a row that had no choice because of a NaN or
+ * +inf logit gets NaN.  The selection itself has no gradient.
+ * E <= 1024, top_k <= min(32, E).  T may be 0.  Pointers 16-byte aligned.
+ * Errors: MOE_ERR_INVALID_ARG.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int32_t tokens;         /* T */
+  int32_t num_experts;    /* E */
+  int32_t top_k;
+  moe_type logits_type;
+  moe_score score;
+  int32_t renormalize;    /* 0 or 1 */
+  float scale;
+  int64_t logits_stride;
+} moe_topk_gate_config;
+
+MOE_API moe_status moe_topk_gate_forward(const moe_topk_gate_config* cfg, const void* logits, const float* select_bias,
+                                         int32_t* ids, float* scores, cudaStream_t stream);
+MOE_API moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const void* logits, const int32_t* ids,
+                                          const float* d_scores, void* d_logits, cudaStream_t stream);
+
+/*
+ * Orthogonalised updates of stacked weights, `batch` contiguous matrices
+ * [rows, cols] (the dW13 [E, 2F, D] and dW2 [E, D, F] of moe_backward; W13 as
+ * 2E matrices [F, D] treats gate and up on their own).  `steps` Newton-Schulz
+ * steps with coefficients (a, b, c) each, from X = U / (|U|_F + eps):
+ *   A = X X^T (X^T X if rows > cols),  X <- a X + (b A + c A A) X
+ * which moves every singular value s through a s + b s^3 + c s^5.
+ * Precision: FP16 tensor-core products with FP32 accumulation; X is kept to
+ * 22 bits and the polynomial's diagonal in FP32 between them.  After five
+ * steps the result is within about 1e-3 of the exact one in norm.  Singular
+ * values have to stay below 8 on the way (they do for polynomials that map
+ * [0, 1] into itself or a little above); beyond that the result is NaN or
+ * infinite.  A zero matrix gives zeros.  |U|_F is an FP32 sum of squares.
+ *
+ * moe_orthogonalize: out (bf16 [batch, rows, cols]) from x (x_type).
+ * moe_muon_update, in place on weight and momentum:
+ *   momentum <- mu * momentum + grad
+ *   U = nesterov ? grad + mu * momentum : momentum
+ *   weight <- (1 - lr * weight_decay) * weight - lr * scale * X(U)
+ *   weight      [batch, rows, cols] of weight_type; an FP32 weight may have
+ *               a BF16 copy written beside it (weight_bf16, else NULL)
+ *   grad        of grad_type;  momentum  float
+ *
+ * workspace: 256-byte aligned, contents need not be kept or cleared.  The
+ * call works through the batch in runs of as many matrices as fit:
+ * moe_muon_workspace_bytes(cfg, matrices) is the size for runs of `matrices`
+ * (0 for an invalid cfg); less than one matrix's is MOE_ERR_CAPACITY.
+ * device_error_word: as for moe_forward_static_scratch (a device wait that
+ * ran out of time sets MOE_DEV_ERR_TIMEOUT; never cleared here).
+ * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, batch < 0, sizes
+ * < 1, steps outside [1, MOE_MUON_MAX_STEPS], |coefficient| > 16, eps not
+ * finite and positive, unknown types, rates not finite), MOE_ERR_UNSUPPORTED
+ * (rows or cols above 65536).  batch may be 0.
+ */
+#define MOE_MUON_MAX_STEPS 16
+typedef struct {
+  int32_t batch, rows, cols;
+  int32_t steps;
+  float coefficients[MOE_MUON_MAX_STEPS][3];
+  float eps;
+} moe_muon_config;
+
+typedef struct {
+  float lr, mu, weight_decay, scale;
+  int32_t nesterov;       /* 0 or 1 */
+} moe_muon_rates;
+
+MOE_API size_t moe_muon_workspace_bytes(const moe_muon_config* cfg, int32_t matrices);
+MOE_API moe_status moe_orthogonalize(const moe_muon_config* cfg, const void* x, moe_type x_type, void* out,
+                                     void* workspace, size_t workspace_bytes, uint32_t* device_error_word,
+                                     cudaStream_t stream);
+MOE_API moe_status moe_muon_update(const moe_muon_config* cfg, const moe_muon_rates* rates, void* weight,
+                                   moe_type weight_type, const void* grad, moe_type grad_type, float* momentum,
+                                   void* weight_bf16, void* workspace, size_t workspace_bytes,
+                                   uint32_t* device_error_word, cudaStream_t stream);
+
 /* Library version string. */
 MOE_API const char* moe_version(void);
 

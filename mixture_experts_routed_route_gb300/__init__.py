@@ -7,4 +7,4 @@ workloads.  Importing ``abi`` or ``layer`` fails if the library has not been
 built: there is no CPU or eager fallback.
 """
 
-__all__ = ["abi", "layer", "synth", "build"]
+__all__ = ["abi", "layer", "block", "optim", "synth", "build"]

@@ -81,6 +81,38 @@ class moe_slot(ctypes.Structure):
                 ("flags", ctypes.c_uint32 * MOE_SLOT_MAX_LAYERS)]
 
 
+# moe_type, moe_gate_mode, moe_score
+MOE_TYPE_BF16, MOE_TYPE_FP32 = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_GROUP, MOE_GATE_TOKEN = range(4)
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_MUON_MAX_STEPS = 16
+
+
+class moe_block_norm_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("d_model", ctypes.c_int32), ("residual_type", ctypes.c_int),
+                ("weight_type", ctypes.c_int), ("gate_type", ctypes.c_int), ("gate_mode", ctypes.c_int),
+                ("gate_rows", ctypes.c_int32), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("branch_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64)]
+
+
+class moe_topk_gate_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("logits_type", ctypes.c_int), ("score", ctypes.c_int), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("logits_stride", ctypes.c_int64)]
+
+
+class moe_muon_config(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("coefficients", ctypes.c_float * 3 * MOE_MUON_MAX_STEPS),
+                ("eps", ctypes.c_float)]
+
+
+class moe_muon_rates(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("mu", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float), ("nesterov", ctypes.c_int32)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, fn, status):
         super().__init__(f"{fn} returned {STATUS_NAMES.get(status, status)}")
@@ -128,6 +160,18 @@ _SIGNATURES = {
     "moe_forward_static_scratch": (ctypes.c_int, [ctypes.POINTER(moe_config), ctypes.c_int32, _P, _P, _P,
                                                   ctypes.POINTER(moe_weight), ctypes.POINTER(moe_weight), _P,
                                                   ctypes.c_uint32, _P, _P]),
+    "moe_block_norm_forward": (ctypes.c_int, [ctypes.POINTER(moe_block_norm_config), _P, _P, _P, _P, _P, _P, _P, _P,
+                                              _P]),
+    "moe_block_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_block_norm_config)]),
+    "moe_block_norm_backward": (ctypes.c_int, [ctypes.POINTER(moe_block_norm_config)] + [_P] * 14
+                                + [ctypes.c_size_t, _P]),
+    "moe_topk_gate_forward": (ctypes.c_int, [ctypes.POINTER(moe_topk_gate_config), _P, _P, _P, _P, _P]),
+    "moe_topk_gate_backward": (ctypes.c_int, [ctypes.POINTER(moe_topk_gate_config), _P, _P, _P, _P, _P]),
+    "moe_muon_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_muon_config), ctypes.c_int32]),
+    "moe_orthogonalize": (ctypes.c_int, [ctypes.POINTER(moe_muon_config), _P, ctypes.c_int, _P, _P, ctypes.c_size_t, _P,
+                                         _P]),
+    "moe_muon_update": (ctypes.c_int, [ctypes.POINTER(moe_muon_config), ctypes.POINTER(moe_muon_rates), _P,
+                                       ctypes.c_int, _P, ctypes.c_int, _P, _P, _P, ctypes.c_size_t, _P, _P]),
 }
 
 MOE_STATIC_SCRATCH_BYTES = 64 << 20
@@ -337,3 +381,52 @@ def moe_backward(ctx, saved, dout, W13, W2, dx, dW13, dW2, d_scores=None, call_f
     _check("moe_backward", LIB.moe_backward(ctx, _ptr(saved), _ptr(dout), ctypes.byref(W13), ctypes.byref(W2),
                                             _ptr(dx), _ptr(dW13), _ptr(dW2), _ptr(d_scores), call_flags,
                                             _stream(stream)))
+
+
+def moe_block_norm_forward(cfg, x, branch, gate, post_weight, pre_weight, y, h, stats=None, stream=None):
+    _check("moe_block_norm_forward",
+           LIB.moe_block_norm_forward(ctypes.byref(cfg), _ptr(x), _ptr(branch), _ptr(gate), _ptr(post_weight),
+                                      _ptr(pre_weight), _ptr(y), _ptr(h), _ptr(stats), _stream(stream)))
+
+
+def moe_block_norm_workspace_bytes(cfg):
+    return LIB.moe_block_norm_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_block_norm_backward(cfg, x, branch, gate, post_weight, pre_weight, stats, dy, dh, dx, dbranch, dgate,
+                            dpost_weight, dpre_weight, workspace, workspace_bytes, stream=None):
+    _check("moe_block_norm_backward",
+           LIB.moe_block_norm_backward(ctypes.byref(cfg), _ptr(x), _ptr(branch), _ptr(gate), _ptr(post_weight),
+                                       _ptr(pre_weight), _ptr(stats), _ptr(dy), _ptr(dh), _ptr(dx), _ptr(dbranch),
+                                       _ptr(dgate), _ptr(dpost_weight), _ptr(dpre_weight), _ptr(workspace),
+                                       workspace_bytes, _stream(stream)))
+
+
+def moe_topk_gate_forward(cfg, logits, select_bias, ids, scores, stream=None):
+    _check("moe_topk_gate_forward",
+           LIB.moe_topk_gate_forward(ctypes.byref(cfg), _ptr(logits), _ptr(select_bias), _ptr(ids), _ptr(scores),
+                                     _stream(stream)))
+
+
+def moe_topk_gate_backward(cfg, logits, ids, d_scores, d_logits, stream=None):
+    _check("moe_topk_gate_backward",
+           LIB.moe_topk_gate_backward(ctypes.byref(cfg), _ptr(logits), _ptr(ids), _ptr(d_scores), _ptr(d_logits),
+                                      _stream(stream)))
+
+
+def moe_muon_workspace_bytes(cfg, matrices):
+    return LIB.moe_muon_workspace_bytes(ctypes.byref(cfg), matrices)
+
+
+def moe_orthogonalize(cfg, x, x_type, out, workspace, workspace_bytes, device_error_word, stream=None):
+    _check("moe_orthogonalize",
+           LIB.moe_orthogonalize(ctypes.byref(cfg), _ptr(x), x_type, _ptr(out), _ptr(workspace), workspace_bytes,
+                                 _ptr(device_error_word), _stream(stream)))
+
+
+def moe_muon_update(cfg, rates, weight, weight_type, grad, grad_type, momentum, weight_bf16, workspace,
+                    workspace_bytes, device_error_word, stream=None):
+    _check("moe_muon_update",
+           LIB.moe_muon_update(ctypes.byref(cfg), ctypes.byref(rates), _ptr(weight), weight_type, _ptr(grad), grad_type,
+                               _ptr(momentum), _ptr(weight_bf16), _ptr(workspace), workspace_bytes,
+                               _ptr(device_error_word), _stream(stream)))

@@ -1,0 +1,312 @@
+// The router's choice: top_k experts a token from its logits, their scores,
+// and the gradient of the logits (moe_topk_gate_forward / _backward).
+//
+// key_e = logit_e + bias_e (one FP32 rounding; the bias steers the choice
+// only).  The K largest keys are taken, equal keys by ascending expert, keys
+// of -inf never; places without an expert get id -1 and score 0, the layer's
+// inactive route.  With scale c, over l = the logits:
+//   softmax                s_k = c exp(l_k) / sum over all experts
+//   softmax, renormalised  s_k = c exp(l_k) / sum over the chosen
+//   sigmoid                s_k = c sig(l_k)
+//   sigmoid, renormalised  s_k = c sig(l_k) / (sum over the chosen + 1e-20)
+// Gradients, with d_k = c ds_k and v_k the unscaled scores:
+//   softmax                dl_e = [e chosen] v_e d_e - p_e sum_k v_k d_k
+//   softmax, renormalised  dl_k = v_k (d_k - sum_j v_j d_j), 0 elsewhere
+//   sigmoid                dl_k = d_k sig(l_k) sig(-l_k), 0 elsewhere;
+//   renormalised           d_k -> (d_k - sum_j v_j d_j) / (sum + 1e-20) first
+// A row with a NaN or +inf logit has no choice: ids -1, scores NaN (and a
+// NaN gradient), so the fault shows instead of routing somewhere.
+//
+// One warp a token; lane i holds the logits of experts i, i + 32, ...  A
+// round of the choice is one maximum over the lanes' best keys, taken on
+// their order-preserving 32-bit images (redux.sync), and one minimum over
+// the expert numbers that reach it.
+#include "kernels.cuh"
+#include "moe_gb300.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kGateThreads = 256;
+constexpr float kSigmoidEps = 1e-20f;
+
+struct GateParams {
+  int T, E, K;
+  const void* logits;   // [T, ld]
+  long long ld;
+  const float* bias;    // [E] or NULL
+  int sigmoid, renorm;
+  float scale;
+  int* ids;             // [T, K]
+  float* scores;        // [T, K] (backward: gradient of the scores)
+  void* dlogits;        // [T, E]
+};
+
+// Unsigned image of a float with the same order (-0 like +0 beforehand).
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+constexpr uint32_t kOrderNegInf = 0x007FFFFFu;   // order_of(-inf)
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// L = experts per lane (ceil(E / 32) rounded up to the instance).
+template <typename X, int L>
+__global__ void __launch_bounds__(kGateThreads) topk_gate_fwd_kernel(const GateParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long t = static_cast<long long>(blockIdx.x) * (kGateThreads / 32) + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const X* row = static_cast<const X*>(p.logits) + t * p.ld;
+  float l[L];
+  uint32_t key[L];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = -INFINITY;
+    if (e < p.E) l[i] = to_f(row[e]);
+  }
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int e = lane + 32 * i;
+    bad |= !(l[i] < INFINITY);
+    const float b = (p.bias && e < p.E) ? l[i] + p.bias[e] : l[i];
+    key[i] = e < p.E ? order_of(b) : 0u;
+    bad |= !(b < INFINITY);
+  }
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  // the K choices: lane k keeps the k-th
+  int my_id = -1;
+  float my_l = 0.0f;
+  uint32_t best = 0;
+  int at = 0;
+  auto rescan = [&] {
+    best = key[0];
+    at = 0;
+#pragma unroll
+    for (int i = 1; i < L; ++i)
+      if (key[i] > best) best = key[i], at = i;
+  };
+  rescan();
+  if (!bad) {
+    for (int k = 0; k < p.K; ++k) {
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+      if (top <= kOrderNegInf) break;
+      const int e = lane + 32 * at;
+      const int who = __reduce_min_sync(0xFFFFFFFFu, best == top ? e : 0x7FFFFFFF);
+      float v = 0.0f;
+      if (who == e && best == top) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          if (i == at) v = l[i], key[i] = 0u;
+        rescan();
+      }
+      v = __shfl_sync(0xFFFFFFFFu, v, who & 31);
+      if (lane == k) my_id = who, my_l = v;
+    }
+  }
+  const bool on = my_id >= 0;
+  float s = 0.0f;
+  if (p.sigmoid) {
+    s = on ? 1.0f / (1.0f + expf(-my_l)) : 0.0f;
+    if (p.renorm) s = s / (warp_sum(s) + kSigmoidEps);
+  } else if (p.renorm) {
+    const float m = warp_max(on ? my_l : -INFINITY);
+    s = on ? expf(my_l - m) : 0.0f;
+    const float sum = warp_sum(s);
+    if (on) s = s / sum;
+  } else {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < L; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < L; ++i) sum += expf(l[i] - m);
+    sum = warp_sum(sum);
+    if (on) s = expf(my_l - m) / sum;
+  }
+  if (lane < p.K) {
+    const long long o = t * p.K + lane;
+    p.ids[o] = my_id;
+    p.scores[o] = bad ? NAN : (on ? s * p.scale : 0.0f);
+  }
+}
+
+template <typename X, int L>
+__global__ void __launch_bounds__(kGateThreads) topk_gate_bwd_kernel(const GateParams p) {
+  const int lane = threadIdx.x & 31;
+  const bool dense = !p.sigmoid && !p.renorm;
+  const long long t = static_cast<long long>(blockIdx.x) * (kGateThreads / 32) + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const X* row = static_cast<const X*>(p.logits) + t * p.ld;
+  X* out = static_cast<X*>(p.dlogits) + t * p.E;
+  int id = -1;
+  float d = 0.0f;
+  if (lane < p.K) {
+    const long long o = t * p.K + lane;
+    id = p.ids[o];
+    if (id < 0 || id >= p.E) id = -1;   // a bad id is an inactive route
+    if (id >= 0) d = p.scale * p.scores[o];
+  }
+  const bool on = id >= 0;
+  float l[L];
+  bool bad = false;
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = -INFINITY;
+    if (e < p.E) l[i] = to_f(row[e]);
+    bad |= !(l[i] < INFINITY);
+  }
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  const float lk = on ? to_f(row[id]) : -INFINITY;
+  float dl = 0.0f;
+  if (p.sigmoid) {
+    const float v = on ? 1.0f / (1.0f + expf(-lk)) : 0.0f;
+    const float slope = on ? v / (1.0f + expf(lk)) : 0.0f;
+    if (p.renorm) {
+      const float sum = warp_sum(v) + kSigmoidEps;
+      const float dot = warp_sum(d * (v / sum));
+      dl = on ? (d - dot) / sum * slope : 0.0f;
+    } else {
+      dl = d * slope;
+    }
+  } else if (p.renorm) {
+    const float top = warp_max(lk);
+    const float v = on ? expf(lk - top) : 0.0f;
+    const float sum = warp_sum(v);
+    const float sv = on ? v / sum : 0.0f;
+    const float dot = warp_sum(d * sv);
+    dl = sv * d - sv * dot;
+  } else {
+#pragma unroll
+    for (int i = 0; i < L; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+    float sum = 0.0f;
+    if (m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        l[i] = expf(l[i] - m);
+        sum += l[i];
+      }
+    }
+    sum = warp_sum(sum);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float pk = on ? expf(lk - m) * inv : 0.0f;
+    const float dot = warp_sum(pk * d);
+    dl = pk * d;
+#pragma unroll
+    for (int i = 0; i < L; ++i) l[i] = m > -INFINITY ? -(l[i] * inv) * dot : 0.0f;
+  }
+  if (!dense) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) l[i] = 0.0f;
+  }
+  // add the chosen experts' own terms to the lanes that hold them
+  for (int k = 0; k < p.K; ++k) {
+    const int e = __shfl_sync(0xFFFFFFFFu, id, k);
+    const float v = __shfl_sync(0xFFFFFFFFu, dl, k);
+    if (e >= 0 && (e & 31) == lane) {
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        if (i == (e >> 5)) l[i] += v;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int e = lane + 32 * i;
+    if (e < p.E) put(out + e, bad ? NAN : l[i]);
+  }
+}
+
+template <typename X, int L>
+void launch_gate(bool fwd, const GateParams& p, cudaStream_t stream) {
+  const int per = kGateThreads / 32;
+  const int ctas = (p.T + per - 1) / per;
+  if (fwd) topk_gate_fwd_kernel<X, L><<<ctas, kGateThreads, 0, stream>>>(p);
+  else topk_gate_bwd_kernel<X, L><<<ctas, kGateThreads, 0, stream>>>(p);
+}
+
+template <typename X>
+void launch_gate_l(bool fwd, const GateParams& p, cudaStream_t stream) {
+  const int l = (p.E + 31) / 32;
+  if (l <= 1) launch_gate<X, 1>(fwd, p, stream);
+  else if (l <= 2) launch_gate<X, 2>(fwd, p, stream);
+  else if (l <= 4) launch_gate<X, 4>(fwd, p, stream);
+  else if (l <= 8) launch_gate<X, 8>(fwd, p, stream);
+  else if (l <= 12) launch_gate<X, 12>(fwd, p, stream);
+  else if (l <= 16) launch_gate<X, 16>(fwd, p, stream);
+  else launch_gate<X, 32>(fwd, p, stream);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+moe_status gate_call(bool fwd, const moe_topk_gate_config* c, const void* logits, const float* bias, int32_t* ids,
+                     float* scores, void* dlogits, cudaStream_t stream) {
+  if (!c || c->tokens < 0 || c->num_experts < 1 || c->num_experts > 1024) return MOE_ERR_INVALID_ARG;
+  if (c->top_k < 1 || c->top_k > 32 || c->top_k > c->num_experts) return MOE_ERR_INVALID_ARG;
+  if (c->logits_type != MOE_TYPE_BF16 && c->logits_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+  if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (c->logits_stride != 0 && c->logits_stride < c->num_experts) return MOE_ERR_INVALID_ARG;
+  if (!(c->scale >= -3.0e38f && c->scale <= 3.0e38f)) return MOE_ERR_INVALID_ARG;
+  if (c->tokens == 0) return MOE_OK;
+  if (!logits || !ids || !scores || (!fwd && !dlogits)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(scores) || !aligned16(dlogits))
+    return MOE_ERR_INVALID_ARG;
+  GateParams p{};
+  p.T = c->tokens;
+  p.E = c->num_experts;
+  p.K = c->top_k;
+  p.logits = logits;
+  p.ld = c->logits_stride ? c->logits_stride : c->num_experts;
+  p.bias = bias;
+  p.sigmoid = c->score == MOE_SCORE_SIGMOID;
+  p.renorm = c->renormalize != 0;
+  p.scale = c->scale;
+  p.ids = ids;
+  p.scores = scores;
+  p.dlogits = dlogits;
+  if (c->logits_type == MOE_TYPE_FP32) launch_gate_l<float>(fwd, p, stream);
+  else launch_gate_l<__nv_bfloat16>(fwd, p, stream);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_topk_gate_forward(const moe_topk_gate_config* cfg, const void* logits, const float* select_bias,
+                                 int32_t* ids, float* scores, cudaStream_t stream) {
+  return gate_call(true, cfg, logits, select_bias, ids, scores, nullptr, stream);
+}
+
+moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const void* logits, const int32_t* ids,
+                                  const float* d_scores, void* d_logits, cudaStream_t stream) {
+  return gate_call(false, cfg, logits, nullptr, const_cast<int32_t*>(ids), const_cast<float*>(d_scores), d_logits,
+                   stream);
+}
+
+}  // extern "C"
