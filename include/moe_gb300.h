@@ -616,12 +616,12 @@ typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_FP32 = 1 } moe_type;
  *                 pre_weight), which the backward reads
  * Strides are elements between rows (0: D); other tensors are contiguous.
  * Pointers are 16-byte aligned; rows are read in 16-byte pieces if D and the
- * strides are multiples of 8, else element by element.  D <= 16384.
+ * strides are multiples of 8, else element by element.  D <= 8192.
  * A row of zeros gives zeros (r = 1/sqrt(eps)).  T may be 0.
  * Errors: MOE_ERR_INVALID_ARG (null cfg, T < 0, D < 1, unknown types or
  * modes, eps not finite and positive, scales not finite, a stride in (0, D),
  * parts that do not belong together, null or misaligned pointers),
- * MOE_ERR_UNSUPPORTED (D > 16384).
+ * MOE_ERR_UNSUPPORTED (D > 8192).
  *
  * moe_block_norm_backward: from dy (residual_type, y_stride; NULL = 0) and
  * dh (bf16, h_stride; with pre_weight), the gradients of y and h, and the

@@ -21,17 +21,28 @@ _TYPE = {torch.bfloat16: abi.MOE_TYPE_BF16, torch.float32: abi.MOE_TYPE_FP32}
 _SCORE = {"softmax": abi.MOE_SCORE_SOFTMAX, "sigmoid": abi.MOE_SCORE_SIGMOID}
 
 
+# the raw handle of a device's current stream (torch.cuda.current_stream builds a Stream object each time)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def on_stream(fn, device, stream):
-    """fn() with `device` current and `stream` (None: the current one) as its stream."""
+    """fn(raw stream) with `device` current, on `stream` (None: the current one), which is then current too."""
     if stream is None and device.index == torch.cuda.current_device():
-        return fn()
+        return fn(_raw_stream(device.index))
     with torch.cuda.device(device):
         if stream is None:
-            return fn()
+            return fn(_raw_stream(device.index))
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         with torch.cuda.stream(stream):
-            return fn()
+            return fn(stream.cuda_stream)
+
+
+def _new(x, dtype=None):
+    """An uninitialised contiguous tensor of x's shape, of its type or another."""
+    if dtype is None or dtype == x.dtype:
+        return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return torch.empty(x.shape, dtype=dtype, device=x.device)
 
 
 def _need(ok, message):
@@ -39,55 +50,66 @@ def _need(ok, message):
         raise ValueError(message)
 
 
+def _wrong(name, t, dtype, shape, device, contiguous=""):
+    raise ValueError(f"{name}: expected {contiguous}{dtype} {list(shape)} on {device}, "
+                     f"got {t.dtype} {list(t.shape)} (strides {list(t.stride())}) on {t.device}")
+
+
 def _rows(name, t, dtype, shape, device):
     """A [T, D] tensor whose rows are contiguous; its row stride."""
-    _need(t.dtype == dtype and tuple(t.shape) == shape and t.device == device,
-          f"{name}: expected {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        _wrong(name, t, dtype, shape, device)
     T, D = shape
-    if T <= 1:
-        _need(D <= 1 or T == 0 or t.stride(1) == 1, f"{name}: its columns are not contiguous")
-        return D
-    _need(D == 1 or t.stride(1) == 1, f"{name}: its columns are not contiguous")
-    _need(t.stride(0) >= D, f"{name}: its rows overlap (stride {t.stride(0)} for {D} columns)")
-    return t.stride(0)
+    row, col = t.stride()
+    if (col != 1 and D > 1 and T > 0) or (row < D and T > 1):
+        raise ValueError(f"{name}: rows have to be contiguous and apart (strides {row}, {col} for {D} columns)")
+    return row if T > 1 else D
 
 
 def _dense(name, t, dtype, shape, device):
-    _need(t.dtype == dtype and tuple(t.shape) == shape and t.device == device and t.is_contiguous(),
-          f"{name}: expected contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _wrong(name, t, dtype, shape, device, "contiguous ")
 
 
-class _Norm:
-    """The checked arguments shared by block_norm and its backward."""
+def _gate_shape(cfg, gate, T, D, device):
+    shape = gate.shape
+    if gate.dtype not in _TYPE or gate.device != device or not gate.is_contiguous() or len(shape) not in (1, 2):
+        raise ValueError(f"gate: expected contiguous bfloat16 or float32 on {device}, got {gate.dtype} {list(shape)} on "
+                         f"{gate.device}")
+    cfg.gate_type = _TYPE[gate.dtype]
+    if len(shape) == 1 and shape[0] == D:
+        cfg.gate_mode = abi.MOE_GATE_CHANNEL
+    elif len(shape) == 2 and shape[1] == D and shape[0] > 0 and T % shape[0] == 0:
+        cfg.gate_mode, cfg.gate_rows = abi.MOE_GATE_GROUP, shape[0]
+    elif len(shape) == 2 and shape[0] == T and shape[1] == 1:
+        cfg.gate_mode = abi.MOE_GATE_TOKEN
+    else:
+        raise ValueError(f"gate {list(shape)}: expected [{D}], [G, {D}] with G dividing {T}, or [{T}, 1]")
 
-    def __init__(self, x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, eps, weight_offset):
-        _need(x.dim() == 2 and x.is_cuda and x.dtype in _TYPE, "x: expected a CUDA bfloat16 or float32 [T, D] tensor")
-        T, D = self.shape = tuple(x.shape)
-        dev = self.device = x.device
-        cfg = self.cfg = abi.moe_block_norm_config(T, D, _TYPE[x.dtype], 0, 0, abi.MOE_GATE_NONE, 0, residual_scale,
-                                                   branch_scale, eps, weight_offset, 0, 0, 0, 0)
-        cfg.x_stride = _rows("x", x, x.dtype, self.shape, dev)
-        if branch is not None:
-            cfg.branch_stride = _rows("branch", branch, torch.bfloat16, self.shape, dev)
-        else:
-            _need(gate is None and post_weight is None, "a gate or post_weight needs a branch")
-        weights = [w for w in (post_weight, pre_weight) if w is not None]
-        for w in weights:
-            _need(w.dtype in _TYPE, "weights are bfloat16 or float32")
-            _dense("weight", w, weights[0].dtype, (D,), dev)
-            cfg.weight_type = _TYPE[w.dtype]
-        if gate is not None:
-            _need(gate.dtype in _TYPE and gate.device == dev and gate.is_contiguous() and gate.dim() in (1, 2),
-                  f"gate: expected contiguous bfloat16 or float32 [D], [G, D] or [T, 1] on {dev}")
-            cfg.gate_type = _TYPE[gate.dtype]
-            if gate.dim() == 1 and gate.shape[0] == D:
-                cfg.gate_mode = abi.MOE_GATE_CHANNEL
-            elif gate.dim() == 2 and gate.shape[1] == D and gate.shape[0] > 0 and T % gate.shape[0] == 0:
-                cfg.gate_mode, cfg.gate_rows = abi.MOE_GATE_GROUP, gate.shape[0]
-            elif gate.dim() == 2 and tuple(gate.shape) == (T, 1):
-                cfg.gate_mode = abi.MOE_GATE_TOKEN
-            else:
-                raise ValueError(f"gate {list(gate.shape)}: expected [{D}], [G, {D}] with G dividing {T}, or [{T}, 1]")
+
+def _norm_config(x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, eps, weight_offset):
+    """The checked configuration shared by block_norm and its backward."""
+    xt, shape, dev = x.dtype, x.shape, x.device
+    if len(shape) != 2 or xt not in _TYPE or not x.is_cuda:
+        raise ValueError("x: expected a CUDA bfloat16 or float32 [T, D] tensor")
+    T, D = shape
+    cfg = abi.moe_block_norm_config(T, D, _TYPE[xt], 0, 0, abi.MOE_GATE_NONE, 0, residual_scale, branch_scale, eps,
+                                    weight_offset, _rows("x", x, xt, shape, dev), 0, 0, 0)
+    if branch is not None:
+        cfg.branch_stride = _rows("branch", branch, torch.bfloat16, shape, dev)
+    elif gate is not None or post_weight is not None:
+        raise ValueError("a gate or post_weight needs a branch")
+    kind = None
+    for w in (post_weight, pre_weight):
+        if w is not None:
+            kind = kind or w.dtype
+            if kind not in _TYPE:
+                raise ValueError("weights are bfloat16 or float32")
+            _dense("weight", w, kind, (D,), dev)
+            cfg.weight_type = _TYPE[kind]
+    if gate is not None:
+        _gate_shape(cfg, gate, T, D, dev)
+    return cfg
 
 
 def block_norm(x, branch=None, *, gate=None, post_weight=None, pre_weight=None, residual_scale=1.0, branch_scale=1.0,
@@ -104,23 +126,23 @@ def block_norm(x, branch=None, *, gate=None, post_weight=None, pre_weight=None, 
     channel), [G, D] (row t takes gate row t // (T / G)) or [T, 1] (a token).
     ``y`` may be x and ``h`` may be branch (in place).  ``stats``: a float32
     [2, T] tensor for the backward to read."""
-    n = _Norm(x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, eps, weight_offset)
-    cfg, dev = n.cfg, n.device
+    cfg = _norm_config(x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, eps, weight_offset)
+    shape, dev = x.shape, x.device
     if y is not None:
-        cfg.y_stride = _rows("y", y, x.dtype, n.shape, dev)
+        cfg.y_stride = _rows("y", y, x.dtype, shape, dev)
     if h is not None:
         _need(pre_weight is not None, "h needs a pre_weight")
-        cfg.h_stride = _rows("h", h, torch.bfloat16, n.shape, dev)
+        cfg.h_stride = _rows("h", h, torch.bfloat16, shape, dev)
     if stats is not None:
-        _dense("stats", stats, torch.float32, (2, n.shape[0]), dev)
+        _dense("stats", stats, torch.float32, (2, shape[0]), dev)
     _need(branch is not None or pre_weight is not None or y is not None or residual_scale != 1.0,
           "nothing to compute: no branch, no pre_weight")
     same = branch is None and y is None and residual_scale == 1.0
 
-    def run():
-        yy = y if y is not None or same else torch.empty(n.shape, dtype=x.dtype, device=dev)
-        hh = h if h is not None or pre_weight is None else torch.empty(n.shape, dtype=torch.bfloat16, device=dev)
-        abi.moe_block_norm_forward(cfg, x, branch, gate, post_weight, pre_weight, yy, hh, stats)
+    def run(s):
+        yy = y if y is not None or same else _new(x)
+        hh = h if h is not None or pre_weight is None else _new(x, torch.bfloat16)
+        abi.moe_block_norm_forward(cfg, x, branch, gate, post_weight, pre_weight, yy, hh, stats, s)
         return (x if same else yy), hh
 
     return on_stream(run, dev, stream)
@@ -140,42 +162,40 @@ def block_norm_backward(x, branch, stats, dy, dh=None, *, gate=None, post_weight
     type; None: zero) and ``dh`` (bfloat16; given with pre_weight), with the
     forward's inputs and ``stats``.  dx has x's type, dbranch is bfloat16,
     dgate has the gate's shape and type, the weights' gradients are float32."""
-    n = _Norm(x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, 1.0, weight_offset)
-    cfg, dev = n.cfg, n.device
-    T, D = n.shape
+    cfg = _norm_config(x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, 1.0, weight_offset)
+    shape, dev = x.shape, x.device
+    T, D = shape
     _need((dh is not None) == (pre_weight is not None), "dh goes with pre_weight")
     _need(dy is not None or dh is not None, "no gradient given")
     if dy is not None:
-        cfg.y_stride = _rows("dy", dy, x.dtype, n.shape, dev)
+        cfg.y_stride = _rows("dy", dy, x.dtype, shape, dev)
     if dh is not None:
-        cfg.h_stride = _rows("dh", dh, torch.bfloat16, n.shape, dev)
+        cfg.h_stride = _rows("dh", dh, torch.bfloat16, shape, dev)
     if post_weight is not None or pre_weight is not None:
         _need(stats is not None, "the norms' backward needs the forward's stats")
         _dense("stats", stats, torch.float32, (2, T), dev)
 
-    def run():
-        dx = torch.empty(n.shape, dtype=x.dtype, device=dev)
-        dbranch = None if branch is None else torch.empty(n.shape, dtype=torch.bfloat16, device=dev)
+    def run(s):
+        dx = _new(x)
+        dbranch = None if branch is None else _new(branch)
         dgate = None if gate is None else torch.empty_like(gate)
         dpost = None if post_weight is None else torch.empty(D, dtype=torch.float32, device=dev)
         dpre = None if pre_weight is None else torch.empty(D, dtype=torch.float32, device=dev)
         nb = abi.moe_block_norm_workspace_bytes(cfg)
         ws = torch.empty(nb, dtype=torch.uint8, device=dev)
         abi.moe_block_norm_backward(cfg, x, branch, gate, post_weight, pre_weight, stats, dy, dh, dx, dbranch, dgate,
-                                    dpost, dpre, ws, nb)
+                                    dpost, dpre, ws, nb, s)
         return BlockNormGrads(dx, dbranch, dgate, dpost, dpre)
 
     return on_stream(run, dev, stream)
 
 
 def _gate_config(logits, top_k, score, renormalize, scale):
-    _need(logits.dim() == 2 and logits.is_cuda and logits.dtype in _TYPE,
-          "logits: expected a CUDA bfloat16 or float32 [T, E] tensor")
-    _need(score in _SCORE, f"score: one of {sorted(_SCORE)}")
-    T, E = logits.shape
-    cfg = abi.moe_topk_gate_config(T, E, top_k, _TYPE[logits.dtype], _SCORE[score], 1 if renormalize else 0, scale, 0)
-    cfg.logits_stride = _rows("logits", logits, logits.dtype, (T, E), logits.device)
-    return cfg
+    kind, shape = logits.dtype, logits.shape
+    _need(len(shape) == 2 and kind in _TYPE and logits.is_cuda, "logits: expected a CUDA bfloat16 or float32 [T, E] tensor")
+    _need(score in _SCORE, "score: softmax or sigmoid")
+    return abi.moe_topk_gate_config(shape[0], shape[1], top_k, _TYPE[kind], _SCORE[score], 1 if renormalize else 0, scale,
+                                    _rows("logits", logits, kind, shape, logits.device))
 
 
 def topk_gate(logits, top_k, *, score="softmax", renormalize=False, scale=1.0, select_bias=None, ids=None, scores=None,
@@ -195,10 +215,10 @@ def topk_gate(logits, top_k, *, score="softmax", renormalize=False, scale=1.0, s
     if scores is not None:
         _dense("scores", scores, torch.float32, shape, dev)
 
-    def run():
+    def run(stream):
         i = torch.empty(shape, dtype=torch.int32, device=dev) if ids is None else ids
         s = torch.empty(shape, dtype=torch.float32, device=dev) if scores is None else scores
-        abi.moe_topk_gate_forward(cfg, logits, select_bias, i, s)
+        abi.moe_topk_gate_forward(cfg, logits, select_bias, i, s, stream)
         return i, s
 
     return on_stream(run, dev, stream)
@@ -214,11 +234,11 @@ def topk_gate_backward(logits, ids, d_scores, *, score="softmax", renormalize=Fa
     _dense("ids", ids, torch.int32, shape, dev)
     _dense("d_scores", d_scores, torch.float32, shape, dev)
     if d_logits is not None:
-        _dense("d_logits", d_logits, logits.dtype, tuple(logits.shape), dev)
+        _dense("d_logits", d_logits, logits.dtype, logits.shape, dev)
 
-    def run():
-        d = torch.empty(logits.shape, dtype=logits.dtype, device=dev) if d_logits is None else d_logits
-        abi.moe_topk_gate_backward(cfg, logits, ids, d_scores, d)
+    def run(stream):
+        d = _new(logits) if d_logits is None else d_logits
+        abi.moe_topk_gate_backward(cfg, logits, ids, d_scores, d, stream)
         return d
 
     return on_stream(run, dev, stream)

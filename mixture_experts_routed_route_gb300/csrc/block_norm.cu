@@ -13,10 +13,25 @@
 //   dx = alpha s,   dg = beta s n w_o,   b = beta g s w_o
 //   do = r_o (b - n mean(b n)),  dw_o = sum_t beta g s n,  dw_h = sum_t dh z
 //
-// Work layout: a group of W warps owns a row (W = ceil(D / 512), 16 columns
-// a thread), so a row stays in registers between its loads and its stores;
-// groups of rows narrower than a CTA share one.  A group's row sums go
-// through shared memory under a named barrier of its own.
+// Work layout: persistent CTAs, one per SM.  A group of W warps owns a row
+// (W = ceil(D / 1024) with 32 columns a thread in four pieces of 8, or twice
+// as many with half of that); as many
+// groups share a CTA as its registers and shared memory hold.  Rows come in
+// through shared memory, cp.async, and are read from there once per pass
+// over them (the row's sums separate the passes), so registers hold only
+// what a later pass needs: the FP32 y in the forward; in the backward the
+// running column sums and one value a column.  Several small groups rather
+// than one of the whole CTA: while one waits for its row or at its named
+// barrier the others issue, and 32 columns a thread carry the fixed cost of
+// a row (two sums over the warps, the copies, the bookkeeping).
+//   V = 8: rows whose length and strides are multiples of 8 elements; a
+//          thread copies just the 16-byte pieces it will read itself, so the
+//          copies need no barrier.
+//   V = 1: any other row; the group copies the aligned 16-byte pieces that
+//          cover it and reads its elements at the row's own offset, between
+//          two more barriers.
+#include <algorithm>
+
 #include "kernels.cuh"
 #include "moe_gb300.h"
 
@@ -24,19 +39,36 @@ namespace moe {
 
 namespace {
 
-constexpr int kCols = 16;             // columns per thread
-constexpr int kWarpCols = 32 * kCols; // columns per warp
-constexpr int kMaxCols = 32 * kWarpCols;
+constexpr int kMaxCols = 8192;           // the table and one row of every stream fit beside each other
+constexpr int kSharedMem = 216 * 1024;   // the columns' factors and the rows in flight
+constexpr int kWarps = 16;            // of a CTA at most: 128 registers a thread
+
+// A tensor whose rows the kernel streams.
+struct Stream {
+  const uint8_t* base;        // NULL: not there
+  long long ld;               // bytes between rows
+  const uint8_t* end;         // past the last row's last element
+  int esz, row_bytes;
+  int off;                    // place in a row's slot
+  int piece;                  // bytes between a thread's 8-column pieces (V = 8)
+};
+enum { kX, kDy, kDh, kG, kO, kStreams };   // kG: a gate of every element; kO: what the backward reads last
+
+// gate_mode inside: a grouped gate whose groups are single rows is a gate of
+// every element, which is streamed like x and has no sums over rows.
+constexpr int kGateFull = MOE_GATE_TOKEN + 1;
 
 struct NormParams {
   int T, D;
   int warps, groups;          // warps per row, rows in flight per CTA
-  const void* x;              // [T, ldx] residual type
-  const __nv_bfloat16* o;     // [T, ldo] or NULL
+  int stages, slot;           // rows in flight per group, bytes of one
+  int table;                  // bytes of the columns' factors
+  int res_f32;                // residual type
+  Stream in[kStreams];
   const void* gate;
   const void* w_post;         // NULL: no norm after the block
   const void* w_pre;          // NULL: no norm before the next
-  long long ldx, ldo, ldy, ldh;
+  long long ldy, ldh;
   int gate_mode, rows_per_group;
   int params_f32, gate_f32;
   float alpha, beta, eps, offset;
@@ -45,348 +77,750 @@ struct NormParams {
   __nv_bfloat16* h;
   float* stats;               // [2][T]: r_o, r_y (backward: read)
   // backward
-  const void* dy;             // or NULL
-  const __nv_bfloat16* dh;    // or NULL
   void* dx;                   // or NULL
   __nv_bfloat16* do_;
   void* dgate;
-  long long lddy, lddh, lddx, lddo;
-  float* partial;             // [3][gridDim.x][D]: dw_post, dw_pre, dgate (channel)
+  float* partial;             // [3][gridDim.x][D]: sum s n (times g: grouped, token gates), dw_pre
   float* gate_partial;        // [slabs][D] (grouped gates cut into several slabs a group)
   int slabs_per_group, slabs;
 };
 
-// V consecutive values at p as FP32 (V = 8: one or two 16-byte loads).
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Two FP32 operations an instruction (packed f32x2): the passes below are
+// bound by instruction issue as soon as the rows stream at full rate.
+__device__ __forceinline__ unsigned long long pair_of(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(unsigned long long v) {
+  float a, b;
+  split(v, a, b);
+  return a + b;
+}
+
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair both(float x) { return pair_of(x, x); }
+
+// V of the kernels: 8 (vector rows), 1 (any row), or kFull: vector rows whose
+// D is a multiple of 1024, so that no column needs a test.
+constexpr int kFull = 16;
+
+// Pieces of 8 columns a thread holds: two in the backward, whose column sums
+// stay in registers too (four: 70 us instead of 51 at 2048 x 7168, with
+// half the warps and spills), and where every column has its own address and
+// test (V = 1).
+template <int V, bool BWD>
+constexpr int kPiecesOf = (V == 1 || BWD) ? 2 : 4;
+
+// A thread's 32 columns of its group's row in pieces i of 8: neighbours
+// (vector rows) or nt apart (V = 1).
 template <int V>
-__device__ __forceinline__ void load_v(const __nv_bfloat16* p, float* v) {
-  if constexpr (V == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-    v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
-  } else {
-    v[0] = __bfloat162float(*p);
-  }
-}
+struct Columns {
+  int t, nt, D;
+  __device__ __forceinline__ int col(int i, int j) const { return V >= 8 ? (t + i * nt) * 8 + j : t + (8 * i + j) * nt; }
+  __device__ __forceinline__ bool any(int i) const { return V == kFull || col(i, 0) < D; }
 
-template <int V>
-__device__ __forceinline__ void load_v(const float* p, float* v) {
-  if constexpr (V == 8) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    v[0] = *p;
-  }
-}
-
-template <int V>
-__device__ __forceinline__ void store_v(__nv_bfloat16* p, const float* v) {
-  if constexpr (V == 8)
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                              pack_bf16x2(v[6], v[7]));
-  else
-    *p = __float2bfloat16_rn(v[0]);
-}
-
-template <int V>
-__device__ __forceinline__ void store_v(float* p, const float* v) {
-  if constexpr (V == 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *p = v[0];
-  }
-}
-
-// Weights and gates come in either type (a uniform branch).
-template <int V>
-__device__ __forceinline__ void load_param(const void* p, int f32, long long at, float* v) {
-  if (f32) load_v<V>(static_cast<const float*>(p) + at, v);
-  else load_v<V>(static_cast<const __nv_bfloat16*>(p) + at, v);
-}
-
-template <int V>
-__device__ __forceinline__ void store_param(void* p, int f32, long long at, const float* v) {
-  if (f32) store_v<V>(static_cast<float*>(p) + at, v);
-  else store_v<V>(static_cast<__nv_bfloat16*>(p) + at, v);
-}
-
-// Sum over a group's `warps` warps in a fixed order: an xor tree in each
-// warp, then the warp sums in warp order.  `red` is the group's 2 x 32
-// floats, used in turns (`turn` flips), so one barrier a sum is enough.
-__device__ __forceinline__ float group_sum(float v, float* red, int warps, int wig, int bar, int& turn) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (warps == 1) return v;
-  float* r = red + turn * 32;
-  turn ^= 1;
-  if ((threadIdx.x & 31) == 0) r[wig] = v;
-  named_bar_sync(bar, warps * 32);
-  float t = 0.0f;
-  for (int w = 0; w < warps; ++w) t += r[w];
-  return t;
-}
-
-__device__ __forceinline__ long long gate_row(const NormParams& p, long long row) {
-  return static_cast<long long>(p.gate_mode == MOE_GATE_GROUP ? row / p.rows_per_group : 0) * p.D;
-}
-
-// g w_o for V columns from c (1 where there is no gate or no norm).
-template <int V>
-__device__ __forceinline__ void gate_v(const NormParams& p, long long row, int c, float* g) {
-  if (p.gate_mode == MOE_GATE_CHANNEL || p.gate_mode == MOE_GATE_GROUP) {
-    load_param<V>(p.gate, p.gate_f32, gate_row(p, row) + c, g);
-  } else {
-    float t = 1.0f;
-    if (p.gate_mode == MOE_GATE_TOKEN) load_param<1>(p.gate, p.gate_f32, row, &t);
-#pragma unroll
-    for (int j = 0; j < V; ++j) g[j] = t;
-  }
-}
-
-template <int V>
-__device__ __forceinline__ void weight_v(const NormParams& p, const void* w, int c, float* v) {
-  if (w == nullptr) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = 1.0f;
-    return;
-  }
-  load_param<V>(w, p.params_f32, c, v);
-#pragma unroll
-  for (int j = 0; j < V; ++j) v[j] += p.offset;
-}
-
-template <typename R, int V, int THREADS>
-__global__ void __launch_bounds__(THREADS) block_norm_fwd_kernel(const NormParams p) {
-  constexpr int NV = kCols / V;
-  __shared__ float red_all[16][64];
-  const int warp = threadIdx.x >> 5;
-  const int grp = warp / p.warps, wig = warp - grp * p.warps;
-  const int t = threadIdx.x - grp * p.warps * 32, nt = p.warps * 32;
-  float* red = red_all[grp];
-  int turn = 0;
-  const float inv_d = 1.0f / static_cast<float>(p.D);
-  const long long row = static_cast<long long>(blockIdx.x) * p.groups + grp;
-  if (row >= p.T) return;   // a whole group: its barrier has no other members
-  const R* x = static_cast<const R*>(p.x) + row * p.ldx;
-  float y[kCols], o[kCols];
-  float so = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (t + i * nt) * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) y[i * V + j] = o[i * V + j] = 0.0f;
-    if (c < p.D) {
-      load_v<V>(x + c, y + i * V);
-      if (p.o) load_v<V>(p.o + row * p.ldo + c, o + i * V);
+  // piece i of a row, as pairs; zeros past D
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int i, Pair (&q)[4]) const {
+    if constexpr (V >= 8) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (any(i)) u = *reinterpret_cast<const uint4*>(row + col(i, 0));
+      q[0] = pair_of(bf16_lo(u.x), bf16_hi(u.x));
+      q[1] = pair_of(bf16_lo(u.y), bf16_hi(u.y));
+      q[2] = pair_of(bf16_lo(u.z), bf16_hi(u.z));
+      q[3] = pair_of(bf16_lo(u.w), bf16_hi(u.w));
+    } else {
+      scalars(row, i, q);
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) so = fmaf(o[i * V + j], o[i * V + j], so);
   }
-  float r_o = 1.0f;
-  if (p.w_post) {
-    r_o = 1.0f / sqrtf(group_sum(so, red, p.warps, wig, 1 + grp, turn) * inv_d + p.eps);
-    if (p.stats && t == 0) p.stats[row] = r_o;
+  __device__ __forceinline__ void load(const float* row, int i, Pair (&q)[4]) const {
+    if constexpr (V >= 8) {
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+      if (any(i)) {
+        a = *reinterpret_cast<const float4*>(row + col(i, 0));
+        b = *reinterpret_cast<const float4*>(row + col(i, 4));
+      }
+      q[0] = pair_of(a.x, a.y);
+      q[1] = pair_of(a.z, a.w);
+      q[2] = pair_of(b.x, b.y);
+      q[3] = pair_of(b.z, b.w);
+    } else {
+      scalars(row, i, q);
+    }
   }
-  float sy = 0.0f;
+  template <typename X>
+  __device__ __forceinline__ void scalars(const X* row, int i, Pair (&q)[4]) const {
+    float v[8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (t + i * nt) * V;
-    if (c < p.D) {
-      if (p.o) {
-        float w[V], g[V];
-        weight_v<V>(p, p.w_post, c, w);
-        gate_v<V>(p, row, c, g);
+    for (int j = 0; j < 8; ++j) v[j] = col(i, j) < D ? to_f(row[col(i, j)]) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          y[i * V + j] = fmaf(p.alpha, y[i * V + j], p.beta * (g[j] * (o[i * V + j] * r_o * w[j])));
+    for (int j = 0; j < 4; ++j) q[j] = pair_of(v[2 * j], v[2 * j + 1]);
+  }
+  __device__ __forceinline__ void load(const void* row, int f32, int i, Pair (&q)[4]) const {
+    if (f32) load(static_cast<const float*>(row), i, q);
+    else load(static_cast<const __nv_bfloat16*>(row), i, q);
+  }
+
+  template <typename X>
+  __device__ __forceinline__ void store(X* row, int i, const Pair (&q)[4]) const {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split(q[j], v[2 * j], v[2 * j + 1]);
+    if constexpr (V >= 8) {
+      if (!any(i)) return;
+      if constexpr (sizeof(X) == 2) {
+        *reinterpret_cast<uint4*>(row + col(i, 0)) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
       } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) y[i * V + j] *= p.alpha;
+        *reinterpret_cast<float4*>(row + col(i, 0)) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(row + col(i, 4)) = make_float4(v[4], v[5], v[6], v[7]);
       }
-      if (p.y) store_v<V>(static_cast<R*>(p.y) + row * p.ldy + c, y + i * V);
+    } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) sy = fmaf(y[i * V + j], y[i * V + j], sy);
+      for (int j = 0; j < 8; ++j)
+        if (col(i, j) < D) put(row + col(i, j), v[j]);
     }
   }
-  if (p.w_pre) {
-    const float r_y = 1.0f / sqrtf(group_sum(sy, red, p.warps, wig, 1 + grp, turn) * inv_d + p.eps);
-    if (p.stats && t == 0) p.stats[p.T + row] = r_y;
+  __device__ __forceinline__ void store(void* row, int f32, int i, const Pair (&q)[4]) const {
+    if (f32) store(static_cast<float*>(row), i, q);
+    else store(static_cast<__nv_bfloat16*>(row), i, q);
+  }
+};
+
+// One value of either type.
+__device__ __forceinline__ float param_at(const void* p, int f32, long long i) {
+  return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void param_put(void* p, int f32, long long i, float v) {
+  if (f32) static_cast<float*>(p)[i] = v;
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ const void* param_row(const void* p, int f32, long long i) {
+  return static_cast<const uint8_t*>(p) + i * (f32 ? 4 : 2);
+}
+__device__ __forceinline__ void* param_row(void* p, int f32, long long i) {
+  return static_cast<uint8_t*>(p) + i * (f32 ? 4 : 2);
+}
+
+// 1/sqrt(x): the hardware's approximation and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = rsqrtf(x);
+  return r < INFINITY && r > 0.0f ? r * fmaf(-0.5f * x * r, r, 1.5f) : r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// the first `bytes` of 16, zeros after them
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 8 values of a weight or gate [D] from column c (16-byte aligned whatever D is).
+__device__ __forceinline__ void params8(const void* p, int f32, int c, int D, float (&v)[8]) {
+  if (c + 8 <= D) {
+    if (f32) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c));
+      v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+      v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+    }
+  } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * nt) * V;
-      if (c < p.D) {
-        float w[V];
-        weight_v<V>(p, p.w_pre, c, w);
+    for (int j = 0; j < 8; ++j) v[j] = c + j < D ? param_at(p, f32, c + j) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ float token_gate(const NormParams& p, long long row) {
+  return p.gate_mode == MOE_GATE_TOKEN ? param_at(p.gate, p.gate_f32, row) : 1.0f;
+}
+
+// A group of warps: its place, its columns' factors and its rows in flight.
+template <int V, int P>
+struct Group {
+  const NormParams& p;
+  Columns<V> cols;
+  int grp, wig, bar;
+  float* red;
+  int turn = 0;
+  const float* table;     // f [D], w_pre [D]
+  uint8_t* slots;
+  long long next_row, step;
+  int left, fill;         // rows still to send for, and the slot of the next
+  int take;               // slot of the row at hand
+
+  __device__ __forceinline__ Group(const NormParams& p_, uint8_t* shared, float (*red_all)[64]) : p(p_) {
+    const int warp = threadIdx.x >> 5;
+    grp = warp / p.warps;
+    wig = warp - grp * p.warps;
+    cols.nt = p.warps * 32;
+    cols.t = threadIdx.x - grp * cols.nt;
+    cols.D = p.D;
+    bar = 1 + grp;
+    red = red_all[grp];
+    for (int i = threadIdx.x; i < 15 * 64; i += blockDim.x) (&red_all[0][0])[i] = 0.0f;
+    table = reinterpret_cast<const float*>(shared);
+    slots = shared + p.table + static_cast<size_t>(grp) * p.stages * p.slot;
+  }
+
+  // Fill the CTA's table with what the weights and a channel gate contribute
+  // to each column: f = beta w_post g, the factor of n in y, and w_pre (all
+  // threads; ends with a barrier).
+  __device__ __forceinline__ void make_table(uint8_t* shared) const {
+    float* f = reinterpret_cast<float*>(shared);
+    float* h = f + p.table / 8;
+    for (int c = threadIdx.x * 8; c < p.D; c += blockDim.x * 8) {
+      float a[8], b[8], w[8];
+      if (p.w_post) params8(p.w_post, p.params_f32, c, p.D, a);
+      if (p.gate_mode == MOE_GATE_CHANNEL) params8(p.gate, p.gate_f32, c, p.D, b);
+      if (p.w_pre) params8(p.w_pre, p.params_f32, c, p.D, w);
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[i * V + j] = y[i * V + j] * r_y * w[j];
-        store_v<V>(p.h + row * p.ldh + c, y + i * V);
+      for (int j = 0; j < 8; ++j) {
+        float v = p.beta;
+        if (p.w_post) v *= a[j] + p.offset;
+        if (p.gate_mode == MOE_GATE_CHANNEL) v *= b[j];
+        if (c + j < p.D) {
+          f[c + j] = v;
+          h[c + j] = p.w_pre ? w[j] + p.offset : 0.0f;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void factor(int which, int i, Pair (&q)[4]) const {
+    cols.load(table + which * (p.table / 8), i, q);
+  }
+
+  __device__ __forceinline__ void sync() const {
+    if (p.warps == 1) __syncwarp();
+    else named_bar_sync(bar, cols.nt);
+  }
+
+  // Sum over the group in a fixed order: an xor tree in each warp, then the
+  // warp sums in quads.  `red` is 2 x 32 floats (zero beyond the warps),
+  // used in turns, so one barrier a sum is enough.
+  __device__ __forceinline__ float sum(Pair v2) {
+    float v = sum2(v2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (p.warps == 1) return v;
+    float* r = red + turn;
+    turn ^= 32;
+    if ((threadIdx.x & 31) == 0) r[wig] = v;
+    named_bar_sync(bar, cols.nt);
+    return warp_sums(r);
+  }
+  __device__ __forceinline__ float warp_sums(const float* r) const {
+    const float4* q = reinterpret_cast<const float4*>(r);
+    float t = (q[0].x + q[0].y) + (q[0].z + q[0].w);
+    if (p.warps > 4) t += (q[1].x + q[1].y) + (q[1].z + q[1].w);
+    if (p.warps > 8) t += ((q[2].x + q[2].y) + (q[2].z + q[2].w)) + ((q[3].x + q[3].y) + (q[3].z + q[3].w));
+    return t;
+  }
+
+  // Two sums at once.
+  __device__ __forceinline__ void sum_two(Pair a2, Pair b2, float& sa, float& sb) {
+    float a = sum2(a2), b = sum2(b2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    if (p.warps == 1) {
+      sa = a;
+      sb = b;
+      return;
+    }
+    float* r = red + turn;
+    turn ^= 32;
+    if ((threadIdx.x & 31) == 0) {
+      r[wig] = a;
+      r[16 + wig] = b;
+    }
+    named_bar_sync(bar, cols.nt);
+    sa = warp_sums(r);
+    sb = warp_sums(r + 16);
+  }
+
+  // Copy the next row's streams LO .. HI - 1 into slot `fill`.
+  template <int LO, int HI>
+  __device__ __forceinline__ void copy() const {
+    const uint32_t slot = smem_u32(slots) + fill * p.slot;
+#pragma unroll
+    for (int k = LO; k < HI; ++k) {
+      if (p.in[k].base == nullptr) continue;
+      const uint8_t* src = p.in[k].base + next_row * p.in[k].ld;
+      uint32_t dst = slot + p.in[k].off;
+      if constexpr (V >= 8) {
+        // this thread's own columns: 8 elements are 16 or 32 bytes
+        const int at = cols.t * 8 * p.in[k].esz;
+        src += at;
+        dst += at;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          if (cols.any(i)) {
+            cp_async16(dst + i * p.in[k].piece, src + i * p.in[k].piece);
+            if (p.in[k].esz == 4) cp_async16(dst + i * p.in[k].piece + 16, src + i * p.in[k].piece + 16);
+          }
+        }
+      } else {
+        const uint8_t* a = src - (reinterpret_cast<uintptr_t>(src) & 15);
+        const int n = static_cast<int>(src - a + p.in[k].row_bytes + 15) >> 4;
+        const long long all = p.in[k].end - a;   // 16 n passes it in the last row only
+        for (int j = cols.t; j < n; j += cols.nt) {
+          const long long rest = all - 16ll * j;
+          cp_async16(dst + 16 * j, a + 16ll * j, rest < 16 ? static_cast<int>(rest) : 16);
+        }
       }
     }
   }
+  __device__ __forceinline__ void sent() {
+    next_row += step;
+    --left;
+    fill = fill + 1 == p.stages ? 0 : fill + 1;
+  }
+
+  // Send for the first rows of first, first + step, ... (n of them).
+  __device__ __forceinline__ void start(long long first, long long step_, int n) {
+    next_row = first;
+    step = step_;
+    left = n;
+    fill = 0;
+    take = -1;
+    for (int i = 0; i < p.stages; ++i) {
+      if (left > 0) {
+        copy<0, kStreams>();
+        sent();
+      }
+      cp_commit();
+    }
+  }
+  // Make the next row ready; its slot.  HELD: the row before it has not been
+  // released yet.
+  template <bool HELD>
+  __device__ __forceinline__ int next() {
+    take = take + 1 == p.stages ? 0 : take + 1;
+    const int newer = p.stages - 1 - HELD;   // rows that may still be under way
+    if (newer <= 0) cp_wait<0>();
+    else if (newer == 1) cp_wait<1>();
+    else if (newer == 2) cp_wait<2>();
+    else cp_wait<3>();
+    if (V == 1) sync();
+    return take;
+  }
+  // The oldest row has been read (early: all of it but o, where a thread
+  // reads what it copied itself): its place takes the row `stages` further on.
+  __device__ __forceinline__ void release_early() {
+    if (V >= 8 && left > 0) copy<0, kO>();
+  }
+  __device__ __forceinline__ void release() {
+    if (left > 0) {
+      if (V == 1) sync();
+      copy<V >= 8 ? kO : 0, kStreams>();
+      sent();
+    }
+    cp_commit();
+  }
+
+  template <typename X = void>
+  __device__ __forceinline__ const X* stream(int k, long long row, int slot) const {
+    const uint8_t* q = slots + slot * p.slot + p.in[k].off;
+    if constexpr (V == 1) q += reinterpret_cast<uintptr_t>(p.in[k].base + row * p.in[k].ld) & 15;
+    return reinterpret_cast<const X*>(q);
+  }
+  // The row's own gate (grouped gates and gates of every element).
+  __device__ __forceinline__ const void* gate_row(long long row, int slot) const {
+    if (p.in[kG].base) return stream(kG, row, slot);
+    return param_row(p.gate, p.gate_f32, static_cast<long long>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.rows_per_group)) * p.D);
+  }
+};
+
+template <typename R, int V, bool ALL>
+__global__ void __launch_bounds__(kWarps * 32, 1) block_norm_fwd_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) uint8_t shared[];
+  __shared__ __align__(16) float red_all[15][64];
+  constexpr int P = kPiecesOf<V, false>;
+  Group<V, P> g(p, shared, red_all);
+  const int first = blockIdx.x * p.groups + g.grp, step = gridDim.x * p.groups;
+  const int n = first < p.T ? (p.T - 1 - first) / step + 1 : 0;
+  g.start(first, step, n);
+  g.make_table(shared);
+  const Columns<V> cols = g.cols;
+  // ALL: every part is there and no gate changes by the row (the common call)
+  const bool has_o = ALL || p.in[kO].base != nullptr, post = ALL || p.w_post != nullptr, pre = ALL || p.w_pre != nullptr;
+  const bool row_gate = !ALL && (p.gate_mode == MOE_GATE_GROUP || p.gate_mode == kGateFull);
+  const float inv_d = 1.0f / static_cast<float>(p.D);
+  const Pair alpha = both(p.alpha);
+  long long row = first;
+  for (int it = 0; it < n; ++it, row += step) {
+    const int slot = g.template next<false>();
+    Pair y[P][4], o[P][4];
+    float r_o = 1.0f;
+    if (has_o) {
+      const __nv_bfloat16* os = g.template stream<__nv_bfloat16>(kO, row, slot);
+      Pair so = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (V >= 8 && !cols.any(i)) continue;
+        Pair f[4];
+        cols.load(os, i, o[i]);
+        g.factor(0, i, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          so = fma2(o[i][j], o[i][j], so);
+          o[i][j] = mul2(o[i][j], f[j]);
+        }
+      }
+      if (row_gate) {
+        const void* gr = g.gate_row(row, slot);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          if (V >= 8 && !cols.any(i)) continue;
+          Pair f[4];
+          cols.load(gr, p.gate_f32, i, f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][j] = mul2(o[i][j], f[j]);
+        }
+      }
+      if (post) {
+        r_o = inv_sqrt(fmaf(g.sum(so), inv_d, p.eps));
+        if (p.stats && cols.t == 0) p.stats[row] = r_o;
+      }
+      r_o *= token_gate(p, row);
+    }
+    const R* xs = g.template stream<R>(kX, row, slot);
+    const Pair r2 = both(r_o);
+    Pair sy = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (V >= 8 && !cols.any(i)) continue;
+      cols.load(xs, i, y[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[i][j] = mul2(alpha, y[i][j]);
+        if (has_o) y[i][j] = fma2(o[i][j], r2, y[i][j]);
+        sy = fma2(y[i][j], y[i][j], sy);
+      }
+      if (ALL || p.y) cols.store(static_cast<R*>(p.y) + row * p.ldy, i, y[i]);
+    }
+    g.release_early();
+    g.release();
+    if (pre) {
+      const float r_y = inv_sqrt(fmaf(g.sum(sy), inv_d, p.eps));
+      if (p.stats && cols.t == 0) p.stats[p.T + row] = r_y;
+      const Pair ry2 = both(r_y);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (V >= 8 && !cols.any(i)) continue;
+        Pair w[4];
+        g.factor(1, i, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = mul2(mul2(y[i][j], ry2), w[j]);
+        cols.store(p.h + row * p.ldh, i, w);
+      }
+    }
+  }
+  cp_wait<0>();
 }
 
 // A group's rows: every gridDim * groups-th one, or (grouped gates) the
-// slabs it owns, each within one gate row.  The parameter gradients of a
-// group's rows stay in its threads' registers (16 columns each) and are
-// added over the CTA's groups, in group order, at the end; slabs of a
-// grouped gate are written out as each one ends.
-template <typename R, int V, int THREADS>
-__global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const NormParams p) {
-  constexpr int NV = kCols / V;
-  __shared__ float red_all[16][64];
-  const int warp = threadIdx.x >> 5;
-  const int grp = warp / p.warps, wig = warp - grp * p.warps;
-  const int t = threadIdx.x - grp * p.warps * 32, nt = p.warps * 32;
-  float* red = red_all[grp];
-  int turn = 0;
+// slabs it owns, each within one gate row.  With f = beta g w_o, y = alpha x
+// + f n and b = f s, so one factor a column serves both directions; and the
+// parameter sums need only S = sum_t s n a column (dw_o = beta g S, dgate =
+// beta w_o S where g does not change with t) and sum_t dh z.  They stay in
+// registers (GATE is MOE_GATE_NONE for every gate that needs no more than
+// that) and are added over the CTA's groups, in group order, at the end; a
+// grouped gate's S is turned into its dgate, and into dw_o, slab by slab.
+// Passes over a row in shared memory: x, o, dh for sum a z; then dh, dy, o
+// for s, dx and b (z, kept, gives its place to b); then o for do.
+template <typename R, int V, int GATE, bool ALL>
+__global__ void __launch_bounds__(kWarps * 32, 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) uint8_t shared[];
+  __shared__ __align__(16) float red_all[15][64];
+  constexpr int P = kPiecesOf<V, true>;
+  Group<V, P> g(p, shared, red_all);
+  const int worker = blockIdx.x * p.groups + g.grp, workers = gridDim.x * p.groups;
+  if constexpr (GATE != MOE_GATE_GROUP) {
+    g.start(worker, workers, worker < p.T ? (p.T - 1 - worker) / workers + 1 : 0);
+  }
+  g.make_table(shared);
+  const Columns<V> cols = g.cols;
+  // ALL: every part is there (the common call), which these tests then cost nothing
+  const bool has_o = ALL || p.in[kO].base != nullptr, has_dy = ALL || p.in[kDy].base != nullptr;
+  const bool post = ALL || p.w_post != nullptr, pre = ALL || p.w_pre != nullptr, has_dx = ALL || p.dx != nullptr;
   const float inv_d = 1.0f / static_cast<float>(p.D);
-  const int worker = blockIdx.x * p.groups + grp, workers = gridDim.x * p.groups;
-  const bool slabbed = p.gate_mode == MOE_GATE_GROUP && p.dgate != nullptr;
-  float aw_o[kCols], aw_h[kCols], ag[kCols];
+  Pair S[P][4], aw_h[P][4];   // running column sums
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) aw_o[i] = aw_h[i] = ag[i] = 0.0f;
+  for (int i = 0; i < P; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) S[i][j] = aw_h[i][j] = both(0.0f);
 
-  auto do_row = [&](long long row) {
-    const R* x = static_cast<const R*>(p.x) + row * p.ldx;
-    float y[kCols], n[kCols], s[kCols];   // s: dy, then the gradient of y; n: o r_o
-    const float r_o = (p.o && p.w_post) ? p.stats[row] : 1.0f;
-    const float r_y = p.w_pre ? p.stats[p.T + row] : 0.0f;
-    float d[kCols];
-    float saz = 0.0f;
+  // a row's statistics and token gate, loaded a row before they are needed
+  struct RowStats {
+    float r_o, r_y, tg;
+  };
+  auto stats_of = [&](long long row) {
+    RowStats q;
+    q.r_o = (has_o && post) ? p.stats[row] : 1.0f;
+    q.r_y = pre ? p.stats[p.T + row] : 0.0f;
+    q.tg = has_o ? token_gate(p, row) : 1.0f;
+    return q;
+  };
+  // the row in ring slot `slot`: z = y r_y, sum_t dh z, and this thread's part of sum a z
+  auto first_pass = [&](long long row, int slot, const RowStats& st, Pair (&z)[P][4]) {
+    Pair saz = both(0.0f);
+    if (!pre) return saz;
+    const R* x = g.template stream<R>(kX, row, slot);
+    const __nv_bfloat16* o = g.template stream<__nv_bfloat16>(kO, row, slot);
+    const __nv_bfloat16* dh = g.template stream<__nv_bfloat16>(kDh, row, slot);
+    const void* gr = GATE != MOE_GATE_NONE ? g.gate_row(row, slot) : nullptr;
+    const Pair ay = both(p.alpha * st.r_y), ro = both(st.r_o * st.tg * st.r_y);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * nt) * V;
+    for (int i = 0; i < P; ++i) {
+      if (V >= 8 && !cols.any(i)) continue;
+      Pair q[4], f[4];
+      cols.load(x, i, z[i]);
 #pragma unroll
-      for (int j = 0; j < V; ++j) y[i * V + j] = n[i * V + j] = s[i * V + j] = d[i * V + j] = 0.0f;
-      if (c < p.D) {
-        load_v<V>(x + c, y + i * V);
-        if (p.o) load_v<V>(p.o + row * p.ldo + c, n + i * V);
-        if (p.dy) load_v<V>(static_cast<const R*>(p.dy) + row * p.lddy + c, s + i * V);
-        if (p.w_pre) load_v<V>(p.dh + row * p.lddh + c, d + i * V);
+      for (int j = 0; j < 4; ++j) z[i][j] = mul2(z[i][j], ay);
+      if (has_o) {
+        cols.load(o, i, q);
+        g.factor(0, i, f);
+        if constexpr (GATE != MOE_GATE_NONE) {
+          Pair gg[4];
+          cols.load(gr, p.gate_f32, i, gg);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], gg[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[i][j] = fma2(mul2(q[j], f[j]), ro, z[i][j]);
+      }
+      cols.load(dh, i, q);
+      g.factor(1, i, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        aw_h[i][j] = fma2(q[j], z[i][j], aw_h[i][j]);
+        saz = fma2(mul2(q[j], f[j]), z[i][j], saz);
       }
     }
-    if (p.w_pre) {
+    return saz;
+  };
+  // s, dx, S and b (in z's place; without the token gate), and this thread's
+  // part of sum f s o; m: mean a z
+  auto second_pass = [&](long long row, int slot, const RowStats& st, float m, Pair (&z)[P][4]) {
+    const R* dy = g.template stream<R>(kDy, row, slot);
+    const __nv_bfloat16* o = g.template stream<__nv_bfloat16>(kO, row, slot);
+    const __nv_bfloat16* dh = g.template stream<__nv_bfloat16>(kDh, row, slot);
+    const void* gr = GATE != MOE_GATE_NONE ? g.gate_row(row, slot) : nullptr;
+    const Pair ro2 = both(st.r_o), rot2 = both(st.r_o * st.tg), ry2 = both(st.r_y), m2 = both(-m), alpha = both(p.alpha);
+    Pair sbn = both(0.0f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * nt) * V;
-        if (c < p.D) {
-          float w[V], g[V], wh[V];
-          weight_v<V>(p, p.w_pre, c, wh);
-          if (p.o) {
-            weight_v<V>(p, p.w_post, c, w);
-            gate_v<V>(p, row, c, g);
-          }
+    for (int i = 0; i < P; ++i) {
+      if (V >= 8 && !cols.any(i)) continue;
+      Pair s[4], q[4], f[4];
+      if (has_dy) {
+        cols.load(dy, i, s);
+      } else {
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int k = i * V + j;
-            float yy = p.alpha * y[k];
-            if (p.o) yy = fmaf(p.beta, g[j] * (n[k] * r_o * w[j]), yy);
-            const float z = yy * r_y;
-            aw_h[k] = fmaf(d[k], z, aw_h[k]);
-            const float a = d[k] * wh[j];
-            saz = fmaf(a, z, saz);
-            d[k] = a;
-            y[k] = z;
-          }
+        for (int j = 0; j < 4; ++j) s[j] = both(0.0f);
+      }
+      if (pre) {
+        cols.load(dh, i, q);
+        g.factor(1, i, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = fma2(ry2, fma2(z[i][j], m2, mul2(q[j], f[j])), s[j]);
+      }
+      if (has_dx) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = mul2(alpha, s[j]);
+        cols.store(static_cast<R*>(p.dx) + row * p.D, i, q);
+      }
+      if (!has_o) continue;
+      cols.load(o, i, q);
+      g.factor(0, i, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = mul2(s[j], q[j]);   // s o
+      if constexpr (GATE == MOE_GATE_NONE) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          S[i][j] = fma2(rot2, q[j], S[i][j]);
+          sbn = fma2(f[j], q[j], sbn);
+          z[i][j] = mul2(s[j], f[j]);
+        }
+      } else {
+        Pair gg[4];
+        cols.load(gr, p.gate_f32, i, gg);
+        if constexpr (GATE == kGateFull) {        // its gradient goes out with the row
+          Pair dg[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dg[j] = mul2(mul2(f[j], q[j]), ro2);
+          cols.store(param_row(p.dgate, p.gate_f32, row * p.D), p.gate_f32, i, dg);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[j] = mul2(f[j], gg[j]);
+          S[i][j] = fma2(GATE == kGateFull ? mul2(gg[j], ro2) : ro2, q[j], S[i][j]);
+          sbn = fma2(f[j], q[j], sbn);
+          z[i][j] = mul2(s[j], f[j]);
         }
       }
-      const float m = group_sum(saz, red, p.warps, wig, 1 + grp, turn) * inv_d;
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) s[k] = fmaf(r_y, d[k] - y[k] * m, s[k]);
     }
+    return sbn;
+  };
+  // do from b; sg: sum b n = r_o sum f s o, without the token gate
+  auto third_pass = [&](long long row, int slot, const RowStats& st, float sg, Pair (&z)[P][4]) {
+    if (GATE == MOE_GATE_NONE && p.gate_mode == MOE_GATE_TOKEN && cols.t == 0) param_put(p.dgate, p.gate_f32, row, sg);
+    const __nv_bfloat16* o = g.template stream<__nv_bfloat16>(kO, row, slot);
+    const float rot = st.r_o * st.tg;
+    const Pair rot2 = both(rot), mm = both(-rot * st.r_o * sg * inv_d);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * nt) * V;
-      if (c < p.D && p.dx) {
-        float v[V];
+    for (int i = 0; i < P; ++i) {
+      if (V >= 8 && !cols.any(i)) continue;
+      if (post) {
+        Pair q[4];
+        cols.load(o, i, q);
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = p.alpha * s[i * V + j];
-        store_v<V>(static_cast<R*>(p.dx) + row * p.lddx + c, v);
+        for (int j = 0; j < 4; ++j) z[i][j] = fma2(q[j], mm, mul2(rot2, z[i][j]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[i][j] = mul2(rot2, z[i][j]);
       }
+      cols.store(p.do_ + row * p.D, i, z[i]);
     }
-    if (!p.o) return;
-    float sbn = 0.0f, sg = 0.0f;
+  };
+  const bool two_sums = has_o && (post || p.gate_mode == MOE_GATE_TOKEN);
+
+  // n rows row0, row0 + step, ...: the second pass of a row and the first of
+  // the next run back to back and share one sum over the group, so that a
+  // row costs one barrier; with one row in flight each has its own.
+  auto rows = [&](long long row0, long long step, int n) {
+    if (n <= 0) return;
+    RowStats st = stats_of(row0), ahead = st;
+    Pair z[P][4];
+    int slot = g.template next<false>();
+    Pair saz = first_pass(row0, slot, st, z);
+    float m = pre ? g.sum(saz) * inv_d : 0.0f;
+    for (int it = 0; it < n; ++it) {
+      const long long row = row0 + it * step;
+      const bool more = it + 1 < n;
+      if (more) ahead = stats_of(row + step);
+      const Pair sbn = second_pass(row, slot, st, m, z);
+      g.release_early();
+      if (p.stages > 1 && more) {
+        Pair zn[P][4];
+        const int slot2 = g.template next<true>();
+        saz = first_pass(row + step, slot2, ahead, zn);
+        float sg = 0.0f;
+        g.sum_two(sbn, saz, sg, m);
+        m *= inv_d;
+        if (has_o) third_pass(row, slot, st, sg * st.r_o, z);
+        g.release();
+        slot = slot2;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * nt) * V;
-      if (c < p.D) {
-        float w[V], g[V];
-        weight_v<V>(p, p.w_post, c, w);
-        gate_v<V>(p, row, c, g);
+        for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int k = i * V + j;
-          const float nn = n[k] * r_o, bs = p.beta * s[k];
-          const float dg = bs * nn * w[j];
-          ag[k] += dg;
-          sg += dg;
-          const float bg = bs * g[j];
-          aw_o[k] = fmaf(bg, nn, aw_o[k]);
-          const float b = bg * w[j];
-          sbn = fmaf(b, nn, sbn);
-          s[k] = b;
-          n[k] = nn;
+          for (int j = 0; j < 4; ++j) z[i][j] = zn[i][j];
+      } else {
+        const float sg = two_sums ? g.sum(sbn) : 0.0f;
+        if (has_o) third_pass(row, slot, st, sg * st.r_o, z);
+        g.release();
+        if (more) {
+          slot = g.template next<false>();
+          saz = first_pass(row + step, slot, ahead, z);
+          if (pre) m = g.sum(saz) * inv_d;
         }
       }
-    }
-    if (p.gate_mode == MOE_GATE_TOKEN && p.dgate) {
-      sg = group_sum(sg, red, p.warps, wig, 1 + grp, turn);
-      if (t == 0) store_param<1>(p.dgate, p.gate_f32, row, &sg);
-    }
-    if (p.w_post) {
-      const float m = group_sum(sbn, red, p.warps, wig, 1 + grp, turn) * inv_d;
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) s[k] = r_o * (s[k] - n[k] * m);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * nt) * V;
-      if (c < p.D) store_v<V>(p.do_ + row * p.lddo + c, s + i * V);
+      st = ahead;
     }
   };
 
-  if (!slabbed) {
-    for (long long row = worker; row < p.T; row += workers) do_row(row);
+  if constexpr (GATE != MOE_GATE_GROUP) {
+    rows(worker, workers, worker < p.T ? (p.T - 1 - worker) / workers + 1 : 0);
   } else {
+    Pair aw_o[P][4];   // sum over slabs of g S
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) aw_o[i][j] = both(0.0f);
     for (long long sl = worker; sl < p.slabs; sl += workers) {
-      const int g = static_cast<int>(sl / p.slabs_per_group), j = static_cast<int>(sl - static_cast<long long>(g) * p.slabs_per_group);
-      const int r0 = static_cast<int>(static_cast<long long>(p.rows_per_group) * j / p.slabs_per_group);
-      const int r1 = static_cast<int>(static_cast<long long>(p.rows_per_group) * (j + 1) / p.slabs_per_group);
-      for (int r = r0; r < r1; ++r) do_row(static_cast<long long>(g) * p.rows_per_group + r);
+      const long long gi = sl / p.slabs_per_group, k = sl - gi * p.slabs_per_group;
+      const long long r0 = gi * p.rows_per_group + p.rows_per_group * k / p.slabs_per_group;
+      const int n = static_cast<int>(gi * p.rows_per_group + p.rows_per_group * (k + 1) / p.slabs_per_group - r0);
+      if (V == 1) g.sync();   // the last slab's rows have been read
+      g.start(r0, 1, n);
+      rows(r0, 1, n);
+      cp_wait<0>();
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * nt) * V;
-        if (c < p.D) {
-          if (p.slabs_per_group == 1) store_param<V>(p.dgate, p.gate_f32, static_cast<long long>(g) * p.D + c, ag + i * V);
-          else store_v<V>(p.gate_partial + sl * p.D + c, ag + i * V);
+      for (int i = 0; i < P; ++i) {
+        if (V >= 8 && !cols.any(i)) continue;
+        Pair f[4], gg[4];
+        g.factor(0, i, f);
+        cols.load(param_row(p.gate, p.gate_f32, gi * p.D), p.gate_f32, i, gg);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[j] = mul2(f[j], S[i][j]);
+          aw_o[i][j] = fma2(gg[j], S[i][j], aw_o[i][j]);
+          S[i][j] = both(0.0f);
         }
-#pragma unroll
-        for (int k = 0; k < V; ++k) ag[i * V + k] = 0.0f;
+        if (p.slabs_per_group == 1) cols.store(param_row(p.dgate, p.gate_f32, gi * p.D), p.gate_f32, i, f);
+        else cols.store(p.gate_partial + sl * p.D, i, f);
       }
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) S[i][j] = aw_o[i][j];
   }
-  // the CTA's parameter gradients, groups in order
-  extern __shared__ float acc[];   // [D] per array when groups > 1
-  const bool want[3] = {p.o != nullptr && p.w_post != nullptr, p.w_pre != nullptr,
-                        p.gate_mode == MOE_GATE_CHANNEL && p.dgate != nullptr};
+  cp_wait<0>();
+  __syncthreads();   // the rows' memory is free: it takes the groups' sums
+  float* acc = reinterpret_cast<float*>(shared + p.table);   // [D], when groups > 1
 #pragma unroll
-  for (int a = 0; a < 3; ++a) {
-    if (!want[a]) continue;
-    float* out = p.partial + (static_cast<long long>(a) * gridDim.x + blockIdx.x) * p.D;
-    float* v = a == 0 ? aw_o : (a == 1 ? aw_h : ag);
-    for (int g = 0; g < p.groups; ++g) {
-      if (g == grp) {
+  for (int arr = 0; arr < 2; ++arr) {
+    if (arr == 0 ? !has_o : !pre) continue;
+    float* out = p.partial + (static_cast<long long>(arr) * gridDim.x + blockIdx.x) * p.D;
+    for (int k = 0; k < p.groups; ++k) {
+      if (k == g.grp) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (t + i * nt) * V;
-          if (c < p.D) {
+        for (int i = 0; i < P; ++i) {
+          if (V >= 8 && !cols.any(i)) continue;
+          Pair b[4];
+          if (k > 0) cols.load(acc, i, b);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const float b = v[i * V + j] + (g > 0 ? acc[c + j] : 0.0f);
-              if (g + 1 < p.groups) acc[c + j] = b;
-              else out[c + j] = b;
-            }
+          for (int j = 0; j < 4; ++j) {
+            const Pair v = arr == 0 ? S[i][j] : aw_h[i][j];
+            b[j] = k > 0 ? add2(b[j], v) : v;
           }
+          cols.store(k + 1 < p.groups ? acc : out, i, b);
         }
       }
       if (p.groups > 1) __syncthreads();
@@ -394,27 +828,37 @@ __global__ void __launch_bounds__(THREADS) block_norm_bwd_kernel(const NormParam
   }
 }
 
-// out[c] = sum over r of in[r][c] for `rows` partial rows, in a fixed order:
-// eight interleaved sums a column, then those in order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ in, int rows, int D, void* out0,
-                                                         void* out1, void* out2, int f32_2) {
+// The CTAs' column sums joined in a fixed order (eight interleaved sums a
+// column, then those in order) and turned into the gradients: blockIdx.y = 0
+// sum s n -> dw_post and a channel gate's dgate, 1 -> dw_pre.
+__global__ void __launch_bounds__(256) norm_param_grad_kernel(const __grid_constant__ NormParams p, int rows,
+                                                              float* dw_post, float* dw_pre) {
   __shared__ float part[8][33];
   const int a = blockIdx.y;
-  void* out = a == 0 ? out0 : (a == 1 ? out1 : out2);
-  if (out == nullptr) return;
+  if (a == 0 ? (dw_post == nullptr && p.gate_mode != MOE_GATE_CHANNEL) : dw_pre == nullptr) return;
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
   float s = 0.0f;
-  if (c < D) {
-    const float* p = in + static_cast<long long>(a) * rows * D + c;
+  if (c < p.D) {
+    const float* q = p.partial + static_cast<long long>(a) * rows * p.D + c;
 #pragma unroll 8
-    for (int r = ry; r < rows; r += 8) s += p[static_cast<long long>(r) * D];
+    for (int r = ry; r < rows; r += 8) s += q[static_cast<long long>(r) * p.D];
   }
   part[ry][cx] = s;
   __syncthreads();
-  if (ry == 0 && c < D) {
+  if (ry == 0 && c < p.D) {
     for (int k = 1; k < 8; ++k) s += part[k][cx];
-    store_param<1>(out, a == 2 ? f32_2 : 1, c, &s);
+    if (a == 1) {
+      dw_pre[c] = s;
+      return;
+    }
+    float g = 1.0f;
+    if (p.gate_mode == MOE_GATE_CHANNEL) {
+      g = param_at(p.gate, p.gate_f32, c);
+      const float w = p.w_post ? param_at(p.w_post, p.params_f32, c) + p.offset : 1.0f;
+      param_put(p.dgate, p.gate_f32, c, w * p.beta * s);
+    }
+    if (dw_post) dw_post[c] = p.beta * g * s;
   }
 }
 
@@ -427,7 +871,7 @@ __global__ void __launch_bounds__(256) gate_slab_sum_kernel(const float* __restr
   float s = 0.0f;
 #pragma unroll 8
   for (int r = 0; r < per_group; ++r) s += p[static_cast<long long>(r) * D];
-  store_param<1>(dgate, f32, static_cast<long long>(blockIdx.y) * D + c, &s);
+  param_put(dgate, f32, static_cast<long long>(blockIdx.y) * D + c, s);
 }
 
 // ------------------------------------------------------------------- host
@@ -435,33 +879,63 @@ __global__ void __launch_bounds__(256) gate_slab_sum_kernel(const float* __restr
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 struct Shape {
-  int warps, groups, threads;
+  int warps, groups, stages, threads;
 };
 
-Shape shape_of(int D) {
+// How many groups share a CTA, and how many rows
+// each has in flight.
+Shape place(NormParams* p, bool fwd, bool vec) {
   Shape s;
-  s.warps = (D + kWarpCols - 1) / kWarpCols;
-  s.groups = s.warps >= 8 ? 1 : 16 / s.warps;
-  if (s.groups > 15) s.groups = 15;   // named barriers 1 .. 15
+  const int warp_cols = 256 * (fwd ? (vec ? kPiecesOf<8, false> : kPiecesOf<1, false>) : (vec ? kPiecesOf<8, true> : kPiecesOf<1, true>));
+  s.warps = (p->D + warp_cols - 1) / warp_cols;
+  p->table = (p->D * 4 + 15) / 16 * 16 * 2;
+  const int room = kSharedMem - p->table;
+  s.groups = std::max(1, std::min({14 / s.warps, 15, room / p->slot}));   // named barriers 1 .. 15
+  s.stages = std::max(1, std::min(4, room / (s.groups * p->slot)));
   s.threads = s.warps * s.groups * 32;
+  p->warps = s.warps;
+  p->groups = s.groups;
+  p->stages = s.stages;
+  for (Stream& q : p->in) q.piece = s.warps * 32 * 8 * q.esz;
   return s;
 }
 
-template <typename R, int THREADS>
-void launch_fwd(bool vec, int ctas, const Shape& s, const NormParams& p, cudaStream_t stream) {
-  if (vec) block_norm_fwd_kernel<R, 8, THREADS><<<ctas, s.threads, 0, stream>>>(p);
-  else block_norm_fwd_kernel<R, 1, THREADS><<<ctas, s.threads, 0, stream>>>(p);
+template <typename K>
+cudaError_t launch(K kernel, PerDeviceOnce& once, int ctas, const Shape& s, size_t smem, const NormParams& p,
+                   cudaStream_t stream) {
+  const cudaError_t e =
+      once.once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMem); });
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, s.threads, smem, stream>>>(p);
+  return cudaGetLastError();
 }
 
-template <typename R, int THREADS>
-void launch_bwd(bool vec, int ctas, const Shape& s, size_t smem, const NormParams& p, cudaStream_t stream) {
-  if (vec) block_norm_bwd_kernel<R, 8, THREADS><<<ctas, s.threads, smem, stream>>>(p);
-  else block_norm_bwd_kernel<R, 1, THREADS><<<ctas, s.threads, smem, stream>>>(p);
+template <typename R, int V>
+cudaError_t launch_v(bool fwd, int ctas, const Shape& s, size_t smem, const NormParams& p, cudaStream_t stream) {
+  static PerDeviceOnce fwd_all, forward, all, none, group, full;
+  if (fwd) {
+    if (p.in[kO].base && p.w_post && p.w_pre && p.y && p.gate_mode != MOE_GATE_GROUP && p.gate_mode != kGateFull)
+      return launch(block_norm_fwd_kernel<R, V, true>, fwd_all, ctas, s, smem, p, stream);
+    return launch(block_norm_fwd_kernel<R, V, false>, forward, ctas, s, smem, p, stream);
+  }
+  if (p.gate_mode == MOE_GATE_GROUP)
+    return launch(block_norm_bwd_kernel<R, V, MOE_GATE_GROUP, false>, group, ctas, s, smem, p, stream);
+  if (p.gate_mode == kGateFull) return launch(block_norm_bwd_kernel<R, V, kGateFull, false>, full, ctas, s, smem, p, stream);
+  if (p.in[kX].base && p.in[kO].base && p.in[kDy].base && p.in[kDh].base && p.w_post && p.dx)
+    return launch(block_norm_bwd_kernel<R, V, MOE_GATE_NONE, true>, all, ctas, s, smem, p, stream);
+  return launch(block_norm_bwd_kernel<R, V, MOE_GATE_NONE, false>, none, ctas, s, smem, p, stream);
 }
 
-int backward_ctas(const Shape& s, int T, int sms) {
-  const int need = (T + s.groups - 1) / s.groups;
-  return need < sms ? need : sms;
+template <typename R>
+cudaError_t launch_norm(bool fwd, bool vec, int ctas, const Shape& s, const NormParams& p, cudaStream_t stream) {
+  const size_t rows = std::max<size_t>(static_cast<size_t>(s.groups) * s.stages * p.slot, s.groups > 1 ? 4ull * p.D : 0);
+  const size_t smem = p.table + rows;
+  if (!vec) return launch_v<R, 1>(fwd, ctas, s, smem, p, stream);
+  return p.D % (256 * (fwd ? kPiecesOf<8, false> : kPiecesOf<8, true>)) == 0 ? launch_v<R, kFull>(fwd, ctas, s, smem, p, stream) : launch_v<R, 8>(fwd, ctas, s, smem, p, stream);
+}
+
+cudaError_t launch_norm(bool fwd, bool vec, int ctas, const Shape& s, const NormParams& p, cudaStream_t stream) {
+  return p.res_f32 ? launch_norm<float>(fwd, vec, ctas, s, p, stream) : launch_norm<__nv_bfloat16>(fwd, vec, ctas, s, p, stream);
 }
 
 bool config_ok(const moe_block_norm_config* c) {
@@ -481,27 +955,25 @@ bool config_ok(const moe_block_norm_config* c) {
 // A row stride: 0 stands for d_model; smaller ones would overlap rows.
 bool stride_ok(int64_t ld, int32_t D) { return ld == 0 || ld >= D; }
 
-NormParams common_params(const moe_block_norm_config* c, const void* x, const void* branch, const void* gate,
-                         const void* w_post, const void* w_pre) {
+NormParams common_params(const moe_block_norm_config* c, const void* branch, const void* gate, const void* w_post,
+                         const void* w_pre) {
   NormParams p{};
   p.T = c->tokens;
   p.D = c->d_model;
-  p.x = x;
-  p.o = static_cast<const __nv_bfloat16*>(branch);
   p.gate = gate;
-  p.w_post = branch ? w_post : nullptr;
+  p.w_post = w_post;
   p.w_pre = w_pre;
-  auto ld = [&](int64_t v) { return v ? static_cast<long long>(v) : static_cast<long long>(c->d_model); };
-  p.ldx = ld(c->x_stride);
-  p.ldo = ld(c->branch_stride);
-  p.ldy = p.lddy = ld(c->y_stride);
-  p.ldh = p.lddh = ld(c->h_stride);
-  p.lddx = p.lddo = c->d_model;
+  p.ldy = c->y_stride ? c->y_stride : c->d_model;
+  p.ldh = c->h_stride ? c->h_stride : c->d_model;
   p.gate_mode = branch ? c->gate_mode : MOE_GATE_NONE;
-  p.rows_per_group = p.gate_mode == MOE_GATE_GROUP ? c->tokens / c->gate_rows : 1;
-  if (p.rows_per_group < 1) p.rows_per_group = 1;
+  p.rows_per_group = 1;
+  if (p.gate_mode == MOE_GATE_GROUP) {
+    p.rows_per_group = c->tokens / c->gate_rows;
+    if (p.rows_per_group == 1) p.gate_mode = kGateFull;
+  }
   p.params_f32 = c->weight_type == MOE_TYPE_FP32;
   p.gate_f32 = c->gate_type == MOE_TYPE_FP32;
+  p.res_f32 = c->residual_type == MOE_TYPE_FP32;
   p.alpha = c->residual_scale;
   p.beta = c->branch_scale;
   p.eps = c->eps;
@@ -509,9 +981,31 @@ NormParams common_params(const moe_block_norm_config* c, const void* x, const vo
   return p;
 }
 
-bool vector_rows(const NormParams& p) {
-  return p.D % 8 == 0 && p.ldx % 8 == 0 && p.ldo % 8 == 0 && p.ldy % 8 == 0 && p.ldh % 8 == 0 && p.lddy % 8 == 0 &&
-         p.lddh % 8 == 0 && p.lddx % 8 == 0 && p.lddo % 8 == 0;
+// Add a streamed tensor (stride in elements, 0: D).
+void add_stream(NormParams* p, int k, const void* base, int64_t ld, moe_type type) {
+  if (base == nullptr) return;
+  Stream& s = p->in[k];
+  s.base = static_cast<const uint8_t*>(base);
+  s.esz = type == MOE_TYPE_FP32 ? 4 : 2;
+  s.ld = static_cast<long long>(ld ? ld : p->D) * s.esz;
+  s.row_bytes = p->D * s.esz;
+  s.end = s.base + (p->T - 1) * s.ld + s.row_bytes;
+}
+
+// Choose the vector path and lay out a row's slot; a gate of every element
+// that leaves no room for one row is read from global memory instead.
+bool lay_out(NormParams* p) {
+  bool vec = p->D % 8 == 0 && p->ldy % 8 == 0 && p->ldh % 8 == 0;
+  for (const Stream& s : p->in) vec = vec && (s.base == nullptr || (s.ld / s.esz) % 8 == 0);
+  p->slot = 0;
+  for (Stream& s : p->in) {
+    if (s.base == nullptr) continue;
+    s.off = p->slot;
+    const int need = (s.row_bytes + 15) / 16 * 16 + (vec ? 0 : 16);
+    if (&s == &p->in[kG] && p->slot + need + 8 * p->D + 32 > kSharedMem) s.base = nullptr;
+    else p->slot += need;
+  }
+  return vec;
 }
 
 int device_sms() {
@@ -547,32 +1041,29 @@ moe_status moe_block_norm_forward(const moe_block_norm_config* cfg, const void* 
   for (const void* q : {x, branch, gate, post_weight, pre_weight, static_cast<const void*>(y),
                         static_cast<const void*>(h), static_cast<const void*>(stats)})
     if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
-  NormParams p = common_params(cfg, x, branch, gate, post_weight, pre_weight);
+  NormParams p = common_params(cfg, branch, gate, post_weight, pre_weight);
   p.y = y;
   p.h = static_cast<__nv_bfloat16*>(h);
   p.stats = stats;
-  const Shape s = shape_of(p.D);
-  p.warps = s.warps;
-  p.groups = s.groups;
+  add_stream(&p, kX, x, cfg->x_stride, cfg->residual_type);
+  add_stream(&p, kO, branch, cfg->branch_stride, MOE_TYPE_BF16);
+  if (p.gate_mode == kGateFull) add_stream(&p, kG, gate, 0, cfg->gate_type);
+  const bool vec = lay_out(&p);
+  const Shape s = place(&p, true, vec);
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  const int ctas = (p.T + s.groups - 1) / s.groups;
-  const bool vec = vector_rows(p);
-  const bool bf = cfg->residual_type == MOE_TYPE_BF16;
-  if (s.threads <= 512) bf ? launch_fwd<__nv_bfloat16, 512>(vec, ctas, s, p, stream) : launch_fwd<float, 512>(vec, ctas, s, p, stream);
-  else bf ? launch_fwd<__nv_bfloat16, 1024>(vec, ctas, s, p, stream) : launch_fwd<float, 1024>(vec, ctas, s, p, stream);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const int ctas = std::min(sms, (p.T - 1) / s.groups + 1);
+  return launch_norm(true, vec, ctas, s, p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 size_t moe_block_norm_workspace_bytes(const moe_block_norm_config* cfg) {
   if (!config_ok(cfg) || cfg->d_model > kMaxCols) return 0;
   const int sms = device_sms();
   if (sms <= 0) return 0;
-  const Shape s = shape_of(cfg->d_model);
-  const size_t ctas = static_cast<size_t>(backward_ctas(s, cfg->tokens, sms));
-  size_t rows = 3 * ctas;
-  if (cfg->gate_mode == MOE_GATE_GROUP) rows += ctas * s.groups + 1;   // slab partials, when a gate row has several
-  return (rows * static_cast<size_t>(cfg->d_model) * sizeof(float) + 255) / 256 * 256 + 256;
+  // two arrays of column sums a CTA, and (grouped gates) a row for each group of warps
+  size_t rows = 2 * static_cast<size_t>(std::min(cfg->tokens, sms));
+  if (cfg->gate_mode == MOE_GATE_GROUP) rows += static_cast<size_t>(std::min(cfg->tokens, 16 * sms));
+  return rows * static_cast<size_t>(cfg->d_model) * sizeof(float) + 256;
 }
 
 moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void* x, const void* branch, const void* gate,
@@ -611,37 +1102,30 @@ moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void*
   if (need == 0) return MOE_ERR_CUDA;
   if (!workspace || workspace_bytes < need) return MOE_ERR_CAPACITY;
   const int sms = device_sms();
-  NormParams p = common_params(cfg, x, branch, gate, post_weight, pre_weight);
+  NormParams p = common_params(cfg, branch, gate, post_weight, pre_weight);
   p.stats = const_cast<float*>(stats);
-  p.dy = dy;
-  p.dh = static_cast<const __nv_bfloat16*>(dh);
   p.dx = dx;
   p.do_ = static_cast<__nv_bfloat16*>(dbranch);
   p.dgate = dgate;
-  const Shape s = shape_of(D);
-  p.warps = s.warps;
-  p.groups = s.groups;
-  const int ctas = backward_ctas(s, T, sms);
+  p.ldy = p.ldh = D;   // the outputs are contiguous
+  if (pre_weight) add_stream(&p, kX, x, cfg->x_stride, cfg->residual_type);
+  add_stream(&p, kO, branch, cfg->branch_stride, MOE_TYPE_BF16);
+  add_stream(&p, kDy, dy, cfg->y_stride, cfg->residual_type);
+  add_stream(&p, kDh, dh, cfg->h_stride, MOE_TYPE_BF16);
+  if (p.gate_mode == kGateFull) add_stream(&p, kG, gate, 0, cfg->gate_type);
+  const bool vec = lay_out(&p);
+  const Shape s = place(&p, false, vec);
+  const int ctas = std::min(sms, (T - 1) / s.groups + 1);
   p.partial = static_cast<float*>(workspace);
-  p.gate_partial = p.partial + 3ll * ctas * D;
+  p.gate_partial = p.partial + 2ll * ctas * D;
   if (p.gate_mode == MOE_GATE_GROUP) {
-    const int workers = ctas * s.groups;
-    int per = workers / cfg->gate_rows;
-    if (per < 1) per = 1;
-    if (per > p.rows_per_group) per = p.rows_per_group;
+    const int per = std::max(1, std::min(ctas * s.groups / cfg->gate_rows, p.rows_per_group));
     p.slabs_per_group = per;
     p.slabs = per * cfg->gate_rows;
   }
-  const bool vec = vector_rows(p);
-  const size_t smem = s.groups > 1 ? static_cast<size_t>(D) * sizeof(float) : 0;
-  const bool bf = cfg->residual_type == MOE_TYPE_BF16;
-  if (s.threads <= 512) bf ? launch_bwd<__nv_bfloat16, 512>(vec, ctas, s, smem, p, stream) : launch_bwd<float, 512>(vec, ctas, s, smem, p, stream);
-  else bf ? launch_bwd<__nv_bfloat16, 1024>(vec, ctas, s, smem, p, stream) : launch_bwd<float, 1024>(vec, ctas, s, smem, p, stream);
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-  void* channel = p.gate_mode == MOE_GATE_CHANNEL ? dgate : nullptr;
-  if (dpost_weight || dpre_weight || channel) {
-    column_sum_kernel<<<dim3((D + 31) / 32, 3), 256, 0, stream>>>(p.partial, ctas, D, dpost_weight, dpre_weight, channel,
-                                                                  p.gate_f32);
+  if (launch_norm(false, vec, ctas, s, p, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dpost_weight || dpre_weight || p.gate_mode == MOE_GATE_CHANNEL) {
+    norm_param_grad_kernel<<<dim3((D + 31) / 32, 2), 256, 0, stream>>>(p, ctas, dpost_weight, dpre_weight);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
   }
   if (p.gate_mode == MOE_GATE_GROUP && p.slabs_per_group > 1) {

@@ -27,7 +27,7 @@ _error_words = {}
 
 def _config(shape, steps, coefficients, eps):
     _need(len(shape) == 3, "expected a stack of matrices [E, rows, cols]")
-    _need(1 <= steps <= abi.MOE_MUON_MAX_STEPS, f"steps: 1 to {abi.MOE_MUON_MAX_STEPS}")
+    _need(1 <= steps <= abi.MOE_MUON_MAX_STEPS, "steps: 1 to 16")
     cfg = abi.moe_muon_config(shape[0], shape[1], shape[2], steps)
     cfg.eps = eps
     table = coefficients if len(coefficients) and hasattr(coefficients[0], "__len__") else [coefficients] * steps
@@ -72,7 +72,7 @@ def _workspace(given, shape, device):
     if given is None:
         return workspace(*shape, device=device)
     _need(given.dtype == torch.uint8 and given.is_contiguous() and given.device == device,
-          f"workspace: expected a contiguous uint8 tensor on {device}")
+          "workspace: expected a contiguous uint8 tensor on the weights' device")
     return given
 
 
@@ -85,10 +85,10 @@ def orthogonalize(x, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, 
     if out is not None:
         _dense("out", out, torch.bfloat16, tuple(x.shape), dev)
 
-    def run():
+    def run(s):
         o = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if out is None else out
         ws = _workspace(workspace, x.shape, dev)
-        abi.moe_orthogonalize(cfg, x, _TYPE[x.dtype], o, ws, ws.numel(), _error_word(dev))
+        abi.moe_orthogonalize(cfg, x, _TYPE[x.dtype], o, ws, ws.numel(), _error_word(dev), s)
         return o
 
     return on_stream(run, dev, stream)
@@ -120,10 +120,10 @@ def muon_update(weight, grad, momentum, *, lr, mu=0.95, nesterov=True, weight_de
         scale = 0.2 * math.sqrt(max(shape[1], shape[2]))
     rates = abi.moe_muon_rates(lr, mu, weight_decay, scale, 1 if nesterov else 0)
 
-    def run():
+    def run(s):
         ws = _workspace(workspace, shape, dev)
         abi.moe_muon_update(cfg, rates, weight, _TYPE[weight.dtype], grad, _TYPE[grad.dtype], momentum, weight_bf16, ws,
-                            ws.numel(), _error_word(dev))
+                            ws.numel(), _error_word(dev), s)
 
     on_stream(run, dev, stream)
 
