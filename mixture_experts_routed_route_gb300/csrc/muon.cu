@@ -52,21 +52,28 @@ namespace {
 
 constexpr float kSx = 4096.0f;   // stored X = X * kSx
 constexpr float kSb = 2048.0f;   // stored A, B = A, B * kSb
-constexpr int kBoxBytes = 2 * 128 * 128;   // two 64-element chunks of 128 rows
-constexpr int kStageBytes = 2 * kBoxBytes;
-constexpr int kStages = 3;
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
-constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
 constexpr int kMaxSteps = MOE_MUON_MAX_STEPS;
+
+// Tile of BN = 256 or 128 columns (256 rows on the pair): stages of 128
+// contraction elements, in two 64-element chunks of 128 (A) and BN / 2 (B)
+// rows per CTA; 4 KB an epilogue warp to turn its 32 x 32 chunks around.
+template <int BN>
+struct NsCfg {
+  static constexpr int kA = 2 * 128 * 128, kB = 2 * (BN / 2) * 128;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = BN == 256 ? 3 : 4;
+  static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * 4096 + 256;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
 
 enum NsKind { kGram, kPoly, kApply, kFinal };
 
 struct NsParams {
   int tiles;            // per matrix
   int total;            // tiles of all matrices
-  int n256;             // 256-row blocks of a symmetric output
-  int col_tiles;        // 256-column tiles of an apply output
+  int col_tiles;        // BN-column tiles of the output
   int kstages;          // stages of 128 contraction elements
   int a_mn, b_mn;       // operand read MN-major
   int rows, cols;       // valid rows, columns written (a multiple of 8)
@@ -114,24 +121,26 @@ __device__ __forceinline__ uint64_t sdesc_mn_f16(uint32_t saddr) {
 }
 
 struct NsTile {
-  int mat, row0, col0;   // this CTA's 128 output rows, the pair's 256 columns
+  int mat, row0, col0;   // this CTA's 128 output rows, the pair's BN columns
 };
 
-// Symmetric outputs: tile t of the upper triangle of n256 x n256 blocks.
-template <int KIND>
+// Symmetric outputs: row q of 256 rows has the column tiles from its first
+// one on.
+template <int KIND, int BN>
 __device__ __forceinline__ NsTile ns_tile(const NsParams& p, int tile, int rank) {
   NsTile t;
   t.mat = tile / p.tiles;
   int i = tile - t.mat * p.tiles, q = 0;
   if (KIND == kGram || KIND == kPoly) {
-    for (; i >= p.n256 - q; ++q) i -= p.n256 - q;
-    t.row0 = q * 256 + 128 * rank;
-    t.col0 = (q + i) * 256;
+    constexpr int kPer = 256 / BN;
+    for (; i >= p.col_tiles - q * kPer; ++q) i -= p.col_tiles - q * kPer;
+    i += q * kPer;
   } else {
     q = i / p.col_tiles;
-    t.row0 = q * 256 + 128 * rank;
-    t.col0 = (i - q * p.col_tiles) * 256;
+    i -= q * p.col_tiles;
   }
+  t.row0 = q * 256 + 128 * rank;
+  t.col0 = i * BN;
   return t;
 }
 
@@ -154,113 +163,184 @@ __device__ __forceinline__ void store_hi_lo(__half* hi, __half* lo, const float*
   *reinterpret_cast<uint4*>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// 32 columns of row r (this lane) and its columns c .. c + 31, from the
-// accumulator values v.
+// A 32 x 32 chunk of FP32 in a warp's 4 KB: float4 slot j of row r at slot
+// j ^ (r % 8), so that row writes, row reads and column reads spread over the
+// banks.
+__device__ __forceinline__ int chunk_at(int r, int c) { return r * 32 + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3)); }
+__device__ __forceinline__ float4& chunk_quad(float* ws, int r, int quad) {
+  return *reinterpret_cast<float4*>(ws + r * 32 + ((quad ^ (r & 7)) << 2));
+}
+
+__device__ __forceinline__ void store_half8(__half* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+}
+__device__ __forceinline__ void add_half8(const uint4& u, float (&x)[8]) {
+  const uint32_t h[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] += half_lo(h[j]);
+    x[2 * j + 1] += half_hi(h[j]);
+  }
+}
+
+// 8 values of the caller's output tensors at row r, columns c .. c + 7 (x:
+// the new X, stored scale).  ucols % 8 == 0: 16-byte accesses.
+__device__ __forceinline__ void put_update8(const NsParams& p, long long u, const float (&x)[8]) {
+  if (p.o16) {
+    constexpr float s = 1.0f / kSx;
+    *reinterpret_cast<uint4*>(p.o16 + u) = make_uint4(pack_bf16x2(x[0] * s, x[1] * s), pack_bf16x2(x[2] * s, x[3] * s),
+                                                      pack_bf16x2(x[4] * s, x[5] * s), pack_bf16x2(x[6] * s, x[7] * s));
+    return;
+  }
+  const float rate = -p.rate * (1.0f / kSx);
+  float w[8];
+  if (p.weight_f32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.weight) + u);
+    const float4 a = q[0], b = q[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = fmaf(p.decay, w[j], rate * x[j]);
+    q[0] = make_float4(w[0], w[1], w[2], w[3]);
+    q[1] = make_float4(w[4], w[5], w[6], w[7]);
+  } else {
+    uint4* q = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.weight) + u);
+    const uint4 a = *q;
+    w[0] = bf16_lo(a.x), w[1] = bf16_hi(a.x), w[2] = bf16_lo(a.y), w[3] = bf16_hi(a.y);
+    w[4] = bf16_lo(a.z), w[5] = bf16_hi(a.z), w[6] = bf16_lo(a.w), w[7] = bf16_hi(a.w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = fmaf(p.decay, w[j], rate * x[j]);
+    *q = make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
+  }
+  if (p.w16)
+    *reinterpret_cast<uint4*>(p.w16 + u) =
+        make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
+}
+__device__ __forceinline__ void put_update1(const NsParams& p, long long u, float x) {
+  if (p.o16) {
+    p.o16[u] = __float2bfloat16_rn(x * (1.0f / kSx));
+    return;
+  }
+  const float rate = -p.rate * (1.0f / kSx);
+  float w;
+  if (p.weight_f32) {
+    float* q = static_cast<float*>(p.weight) + u;
+    w = fmaf(p.decay, *q, rate * x);
+    *q = w;
+  } else {
+    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.weight) + u;
+    w = fmaf(p.decay, __bfloat162float(*q), rate * x);
+    *q = __float2bfloat16_rn(w);
+  }
+  if (p.w16) p.w16[u] = __float2bfloat16_rn(w);
+}
+
+// What a chunk needs besides the accumulator: 8 columns of rows lane / 4 + 8 it.
+struct ChunkIn {
+  uint4 hi[4], lo[4];
+};
+
 template <int KIND>
-__device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int r, int c, const uint32_t (&v)[32]) {
-  const bool in_rows = r < p.rows;
-  const long long at = t.mat * p.mat + static_cast<long long>(r) * p.pitch + c;
-  if constexpr (KIND == kGram || KIND == kPoly) {
-    uint32_t w[16];
+__device__ __forceinline__ void load_chunk_in(const NsParams& p, const NsTile& t, int r0, int c0, int lane, ChunkIn& in) {
+  if constexpr (KIND == kGram) return;
+  const int c = c0 + (lane & 3) * 8;
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int r = r0 + it * 8 + (lane >> 2);
+    in.hi[it] = in.lo[it] = make_uint4(0, 0, 0, 0);
+    if (r < p.rows && c < p.cols) {
+      const long long at = t.mat * p.mat + r * p.pitch + c;
+      in.hi[it] = *reinterpret_cast<const uint4*>(p.in_hi + at);
+      if constexpr (KIND == kApply || KIND == kFinal) in.lo[it] = *reinterpret_cast<const uint4*>(p.lo + at);
+    }
+  }
+}
+
+// The 32 x 32 chunk at rows r0, columns c0, whose accumulator values are in
+// ws.  Lanes take 8 columns of 8 rows at a time, so that the accesses of a
+// warp cover whole 64-byte (FP16) or 128-byte (FP32) pieces of rows.
+template <int KIND>
+__device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int r0, int c0, int lane, float* ws,
+                                         const ChunkIn& in) {
+  const int quad = (lane & 3) * 2, c = c0 + (lane & 3) * 8;
+  const float* d = p.diag + static_cast<long long>(t.mat) * p.diag_n;
+  const bool mirror = (KIND == kGram || KIND == kPoly) && (c0 >> 7) > (r0 >> 7);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int rr = it * 8 + (lane >> 2), r = r0 + rr;
+    const float4 a = chunk_quad(ws, rr, quad), b = chunk_quad(ws, rr, quad + 1);
+    float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const bool inside = r < p.rows && c < p.cols;
+    const long long at = t.mat * p.mat + r * p.pitch + c;
     if constexpr (KIND == kGram) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        w[j] = pack_half2(__uint_as_float(v[2 * j]) * (kSb / (kSx * kSx)), __uint_as_float(v[2 * j + 1]) * (kSb / (kSx * kSx)));
-    } else {
+      for (int j = 0; j < 8; ++j) x[j] *= kSb / (kSx * kSx);
+      if (inside) store_half8(p.out_hi + at, x);
+    } else if constexpr (KIND == kPoly) {
       const float cs = p.c * (1.0f / kSb);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (in_rows && c + 8 * g < p.cols) u = *reinterpret_cast<const uint4*>(p.in_hi + at + 8 * g);
-        const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = 8 * g + 2 * j;
-          float x0 = fmaf(cs, __uint_as_float(v[k]), p.b * half_lo(a[j]));
-          float x1 = fmaf(cs, __uint_as_float(v[k + 1]), p.b * half_hi(a[j]));
-          if (c + k == r) {
-            if (in_rows) p.diag[static_cast<long long>(t.mat) * p.diag_n + r] = x0 * (1.0f / kSb);
-            x0 = 0.0f;
-          }
-          if (c + k + 1 == r) {
-            if (in_rows) p.diag[static_cast<long long>(t.mat) * p.diag_n + r] = x1 * (1.0f / kSb);
-            x1 = 0.0f;
-          }
-          w[4 * g + j] = pack_half2(x0, x1);
-        }
-      }
-    }
-    if (in_rows) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        if (c + 8 * g < p.cols)
-          *reinterpret_cast<uint4*>(p.out_hi + at + 8 * g) = make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
-    }
-    // the mirror image of blocks above the diagonal (column r of rows c ..)
-    if ((c >> 7) > (r >> 7) && r < p.cols) {
-      __half* m = p.out_hi + t.mat * p.mat + r;
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (c + k < p.rows)
-          m[(c + k) * p.pitch] = __ushort_as_half(static_cast<unsigned short>((k & 1) ? (w[k >> 1] >> 16) : (w[k >> 1] & 0xFFFFu)));
-    }
-  } else {
-    if (!in_rows) return;
-    const float* d = p.diag + static_cast<long long>(t.mat) * p.diag_n;
-    const float drow = p.diag_cols ? 0.0f : d[r];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int cg = c + 8 * g;
-      if (cg >= p.cols) continue;
-      const uint4 uh = *reinterpret_cast<const uint4*>(p.in_hi + at + 8 * g);
-      const uint4 ul = *reinterpret_cast<const uint4*>(p.lo + at + 8 * g);
-      const uint32_t h[4] = {uh.x, uh.y, uh.z, uh.w}, l[4] = {ul.x, ul.y, ul.z, ul.w};
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[2 * j] = half_lo(h[j]) + half_lo(l[j]);
-        x[2 * j + 1] = half_hi(h[j]) + half_hi(l[j]);
-      }
+      float g[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      add_half8(in.hi[it], g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float dj = p.diag_cols ? (cg + j < p.diag_n ? d[cg + j] : 0.0f) : drow;
-        x[j] = fmaf(p.a + dj, x[j], __uint_as_float(v[8 * g + j]) * (1.0f / kSb));
+        x[j] = fmaf(cs, x[j], p.b * g[j]);
+        if (c + j == r) {
+          if (r < p.rows) p.diag[static_cast<long long>(t.mat) * p.diag_n + r] = x[j] * (1.0f / kSb);
+          x[j] = 0.0f;
+        }
+      }
+      if (inside) store_half8(p.out_hi + at, x);
+      if (mirror) {
+        chunk_quad(ws, rr, quad) = make_float4(x[0], x[1], x[2], x[3]);
+        chunk_quad(ws, rr, quad + 1) = make_float4(x[4], x[5], x[6], x[7]);
+      }
+    } else {
+      float g[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      add_half8(in.hi[it], g);
+      add_half8(in.lo[it], g);
+      if (p.diag_cols) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float dj = c + j < p.diag_n ? __ldg(d + c + j) : 0.0f;
+          x[j] = fmaf(p.a + dj, g[j], x[j] * (1.0f / kSb));
+        }
+      } else {
+        const float f = p.a + (r < p.rows ? __ldg(d + r) : 0.0f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = fmaf(f, g[j], x[j] * (1.0f / kSb));
       }
       if constexpr (KIND == kApply) {
-        store_hi_lo(p.out_hi + at + 8 * g, p.lo + at + 8 * g, x);
+        if (inside) store_hi_lo(p.out_hi + at, p.lo + at, x);
+      } else if (p.ucols % 8 == 0) {
+        if (inside && c < p.ucols) put_update8(p, (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + c, x);
       } else {
-        const long long u = (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + cg;
-        if (p.o16) {
-          if (p.ucols % 8 == 0) {
-            *reinterpret_cast<uint4*>(p.o16 + u) =
-                make_uint4(pack_bf16x2(x[0] / kSx, x[1] / kSx), pack_bf16x2(x[2] / kSx, x[3] / kSx),
-                           pack_bf16x2(x[4] / kSx, x[5] / kSx), pack_bf16x2(x[6] / kSx, x[7] / kSx));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (cg + j < p.ucols) p.o16[u + j] = __float2bfloat16_rn(x[j] / kSx);
-          }
-        } else {
-          const float rate = p.rate / kSx;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (cg + j >= p.ucols) continue;
-            float w;
-            if (p.weight_f32) {
-              float* q = static_cast<float*>(p.weight) + u + j;
-              w = fmaf(p.decay, *q, -rate * x[j]);
-              *q = w;
-            } else {
-              __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.weight) + u + j;
-              w = fmaf(p.decay, __bfloat162float(*q), -rate * x[j]);
-              *q = __float2bfloat16_rn(w);
-            }
-            if (p.w16) p.w16[u + j] = __float2bfloat16_rn(w);
-          }
-        }
+        chunk_quad(ws, rr, quad) = make_float4(x[0], x[1], x[2], x[3]);
+        chunk_quad(ws, rr, quad + 1) = make_float4(x[4], x[5], x[6], x[7]);
       }
     }
   }
+  if (KIND == kFinal && p.ucols % 8 != 0) {   // rows that no vector divides: a lane a column
+    __syncwarp();
+    const int cc = c0 + lane;
+#pragma unroll 4
+    for (int rr = 0; rr < 32; ++rr) {
+      const int r = r0 + rr;
+      if (r < p.rows && cc < p.ucols)
+        put_update1(p, (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + cc, ws[chunk_at(rr, lane)]);
+    }
+  }
+  if (mirror) {   // rows c0 .. c0 + 31 of the image, columns r0 .. r0 + 31
+    __syncwarp();
+    const int col = r0 + (lane & 3) * 8;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int rr = it * 8 + (lane >> 2), r = c0 + rr;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = ws[chunk_at((lane & 3) * 8 + j, rr)] * (KIND == kGram ? kSb / (kSx * kSx) : 1.0f);
+      if (r < p.rows && col < p.cols) store_half8(p.out_hi + t.mat * p.mat + r * p.pitch + col, x);
+    }
+  }
+  __syncwarp();   // the chunk has been read
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
@@ -270,12 +350,23 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-template <int KIND>
+// The kernels of a call are launched with programmatic dependence: the next
+// one may set itself up (barriers, tensor memory, tensor maps) while this one
+// runs, and waits here for its results.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <int KIND, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ns_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const NsParams p) {
+  using C = NsCfg<BN>;
+  constexpr int kStages = C::kStages, kStageBytes = C::kStage;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);   // rank 0: both CTAs' operands landed
+  float* turn = reinterpret_cast<float*>(smem + kStages * kStageBytes);   // [8 warps][32 x 32]
+  uint64_t* full = reinterpret_cast<uint64_t*>(turn + kEpiWarps * 1024);   // rank 0: both CTAs' operands landed
   uint64_t* empty = full + kStages;    // the stage's MMAs are done
   uint64_t* tfull = empty + kStages;   // [2] an accumulator is complete
   uint64_t* tempty = tfull + 2;        // [2] rank 0: both CTAs drained it
@@ -302,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc_cg<2>(tmem_slot, 512);
+    tmem_alloc_cg<2>(tmem_slot, 2 * BN);
     tmem_relinquish_cg<2>();
   }
   tc_fence_before();
@@ -310,14 +401,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   cluster_sync();   // the other CTA's barriers exist before anything arrives on them
+  after_previous();
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     uint32_t it = 0;
     bool ok = true;
     for (int tile = cid; ok && tile < p.total; tile += ncl) {
-      const NsTile t = ns_tile<KIND>(p, tile, rank);
-      const int brow = t.col0 + 128 * rank;   // this CTA's half of the N rows
+      const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
+      const int brow = t.col0 + BN / 2 * rank;   // this CTA's half of the N rows
       for (int ks = 0; ks < p.kstages; ++ks, ++it) {
         const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&empty[slot], ph ^ 1, abort_flag, p.err))) {
@@ -331,8 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int k0 = ks * 128;
           if (p.a_mn) tma_load_4d_pair(sa, &tmA, bar, 0, k0, t.row0 >> 6, t.mat);
           else tma_load_4d_pair(sa, &tmA, bar, 0, t.row0, k0 >> 6, t.mat);
-          if (p.b_mn) tma_load_4d_pair(sa + kBoxBytes, &tmB, bar, 0, k0, brow >> 6, t.mat);
-          else tma_load_4d_pair(sa + kBoxBytes, &tmB, bar, 0, brow, k0 >> 6, t.mat);
+          if (p.b_mn) tma_load_4d_pair(sa + C::kA, &tmB, bar, 0, k0, brow >> 6, t.mat);
+          else tma_load_4d_pair(sa + C::kA, &tmB, bar, 0, brow, k0 >> 6, t.mat);
         }
         __syncwarp();
       }
@@ -350,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       // ----------------------------------------------------- MMA issuer
       // FP16 operands (formats 0), FP32 accumulators; bits 15, 16: A, B MN-major
-      const uint32_t idesc = (1u << 4) | ((256u >> 3) << 17) | ((256u >> 4) << 24) | (p.a_mn ? kIdescAMnMajor : 0u) |
+      const uint32_t idesc = (1u << 4) | ((static_cast<uint32_t>(BN) >> 3) << 17) | ((256u >> 4) << 24) | (p.a_mn ? kIdescAMnMajor : 0u) |
                              (p.b_mn ? (1u << 16) : 0u);
       uint32_t it = 0, tc = 0;
       bool ok = true;
@@ -358,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem + acc * 256;
+        const uint32_t d_tmem = tmem + acc * BN;
         for (int ks = 0; ks < p.kstages; ++ks, ++it) {
           const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
           if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&full[slot], ph, abort_flag, p.err))) {
@@ -367,11 +459,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t sa = smem_u32(smem + slot * kStageBytes), sb = sa + kBoxBytes;
+            const uint32_t sa = smem_u32(smem + slot * kStageBytes), sb = sa + C::kA;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {   // 16 contraction elements each
               const uint64_t ad = p.a_mn ? sdesc_mn_f16(sa + j * 2048) : sdesc_k_sw128(sa + (j >> 2) * 16384 + (j & 3) * 32);
-              const uint64_t bd = p.b_mn ? sdesc_mn_f16(sb + j * 2048) : sdesc_k_sw128(sb + (j >> 2) * 16384 + (j & 3) * 32);
+              const uint64_t bd = p.b_mn ? sdesc_mn_f16(sb + j * 2048) : sdesc_k_sw128(sb + (j >> 2) * (C::kB / 2) + (j & 3) * 32);
               mma_bf16_pair(d_tmem, ad, bd, idesc, (ks | j) ? 1u : 0u);
             }
             tc_commit_pair_mc(&empty[slot], 3);
@@ -391,41 +483,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // --------------------------------------------------------- epilogue
     const int q = warp & 3, h = (warp - 2) >> 2;
+    constexpr int kChunks = BN / 64;     // of 32 columns, per warp
+    float* ws = turn + (warp - 2) * 1024;
     const uint32_t tempty0 = cluster_addr(tempty, 0);
     uint32_t tc = 0;
     for (int tile = cid; tile < p.total; tile += ncl, ++tc) {
-      const NsTile t = ns_tile<KIND>(p, tile, rank);
+      const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
       const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+      const int r0 = t.row0 + q * 32, cw = t.col0 + BN / 2 * h;
+      ChunkIn in;
+      load_chunk_in<KIND>(p, t, r0, cw, lane, in);
       if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
       tc_fence_after();
-      const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + 128 * h;
-      const int r = t.row0 + q * 32 + lane, c = t.col0 + 128 * h;
-      // a symmetric tile's block below the diagonal is its mirror's
-      const bool skip = (KIND == kGram || KIND == kPoly) && (c >> 7) < (t.row0 >> 7);
+      const uint32_t tbase = tmem + acc * BN + (static_cast<uint32_t>(q * 32) << 16) + BN / 2 * h;
 #pragma unroll 1
-      for (int ci = 0; ci < 4; ++ci) {
-        if (skip || c + 32 * ci >= p.cols) continue;
-        uint32_t v[32];
-        tmem_ld32(tbase + 32 * ci, v);
-        tmem_ld_wait();
-        ns_chunk<KIND>(p, t, r, c + 32 * ci, v);
+      for (int ci = 0; ci < kChunks; ++ci) {
+        const int c0 = cw + 32 * ci;
+        // a symmetric output's blocks below the diagonal are their mirrors'
+        const bool skip = c0 >= p.cols || ((KIND == kGram || KIND == kPoly) && (c0 >> 7) < (t.row0 >> 7));
+        if (!skip) {
+          uint32_t v[32];
+          tmem_ld32(tbase + 32 * ci, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            chunk_quad(ws, lane, j) = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                                  __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+        }
+        if (ci == kChunks - 1) {   // every column has been read: the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
+        }
+        if (!skip) {
+          __syncwarp();
+          const ChunkIn now = in;
+          if (ci + 1 < kChunks) load_chunk_in<KIND>(p, t, r0, c0 + 32, lane, in);
+          ns_chunk<KIND>(p, t, r0, c0, lane, ws, now);
+        } else if (ci + 1 < kChunks) {
+          load_chunk_in<KIND>(p, t, r0, c0 + 32, lane, in);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   cluster_sync();
-  if (warp == 1) tmem_dealloc_cg<2>(tmem, 512);
+  if (warp == 1) tmem_dealloc_cg<2>(tmem, 2 * BN);
 }
 
 // ---------------------------------------------------- momentum and start
 
 constexpr int kMixThreads = 256;
-constexpr int kMixBlocks = 64;   // blocks (and partial sums) per matrix at most
+constexpr int kMixBlocks = 128;   // blocks (and partial sums) per matrix at most
 
 struct MixParams {
   const void* grad;        // matrices [rows, cols], contiguous
@@ -441,33 +552,63 @@ struct MixParams {
   long long pitch, mat;    // stored X
 };
 
-__device__ __forceinline__ float grad_at(const MixParams& p, long long i) {
-  return p.grad_f32 ? static_cast<const float*>(p.grad)[i]
-                    : __bfloat162float(static_cast<const __nv_bfloat16*>(p.grad)[i]);
+// N values of the gradient from element i (N = 8: 16-byte aligned).
+template <int N>
+__device__ __forceinline__ void grad_at(const MixParams& p, long long i, float (&v)[N]) {
+  if constexpr (N == 8) {
+    if (p.grad_f32) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.grad) + i);
+      const float4 a = __ldg(q), b = __ldg(q + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.grad) + i));
+      v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+      v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+    }
+  } else {
+    v[0] = p.grad_f32 ? static_cast<const float*>(p.grad)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.grad)[i]);
+  }
 }
-
-__device__ __forceinline__ float update_at(const MixParams& p, long long i, float m) {
-  const float g = grad_at(p, i);
-  return p.momentum ? (p.nesterov ? fmaf(p.mu, m, g) : m) : g;
+template <int N>
+__device__ __forceinline__ void momentum_at(const float* p, float (&v)[N]) {
+  if constexpr (N == 8) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    v[0] = *p;
+  }
 }
 
 // M <- mu M + G and the squares of U = G + mu M (or M): one partial sum a
-// block, rows dealt to the blocks in turn.
+// block over its share of the matrix's elements, taken N at a time.
+template <int N>
 __global__ void __launch_bounds__(kMixThreads) muon_mix_kernel(const MixParams p) {
   __shared__ float red[kMixThreads / 32];
-  const long long base = static_cast<long long>(blockIdx.y) * p.rows * p.cols;
+  const long long elems = static_cast<long long>(p.rows) * p.cols, base = blockIdx.y * elems;
   float s = 0.0f;
-  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
-    const long long row = base + static_cast<long long>(r) * p.cols;
-    for (int c = threadIdx.x; c < p.cols; c += kMixThreads) {
-      float m = 0.0f;
-      if (p.momentum) {
-        m = fmaf(p.mu, p.momentum[row + c], grad_at(p, row + c));
-        p.momentum[row + c] = m;
+#pragma unroll 4
+  for (long long i = (static_cast<long long>(blockIdx.x) * kMixThreads + threadIdx.x) * N; i < elems;
+       i += static_cast<long long>(gridDim.x) * kMixThreads * N) {
+    float u[N];
+    grad_at<N>(p, base + i, u);
+    if (p.momentum) {
+      float m[N];
+      momentum_at<N>(p.momentum + base + i, m);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        m[j] = fmaf(p.mu, m[j], u[j]);
+        u[j] = p.nesterov ? fmaf(p.mu, m[j], u[j]) : m[j];
       }
-      const float u = update_at(p, row + c, m);
-      s = fmaf(u, u, s);
+      float* o = p.momentum + base + i;
+      if constexpr (N == 8) {
+        reinterpret_cast<float4*>(o)[0] = make_float4(m[0], m[1], m[2], m[3]);
+        reinterpret_cast<float4*>(o)[1] = make_float4(m[4], m[5], m[6], m[7]);
+      } else {
+        *o = m[0];
+      }
     }
+#pragma unroll
+    for (int j = 0; j < N; ++j) s = fmaf(u[j], u[j], s);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -477,27 +618,53 @@ __global__ void __launch_bounds__(kMixThreads) muon_mix_kernel(const MixParams p
     for (int w = 1; w < kMixThreads / 32; ++w) s += red[w];
     p.partial[static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x] = s;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// X = U / (|U| + eps) as stored halves, zeros in the row padding.
+// X = U / (|U| + eps) as stored halves, zeros in the row padding.  N = 8: cols
+// % 8 == 0; else a thread takes single columns.
+template <int N>
 __global__ void __launch_bounds__(kMixThreads) muon_start_kernel(const MixParams p, int parts) {
+  __shared__ float red[kMixThreads / 32];
+  after_previous();
   const float* part = p.partial + static_cast<long long>(blockIdx.y) * parts;
-  float s = 0.0f;
-  for (int i = 0; i < parts; ++i) s += part[i];
+  float s = threadIdx.x < parts ? part[threadIdx.x] : 0.0f;   // parts <= 128
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = (red[0] + red[1]) + (red[2] + red[3]);
   const float f = kSx / (sqrtf(s) + p.eps);
   const long long base = static_cast<long long>(blockIdx.y) * p.rows * p.cols;
-  const int groups = static_cast<int>(p.pitch >> 3);
-  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
-    const long long row = base + static_cast<long long>(r) * p.cols;
-    const long long out = blockIdx.y * p.mat + r * p.pitch;
-    for (int g = threadIdx.x; g < groups; g += kMixThreads) {
-      float v[8];
+  const int groups = static_cast<int>(p.pitch / N);
+  // (row, group) pairs of the matrix, dealt to all its threads
+  const long long all = static_cast<long long>(p.rows) * groups;
+#pragma unroll 2
+  for (long long k = static_cast<long long>(blockIdx.x) * kMixThreads + threadIdx.x; k < all;
+       k += static_cast<long long>(gridDim.x) * kMixThreads) {
+    const int r = static_cast<int>(k / groups), c = static_cast<int>(k - static_cast<long long>(r) * groups) * N;
+    const long long at = base + static_cast<long long>(r) * p.cols + c, out = blockIdx.y * p.mat + r * p.pitch + c;
+    float u[N];
+    if (c < p.cols) {
+      grad_at<N>(p, at, u);
+      if (p.momentum) {
+        float m[N];
+        momentum_at<N>(p.momentum + at, m);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = 8 * g + j;
-        v[j] = c < p.cols ? f * update_at(p, row + c, p.momentum ? p.momentum[row + c] : 0.0f) : 0.0f;
+        for (int j = 0; j < N; ++j) u[j] = p.nesterov ? fmaf(p.mu, m[j], u[j]) : m[j];
       }
-      store_hi_lo(p.hi + out + 8 * g, p.lo + out + 8 * g, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) u[j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) u[j] *= f;
+    if constexpr (N == 8) {
+      store_hi_lo(p.hi + out, p.lo + out, u);
+    } else {
+      const __half hi = __float2half_rn(u[0]);
+      p.hi[out] = hi;
+      p.lo[out] = __float2half_rn(u[0] - __half2float(hi));
     }
   }
 }
@@ -543,24 +710,55 @@ bool muon_config_ok(const moe_muon_config* c) {
 // A CTA pair's matrix sizes: box coordinates and chunk counts are ints.
 bool muon_size_ok(const moe_muon_config* c) { return c->rows <= 65536 && c->cols <= 65536; }
 
-bool map_of(CUtensorMap* tm, const void* base, long long pitch, int rows, int mats) {
+// Boxes of two (MN-major B of narrow tiles: one) 64-column chunks of `box_rows` rows.
+bool map_of(CUtensorMap* tm, const void* base, long long pitch, int rows, int mats, int box_rows, int chunks) {
   const cuuint64_t d[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(pitch / 64),
                            static_cast<cuuint64_t>(mats)};
   const cuuint64_t st[3] = {static_cast<cuuint64_t>(pitch) * 2, 128, static_cast<cuuint64_t>(pitch) * rows * 2};
-  const cuuint32_t bx[4] = {64, 128, 2, 1};
+  const cuuint32_t bx[4] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(chunks), 1};
   return make_tmap_nd(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, d, st, bx, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int KIND>
+cudaError_t launch_next(const void* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, void** args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <int KIND, int BN>
 cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const NsParams& p, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
+  const void* kernel = reinterpret_cast<const void*>(ns_kernel<KIND, BN>);
   cudaError_t e = once.once(
-      [] { return cudaFuncSetAttribute(ns_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+      [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NsCfg<BN>::kSmem); });
   if (e != cudaSuccess) return e;
-  int pairs = sms / 2;
-  if (p.total < pairs) pairs = p.total;
-  ns_kernel<KIND><<<2 * pairs, kThreads, kSmem, stream>>>(a, b, p);
-  return cudaGetLastError();
+  void* args[3] = {const_cast<CUtensorMap*>(&a), const_cast<CUtensorMap*>(&b), const_cast<NsParams*>(&p)};
+  return launch_next(kernel, dim3(2 * std::min(sms / 2, p.total)), kThreads, NsCfg<BN>::kSmem, stream, args);
+}
+
+// Tiles of a product: 256 columns wide, or 128 where that leaves CTA pairs idle.
+template <int KIND>
+cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap (&b)[2], NsParams p, int mats, int out_rows,
+                         int out_cols, int sms, cudaStream_t stream) {
+  constexpr bool sym = KIND == kGram || KIND == kPoly;
+  auto count = [&](int bn) {
+    p.col_tiles = (out_cols + bn - 1) / bn;
+    const int q = (out_rows + 255) / 256, per = 256 / bn;
+    p.tiles = q * p.col_tiles - (sym ? per * (q * (q - 1) / 2) : 0);
+    p.total = p.tiles * mats;
+  };
+  count(256);
+  if (p.total > sms / 4) return launch_ns<KIND, 256>(a, b[0], p, sms, stream);
+  count(128);
+  return launch_ns<KIND, 128>(a, b[1], p, sms, stream);
 }
 
 // What the last product writes and the first kernels read.
@@ -609,10 +807,22 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
   float* diag = reinterpret_cast<float*>(take(sizeof(float) * L.m * chunk));
   float* partial = reinterpret_cast<float*>(take(sizeof(float) * kMixBlocks * chunk));
 
-  CUtensorMap tx[2], ta, tb;
-  if (!map_of(&tx[0], hi[0], L.pitch_x, c->rows, chunk) || !map_of(&tx[1], hi[1], L.pitch_x, c->rows, chunk) ||
-      !map_of(&ta, A, L.pitch_a, L.m, chunk) || !map_of(&tb, B, L.pitch_a, L.m, chunk))
-    return MOE_ERR_CUDA;
+  // tensor maps of X (both buffers), A and B: as the A operand, and as the B
+  // operand of 256- and 128-column tiles (B's rows, or X's columns if wide)
+  CUtensorMap xa[2], xb[2][2], aa, ab[2], ba, bb[2];
+  bool ok = map_of(&aa, A, L.pitch_a, L.m, chunk, 128, 2) && map_of(&ba, B, L.pitch_a, L.m, chunk, 128, 2);
+  for (int i = 0; i < 2; ++i) {
+    ok = ok && map_of(&xa[i], hi[i], L.pitch_x, c->rows, chunk, 128, 2);
+    for (int n = 0; n < 2; ++n) {
+      // K-major: BN / 2 rows; MN-major: 128 contraction rows of BN / 2 columns
+      ok = ok && map_of(&xb[i][n], hi[i], L.pitch_x, c->rows, chunk, 128, 2 - n);
+    }
+    ok = ok && map_of(&ab[i], A, L.pitch_a, L.m, chunk, 128 >> i, 2) && map_of(&bb[i], B, L.pitch_a, L.m, chunk, 128 >> i, 2);
+  }
+  CUtensorMap xk[2][2];   // wide: X as the K-major B operand of its own Gram matrix
+  for (int i = 0; i < 2; ++i)
+    for (int n = 0; n < 2; ++n) ok = ok && map_of(&xk[i][n], hi[i], L.pitch_x, c->rows, chunk, 128 >> n, 2);
+  if (!ok) return MOE_ERR_CUDA;
 
   const long long elems = static_cast<long long>(c->rows) * c->cols;
   for (int e0 = 0; e0 < c->batch; e0 += chunk) {
@@ -632,20 +842,24 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
     mp.lo = lo;
     mp.pitch = L.pitch_x;
     mp.mat = L.mat_x;
-    const int parts = std::min(kMixBlocks, c->rows);
-    muon_mix_kernel<<<dim3(parts, n), kMixThreads, 0, stream>>>(mp);
+    const bool vec = elems % 8 == 0, vec_rows = c->cols % 8 == 0;
+    const int parts = static_cast<int>(std::min<long long>(kMixBlocks, (elems + 8 * kMixThreads - 1) / (8 * kMixThreads)));
+    if (vec) muon_mix_kernel<8><<<dim3(parts, n), kMixThreads, 0, stream>>>(mp);
+    else muon_mix_kernel<1><<<dim3(parts, n), kMixThreads, 0, stream>>>(mp);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    muon_start_kernel<<<dim3(std::min(c->rows, 1024), n), kMixThreads, 0, stream>>>(mp, parts);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    int parts_arg = parts;
+    void* sargs[2] = {&mp, &parts_arg};
+    const long long pieces = L.mat_x / (vec_rows ? 8 : 1);
+    const dim3 sgrid(static_cast<unsigned>(std::min<long long>(1024, (pieces + kMixThreads - 1) / kMixThreads)), n);
+    if (launch_next(vec_rows ? reinterpret_cast<const void*>(muon_start_kernel<8>) : reinterpret_cast<const void*>(muon_start_kernel<1>),
+                    sgrid, kMixThreads, 0, stream, sargs) != cudaSuccess)
+      return MOE_ERR_CUDA;
 
     for (int s = 0; s < c->steps; ++s) {
       const int cur = s & 1;
       const float* co = c->coefficients[s];
       NsParams p{};
       p.err = err;
-      p.n256 = (L.m + 255) / 256;
-      p.tiles = p.n256 * (p.n256 + 1) / 2;
-      p.total = p.tiles * n;
       p.rows = L.m;
       p.cols = static_cast<int>(L.pitch_a);
       p.pitch = L.pitch_a;
@@ -658,28 +872,26 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
       p.a_mn = p.b_mn = L.tall;
       p.kstages = (L.k + 127) / 128;
       p.out_hi = A;
-      if (launch_ns<kGram>(tx[cur], tx[cur], p, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+      if (launch_tiles<kGram>(xa[cur], L.tall ? xb[cur] : xk[cur], p, n, L.m, L.m, sms, stream) != cudaSuccess)
+        return MOE_ERR_CUDA;
       p.a_mn = p.b_mn = 0;
       p.kstages = (L.m + 127) / 128;
       p.in_hi = A;
       p.out_hi = B;
-      if (launch_ns<kPoly>(ta, ta, p, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+      if (launch_tiles<kPoly>(aa, ab, p, n, L.m, L.m, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
       p.rows = c->rows;
       p.cols = static_cast<int>(L.pitch_x);
       p.pitch = L.pitch_x;
       p.mat = L.mat_x;
-      p.col_tiles = (c->cols + 255) / 256;
-      p.tiles = (c->rows + 255) / 256 * p.col_tiles;
-      p.total = p.tiles * n;
       p.in_hi = hi[cur];
       p.out_hi = hi[cur ^ 1];
       p.lo = lo;
       p.diag_cols = L.tall;
       p.b_mn = !L.tall;
-      const CUtensorMap& opa = L.tall ? tx[cur] : tb;
-      const CUtensorMap& opb = L.tall ? tb : tx[cur];
+      const CUtensorMap& opa = L.tall ? xa[cur] : ba;
+      const CUtensorMap (&opb)[2] = L.tall ? bb : xb[cur];
       if (s + 1 < c->steps) {
-        if (launch_ns<kApply>(opa, opb, p, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch_tiles<kApply>(opa, opb, p, n, c->rows, c->cols, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
       } else {
         p.ucols = c->cols;
         if (io.o16) p.o16 = io.o16 + u0;
@@ -688,7 +900,7 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
         p.w16 = io.w16 ? io.w16 + u0 : nullptr;
         p.decay = io.decay;
         p.rate = io.rate;
-        if (launch_ns<kFinal>(opa, opb, p, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch_tiles<kFinal>(opa, opb, p, n, c->rows, c->cols, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
       }
     }
   }
