@@ -68,20 +68,23 @@ struct NsCfg {
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
-enum NsKind { kGram, kPoly, kApply, kFinal };
+enum NsKind { kGram, kPoly, kApply, kFinal, kUpdate };   // the last apply: BF16 result, or weight update
 
 struct NsParams {
   int tiles;            // per matrix
   int total;            // tiles of all matrices
   int col_tiles;        // BN-column tiles of the output
   int kstages;          // stages of 128 contraction elements
+  int split;            // apply: a second round over them reads X's lo half
   int a_mn, b_mn;       // operand read MN-major
-  int rows, cols;       // valid rows, columns written (a multiple of 8)
+  int rows, cols;       // valid rows, columns written (a multiple of 64)
+  int valid_cols;
   long long pitch;      // elements per stored row (multiple of 64)
   long long mat;        // elements per stored matrix
   const __half* in_hi;  // poly: A; apply: X hi
   __half* out_hi;       // gram: A; poly: B; apply: X hi (next)
-  __half* lo;           // apply: X lo, in place
+  const __half* in_lo;  // apply: X lo
+  __half* out_lo;       // and where the new one goes (in place unless split)
   float* diag;          // [matrix][diag_n]: B's diagonal
   int diag_n;
   int diag_cols;        // apply: the diagonal scales columns (tall) or rows (wide)
@@ -121,7 +124,8 @@ __device__ __forceinline__ uint64_t sdesc_mn_f16(uint32_t saddr) {
 }
 
 struct NsTile {
-  int mat, row0, col0;   // this CTA's 128 output rows, the pair's BN columns
+  int mat, row0, col0;   // this CTA's 128 output rows, the pair's columns
+  int n;                 // columns of the product: BN, or 128 where a last tile needs no more
 };
 
 // Symmetric outputs: row q of 256 rows has the column tiles from its first
@@ -141,6 +145,7 @@ __device__ __forceinline__ NsTile ns_tile(const NsParams& p, int tile, int rank)
   }
   t.row0 = q * 256 + 128 * rank;
   t.col0 = i * BN;
+  t.n = (BN == 256 && p.valid_cols - t.col0 <= 128) ? 128 : BN;
   return t;
 }
 
@@ -184,37 +189,33 @@ __device__ __forceinline__ void add_half8(const uint4& u, float (&x)[8]) {
   }
 }
 
-// 8 values of the caller's output tensors at row r, columns c .. c + 7 (x:
-// the new X, stored scale).  ucols % 8 == 0: 16-byte accesses.
-__device__ __forceinline__ void put_update8(const NsParams& p, long long u, const float (&x)[8]) {
-  if (p.o16) {
-    constexpr float s = 1.0f / kSx;
-    *reinterpret_cast<uint4*>(p.o16 + u) = make_uint4(pack_bf16x2(x[0] * s, x[1] * s), pack_bf16x2(x[2] * s, x[3] * s),
-                                                      pack_bf16x2(x[4] * s, x[5] * s), pack_bf16x2(x[6] * s, x[7] * s));
-    return;
-  }
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8], float s) {
+  return make_uint4(pack_bf16x2(x[0] * s, x[1] * s), pack_bf16x2(x[2] * s, x[3] * s), pack_bf16x2(x[4] * s, x[5] * s),
+                    pack_bf16x2(x[6] * s, x[7] * s));
+}
+
+// 8 values of the caller's weight from element u (x: the new X, stored
+// scale; w4: the weight there).  16-byte accesses.
+__device__ __forceinline__ void put_weight8(const NsParams& p, long long u, const float (&x)[8], const uint4 (&w4)[2]) {
   const float rate = -p.rate * (1.0f / kSx);
   float w[8];
   if (p.weight_f32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.weight) + u);
-    const float4 a = q[0], b = q[1];
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    const uint32_t q[8] = {w4[0].x, w4[0].y, w4[0].z, w4[0].w, w4[1].x, w4[1].y, w4[1].z, w4[1].w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = fmaf(p.decay, w[j], rate * x[j]);
-    q[0] = make_float4(w[0], w[1], w[2], w[3]);
-    q[1] = make_float4(w[4], w[5], w[6], w[7]);
+    for (int j = 0; j < 8; ++j) w[j] = fmaf(p.decay, __uint_as_float(q[j]), rate * x[j]);
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.weight) + u);
+    o[0] = make_float4(w[0], w[1], w[2], w[3]);
+    o[1] = make_float4(w[4], w[5], w[6], w[7]);
+    if (p.w16) *reinterpret_cast<uint4*>(p.w16 + u) = pack_bf16x8(w, 1.0f);
   } else {
-    uint4* q = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.weight) + u);
-    const uint4 a = *q;
-    w[0] = bf16_lo(a.x), w[1] = bf16_hi(a.x), w[2] = bf16_lo(a.y), w[3] = bf16_hi(a.y);
-    w[4] = bf16_lo(a.z), w[5] = bf16_hi(a.z), w[6] = bf16_lo(a.w), w[7] = bf16_hi(a.w);
+    const uint32_t q[4] = {w4[0].x, w4[0].y, w4[0].z, w4[0].w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = fmaf(p.decay, w[j], rate * x[j]);
-    *q = make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
+    for (int j = 0; j < 4; ++j) {
+      w[2 * j] = fmaf(p.decay, bf16_lo(q[j]), rate * x[2 * j]);
+      w[2 * j + 1] = fmaf(p.decay, bf16_hi(q[j]), rate * x[2 * j + 1]);
+    }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.weight) + u) = pack_bf16x8(w, 1.0f);
   }
-  if (p.w16)
-    *reinterpret_cast<uint4*>(p.w16 + u) =
-        make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
 }
 __device__ __forceinline__ void put_update1(const NsParams& p, long long u, float x) {
   if (p.o16) {
@@ -236,12 +237,14 @@ __device__ __forceinline__ void put_update1(const NsParams& p, long long u, floa
 }
 
 // What a chunk needs besides the accumulator: 8 columns of rows lane / 4 + 8 it.
+template <int KIND>
 struct ChunkIn {
   uint4 hi[4], lo[4];
+  uint4 w[KIND == kUpdate ? 4 : 1][2];   // the weight (rows that vectors divide)
 };
 
 template <int KIND>
-__device__ __forceinline__ void load_chunk_in(const NsParams& p, const NsTile& t, int r0, int c0, int lane, ChunkIn& in) {
+__device__ __forceinline__ void load_chunk_in(const NsParams& p, const NsTile& t, int r0, int c0, int lane, ChunkIn<KIND>& in) {
   if constexpr (KIND == kGram) return;
   const int c = c0 + (lane & 3) * 8;
 #pragma unroll
@@ -251,7 +254,18 @@ __device__ __forceinline__ void load_chunk_in(const NsParams& p, const NsTile& t
     if (r < p.rows && c < p.cols) {
       const long long at = t.mat * p.mat + r * p.pitch + c;
       in.hi[it] = *reinterpret_cast<const uint4*>(p.in_hi + at);
-      if constexpr (KIND == kApply || KIND == kFinal) in.lo[it] = *reinterpret_cast<const uint4*>(p.lo + at);
+      if constexpr (KIND >= kApply) in.lo[it] = *reinterpret_cast<const uint4*>(p.in_lo + at);
+    }
+    if constexpr (KIND == kUpdate) {
+      if (p.ucols % 8 == 0 && r < p.rows && c < p.ucols) {
+        const long long u = (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + c;
+        if (p.weight_f32) {
+          in.w[it][0] = reinterpret_cast<const uint4*>(static_cast<const float*>(p.weight) + u)[0];
+          in.w[it][1] = reinterpret_cast<const uint4*>(static_cast<const float*>(p.weight) + u)[1];
+        } else {
+          in.w[it][0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.weight) + u);
+        }
+      }
     }
   }
 }
@@ -261,7 +275,7 @@ __device__ __forceinline__ void load_chunk_in(const NsParams& p, const NsTile& t
 // warp cover whole 64-byte (FP16) or 128-byte (FP32) pieces of rows.
 template <int KIND>
 __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int r0, int c0, int lane, float* ws,
-                                         const ChunkIn& in) {
+                                         const ChunkIn<KIND>& in) {
   const int quad = (lane & 3) * 2, c = c0 + (lane & 3) * 8;
   const float* d = p.diag + static_cast<long long>(t.mat) * p.diag_n;
   const bool mirror = (KIND == kGram || KIND == kPoly) && (c0 >> 7) > (r0 >> 7);
@@ -309,16 +323,20 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int
         for (int j = 0; j < 8; ++j) x[j] = fmaf(f, g[j], x[j] * (1.0f / kSb));
       }
       if constexpr (KIND == kApply) {
-        if (inside) store_hi_lo(p.out_hi + at, p.lo + at, x);
+        if (inside) store_hi_lo(p.out_hi + at, p.out_lo + at, x);
       } else if (p.ucols % 8 == 0) {
-        if (inside && c < p.ucols) put_update8(p, (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + c, x);
+        if (inside && c < p.ucols) {
+          const long long u = (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + c;
+          if constexpr (KIND == kFinal) *reinterpret_cast<uint4*>(p.o16 + u) = pack_bf16x8(x, 1.0f / kSx);
+          else put_weight8(p, u, x, in.w[it]);
+        }
       } else {
         chunk_quad(ws, rr, quad) = make_float4(x[0], x[1], x[2], x[3]);
         chunk_quad(ws, rr, quad + 1) = make_float4(x[4], x[5], x[6], x[7]);
       }
     }
   }
-  if (KIND == kFinal && p.ucols % 8 != 0) {   // rows that no vector divides: a lane a column
+  if (KIND >= kFinal && p.ucols % 8 != 0) {   // rows that no vector divides: a lane a column
     __syncwarp();
     const int cc = c0 + lane;
 #pragma unroll 4
@@ -360,7 +378,8 @@ __device__ __forceinline__ void after_previous() {
 
 template <int KIND, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    ns_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const NsParams p) {
+    ns_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ CUtensorMap tmLo, const NsParams p) {
   using C = NsCfg<BN>;
   constexpr int kStages = C::kStages, kStageBytes = C::kStage;
   extern __shared__ uint8_t smem_raw[];
@@ -409,8 +428,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int tile = cid; ok && tile < p.total; tile += ncl) {
       const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
-      const int brow = t.col0 + BN / 2 * rank;   // this CTA's half of the N rows
-      for (int ks = 0; ks < p.kstages; ++ks, ++it) {
+      const int brow = t.col0 + t.n / 2 * rank;   // this CTA's half of the N rows
+      const int ks_all = p.split ? 2 * p.kstages : p.kstages;
+      for (int ks = 0; ks < ks_all; ++ks, ++it) {
         const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&empty[slot], ph ^ 1, abort_flag, p.err))) {
           ok = false;
@@ -420,11 +440,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint8_t* sa = smem + slot * kStageBytes;
           const uint32_t bar = cluster_addr(&full[slot], 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * kStageBytes);
-          const int k0 = ks * 128;
-          if (p.a_mn) tma_load_4d_pair(sa, &tmA, bar, 0, k0, t.row0 >> 6, t.mat);
-          else tma_load_4d_pair(sa, &tmA, bar, 0, t.row0, k0 >> 6, t.mat);
-          if (p.b_mn) tma_load_4d_pair(sa + C::kA, &tmB, bar, 0, k0, brow >> 6, t.mat);
-          else tma_load_4d_pair(sa + C::kA, &tmB, bar, 0, brow, k0 >> 6, t.mat);
+          const bool low = ks >= p.kstages;   // X, the A operand if tall, is its lo half
+          const int k0 = (low ? ks - p.kstages : ks) * 128;
+          const CUtensorMap* ta = low && p.diag_cols ? &tmLo : &tmA;
+          const CUtensorMap* tb = low && !p.diag_cols ? &tmLo : &tmB;
+          if (p.a_mn) tma_load_4d_pair(sa, ta, bar, 0, k0, t.row0 >> 6, t.mat);
+          else tma_load_4d_pair(sa, ta, bar, 0, t.row0, k0 >> 6, t.mat);
+          if (p.b_mn) tma_load_4d_pair(sa + C::kA, tb, bar, 0, k0, brow >> 6, t.mat);
+          else tma_load_4d_pair(sa + C::kA, tb, bar, 0, brow, k0 >> 6, t.mat);
         }
         __syncwarp();
       }
@@ -442,16 +465,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       // ----------------------------------------------------- MMA issuer
       // FP16 operands (formats 0), FP32 accumulators; bits 15, 16: A, B MN-major
-      const uint32_t idesc = (1u << 4) | ((static_cast<uint32_t>(BN) >> 3) << 17) | ((256u >> 4) << 24) | (p.a_mn ? kIdescAMnMajor : 0u) |
-                             (p.b_mn ? (1u << 16) : 0u);
+      const uint32_t idesc0 = (1u << 4) | ((256u >> 4) << 24) | (p.a_mn ? kIdescAMnMajor : 0u) | (p.b_mn ? (1u << 16) : 0u);
       uint32_t it = 0, tc = 0;
       bool ok = true;
       for (int tile = cid; ok && tile < p.total; tile += ncl, ++tc) {
+        const uint32_t idesc = idesc0 | ((static_cast<uint32_t>(ns_tile<KIND, BN>(p, tile, rank).n) >> 3) << 17);
         const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + acc * BN;
-        for (int ks = 0; ks < p.kstages; ++ks, ++it) {
+        const int ks_all = p.split ? 2 * p.kstages : p.kstages;
+        for (int ks = 0; ks < ks_all; ++ks, ++it) {
           const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
           if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&full[slot], ph, abort_flag, p.err))) {
             ok = false;
@@ -491,7 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
       const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
       const int r0 = t.row0 + q * 32, cw = t.col0 + BN / 2 * h;
-      ChunkIn in;
+      ChunkIn<KIND> in;
       load_chunk_in<KIND>(p, t, r0, cw, lane, in);
       if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
       tc_fence_after();
@@ -517,7 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!skip) {
           __syncwarp();
-          const ChunkIn now = in;
+          const ChunkIn<KIND> now = in;
           if (ci + 1 < kChunks) load_chunk_in<KIND>(p, t, r0, c0 + 32, lane, in);
           ns_chunk<KIND>(p, t, r0, c0, lane, ws, now);
         } else if (ci + 1 < kChunks) {
@@ -536,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------- momentum and start
 
 constexpr int kMixThreads = 256;
-constexpr int kMixBlocks = 128;   // blocks (and partial sums) per matrix at most
+constexpr int kMixBlocks = 256;   // blocks (and partial sums) per matrix at most
 
 struct MixParams {
   const void* grad;        // matrices [rows, cols], contiguous
@@ -579,36 +603,49 @@ __device__ __forceinline__ void momentum_at(const float* p, float (&v)[N]) {
   }
 }
 
-// M <- mu M + G and the squares of U = G + mu M (or M): one partial sum a
-// block over its share of the matrix's elements, taken N at a time.
-template <int N>
+// M <- mu M + G and the squares of U = G + mu M (or M), M: there is a
+// momentum; one partial sum a block over its share of the matrix's elements, N
+// at a time, a few of them in flight.
+template <int N, bool M>
 __global__ void __launch_bounds__(kMixThreads) muon_mix_kernel(const MixParams p) {
+  constexpr int kBatch = M ? 2 : 4;
   __shared__ float red[kMixThreads / 32];
   const long long elems = static_cast<long long>(p.rows) * p.cols, base = blockIdx.y * elems;
+  const long long hop = static_cast<long long>(gridDim.x) * kMixThreads * N;
   float s = 0.0f;
-#pragma unroll 4
-  for (long long i = (static_cast<long long>(blockIdx.x) * kMixThreads + threadIdx.x) * N; i < elems;
-       i += static_cast<long long>(gridDim.x) * kMixThreads * N) {
-    float u[N];
-    grad_at<N>(p, base + i, u);
-    if (p.momentum) {
-      float m[N];
-      momentum_at<N>(p.momentum + base + i, m);
+  for (long long i0 = (static_cast<long long>(blockIdx.x) * kMixThreads + threadIdx.x) * N; i0 < elems; i0 += kBatch * hop) {
+    float u[kBatch][N], m[M ? kBatch : 1][N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        m[j] = fmaf(p.mu, m[j], u[j]);
-        u[j] = p.nesterov ? fmaf(p.mu, m[j], u[j]) : m[j];
-      }
-      float* o = p.momentum + base + i;
-      if constexpr (N == 8) {
-        reinterpret_cast<float4*>(o)[0] = make_float4(m[0], m[1], m[2], m[3]);
-        reinterpret_cast<float4*>(o)[1] = make_float4(m[4], m[5], m[6], m[7]);
-      } else {
-        *o = m[0];
+    for (int k = 0; k < kBatch; ++k) {
+      const long long i = i0 + k * hop;
+#pragma unroll
+      for (int j = 0; j < N; ++j) u[k][j] = 0.0f;
+      if (i < elems) {
+        grad_at<N>(p, base + i, u[k]);
+        if constexpr (M) momentum_at<N>(p.momentum + base + i, m[k]);
       }
     }
 #pragma unroll
-    for (int j = 0; j < N; ++j) s = fmaf(u[j], u[j], s);
+    for (int k = 0; k < kBatch; ++k) {
+      if constexpr (M) {
+        const long long i = i0 + k * hop;
+        if (i >= elems) continue;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          m[k][j] = fmaf(p.mu, m[k][j], u[k][j]);
+          u[k][j] = p.nesterov ? fmaf(p.mu, m[k][j], u[k][j]) : m[k][j];
+        }
+        float* o = p.momentum + base + i;
+        if constexpr (N == 8) {
+          reinterpret_cast<float4*>(o)[0] = make_float4(m[k][0], m[k][1], m[k][2], m[k][3]);
+          reinterpret_cast<float4*>(o)[1] = make_float4(m[k][4], m[k][5], m[k][6], m[k][7]);
+        } else {
+          *o = m[k][0];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) s = fmaf(u[k][j], u[k][j], s);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -628,12 +665,12 @@ __global__ void __launch_bounds__(kMixThreads) muon_start_kernel(const MixParams
   __shared__ float red[kMixThreads / 32];
   after_previous();
   const float* part = p.partial + static_cast<long long>(blockIdx.y) * parts;
-  float s = threadIdx.x < parts ? part[threadIdx.x] : 0.0f;   // parts <= 128
+  float s = threadIdx.x < parts ? part[threadIdx.x] : 0.0f;   // parts <= kMixThreads
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
-  s = (red[0] + red[1]) + (red[2] + red[3]);
+  s = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
   const float f = kSx / (sqrtf(s) + p.eps);
   const long long base = static_cast<long long>(blockIdx.y) * p.rows * p.cols;
   const int groups = static_cast<int>(p.pitch / N);
@@ -673,9 +710,12 @@ __global__ void __launch_bounds__(kMixThreads) muon_start_kernel(const MixParams
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Smaller sizes at or below this have their apply product read lo as well.
+constexpr int kSplitMax = 256;
+
 struct NsLayout {
   int m, k;                    // smaller, larger size
-  bool tall;
+  bool tall, split;
   long long pitch_x, mat_x;    // stored X
   long long pitch_a, mat_a;    // stored A, B
   size_t per_matrix;           // workspace bytes
@@ -688,12 +728,13 @@ NsLayout ns_layout(const moe_muon_config* c) {
   L.tall = c->rows > c->cols;
   L.m = L.tall ? c->cols : c->rows;
   L.k = L.tall ? c->rows : c->cols;
+  L.split = L.m <= kSplitMax;
   L.pitch_x = static_cast<long long>(up(c->cols, 64));
   L.mat_x = L.pitch_x * c->rows;
   L.pitch_a = static_cast<long long>(up(L.m, 64));
   L.mat_a = L.pitch_a * L.m;
-  size_t x = static_cast<size_t>(L.mat_x) * 2, a = static_cast<size_t>(L.mat_a) * 2;
-  L.per_matrix = 3 * x + 2 * a + up(L.m * sizeof(float), 16) + kMixBlocks * sizeof(float);
+  const size_t x = static_cast<size_t>(L.mat_x) * 2, a = static_cast<size_t>(L.mat_a) * 2;
+  L.per_matrix = (L.split ? 4 : 3) * x + 2 * a + up(L.m * sizeof(float), 16) + kMixBlocks * sizeof(float);
   return L;
 }
 
@@ -734,21 +775,24 @@ cudaError_t launch_next(const void* kernel, dim3 grid, int threads, size_t smem,
 }
 
 template <int KIND, int BN>
-cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const NsParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& lo, const NsParams& p, int sms,
+                      cudaStream_t stream) {
   static PerDeviceOnce once;
   const void* kernel = reinterpret_cast<const void*>(ns_kernel<KIND, BN>);
   cudaError_t e = once.once(
       [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NsCfg<BN>::kSmem); });
   if (e != cudaSuccess) return e;
-  void* args[3] = {const_cast<CUtensorMap*>(&a), const_cast<CUtensorMap*>(&b), const_cast<NsParams*>(&p)};
+  void* args[4] = {const_cast<CUtensorMap*>(&a), const_cast<CUtensorMap*>(&b), const_cast<CUtensorMap*>(&lo),
+                   const_cast<NsParams*>(&p)};
   return launch_next(kernel, dim3(2 * std::min(sms / 2, p.total)), kThreads, NsCfg<BN>::kSmem, stream, args);
 }
 
 // Tiles of a product: 256 columns wide, or 128 where that leaves CTA pairs idle.
 template <int KIND>
-cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap (&b)[2], NsParams p, int mats, int out_rows,
-                         int out_cols, int sms, cudaStream_t stream) {
+cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap (&b)[2], const CUtensorMap (&lo)[2], NsParams p, int mats,
+                         int out_rows, int out_cols, int sms, cudaStream_t stream) {
   constexpr bool sym = KIND == kGram || KIND == kPoly;
+  p.valid_cols = out_cols;
   auto count = [&](int bn) {
     p.col_tiles = (out_cols + bn - 1) / bn;
     const int q = (out_rows + 255) / 256, per = 256 / bn;
@@ -756,9 +800,9 @@ cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap (&b)[2], NsPara
     p.total = p.tiles * mats;
   };
   count(256);
-  if (p.total > sms / 4) return launch_ns<KIND, 256>(a, b[0], p, sms, stream);
+  if (p.total > sms / 4) return launch_ns<KIND, 256>(a, b[0], lo[0], p, sms, stream);
   count(128);
-  return launch_ns<KIND, 128>(a, b[1], p, sms, stream);
+  return launch_ns<KIND, 128>(a, b[1], lo[1], p, sms, stream);
 }
 
 // What the last product writes and the first kernels read.
@@ -787,7 +831,7 @@ int device_sms() {
 moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace, size_t bytes, uint32_t* err,
                     cudaStream_t stream) {
   const NsLayout L = ns_layout(c);
-  const size_t slack = 8 * 256;
+  const size_t slack = 16 * 256;
   if (bytes < slack + L.per_matrix) return MOE_ERR_CAPACITY;
   int chunk = static_cast<int>(std::min<size_t>((bytes - slack) / L.per_matrix, static_cast<size_t>(c->batch)));
   if (chunk > 65535) chunk = 65535;
@@ -801,7 +845,8 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
   };
   const size_t nx = static_cast<size_t>(L.mat_x) * 2 * chunk, na = static_cast<size_t>(L.mat_a) * 2 * chunk;
   __half* hi[2] = {reinterpret_cast<__half*>(take(nx)), reinterpret_cast<__half*>(take(nx))};
-  __half* lo = reinterpret_cast<__half*>(take(nx));
+  __half* lo[2] = {reinterpret_cast<__half*>(take(nx)), nullptr};
+  lo[1] = L.split ? reinterpret_cast<__half*>(take(nx)) : lo[0];
   __half* A = reinterpret_cast<__half*>(take(na));
   __half* B = reinterpret_cast<__half*>(take(na));
   float* diag = reinterpret_cast<float*>(take(sizeof(float) * L.m * chunk));
@@ -819,6 +864,9 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
     }
     ok = ok && map_of(&ab[i], A, L.pitch_a, L.m, chunk, 128 >> i, 2) && map_of(&bb[i], B, L.pitch_a, L.m, chunk, 128 >> i, 2);
   }
+  CUtensorMap xl[2][2];   // X's lo half as the operand X is in the apply product
+  for (int i = 0; i < 2; ++i)
+    for (int n = 0; n < 2; ++n) ok = ok && map_of(&xl[i][n], lo[i], L.pitch_x, c->rows, chunk, 128, L.tall ? 2 : 2 - n);
   CUtensorMap xk[2][2];   // wide: X as the K-major B operand of its own Gram matrix
   for (int i = 0; i < 2; ++i)
     for (int n = 0; n < 2; ++n) ok = ok && map_of(&xk[i][n], hi[i], L.pitch_x, c->rows, chunk, 128 >> n, 2);
@@ -839,13 +887,16 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
     mp.eps = c->eps;
     mp.partial = partial;
     mp.hi = hi[0];
-    mp.lo = lo;
+    mp.lo = lo[0];
     mp.pitch = L.pitch_x;
     mp.mat = L.mat_x;
     const bool vec = elems % 8 == 0, vec_rows = c->cols % 8 == 0;
     const int parts = static_cast<int>(std::min<long long>(kMixBlocks, (elems + 8 * kMixThreads - 1) / (8 * kMixThreads)));
-    if (vec) muon_mix_kernel<8><<<dim3(parts, n), kMixThreads, 0, stream>>>(mp);
-    else muon_mix_kernel<1><<<dim3(parts, n), kMixThreads, 0, stream>>>(mp);
+    const dim3 mgrid(parts, n);
+    if (vec && mp.momentum) muon_mix_kernel<8, true><<<mgrid, kMixThreads, 0, stream>>>(mp);
+    else if (vec) muon_mix_kernel<8, false><<<mgrid, kMixThreads, 0, stream>>>(mp);
+    else if (mp.momentum) muon_mix_kernel<1, true><<<mgrid, kMixThreads, 0, stream>>>(mp);
+    else muon_mix_kernel<1, false><<<mgrid, kMixThreads, 0, stream>>>(mp);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     int parts_arg = parts;
     void* sargs[2] = {&mp, &parts_arg};
@@ -872,26 +923,28 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
       p.a_mn = p.b_mn = L.tall;
       p.kstages = (L.k + 127) / 128;
       p.out_hi = A;
-      if (launch_tiles<kGram>(xa[cur], L.tall ? xb[cur] : xk[cur], p, n, L.m, L.m, sms, stream) != cudaSuccess)
+      if (launch_tiles<kGram>(xa[cur], L.tall ? xb[cur] : xk[cur], xl[cur], p, n, L.m, L.m, sms, stream) != cudaSuccess)
         return MOE_ERR_CUDA;
       p.a_mn = p.b_mn = 0;
       p.kstages = (L.m + 127) / 128;
       p.in_hi = A;
       p.out_hi = B;
-      if (launch_tiles<kPoly>(aa, ab, p, n, L.m, L.m, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+      if (launch_tiles<kPoly>(aa, ab, xl[cur], p, n, L.m, L.m, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
       p.rows = c->rows;
       p.cols = static_cast<int>(L.pitch_x);
       p.pitch = L.pitch_x;
       p.mat = L.mat_x;
       p.in_hi = hi[cur];
       p.out_hi = hi[cur ^ 1];
-      p.lo = lo;
+      p.in_lo = lo[cur];
+      p.out_lo = lo[cur ^ 1];
+      p.split = L.split;
       p.diag_cols = L.tall;
       p.b_mn = !L.tall;
       const CUtensorMap& opa = L.tall ? xa[cur] : ba;
       const CUtensorMap (&opb)[2] = L.tall ? bb : xb[cur];
       if (s + 1 < c->steps) {
-        if (launch_tiles<kApply>(opa, opb, p, n, c->rows, c->cols, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch_tiles<kApply>(opa, opb, xl[cur], p, n, c->rows, c->cols, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
       } else {
         p.ucols = c->cols;
         if (io.o16) p.o16 = io.o16 + u0;
@@ -900,7 +953,9 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
         p.w16 = io.w16 ? io.w16 + u0 : nullptr;
         p.decay = io.decay;
         p.rate = io.rate;
-        if (launch_tiles<kFinal>(opa, opb, p, n, c->rows, c->cols, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        const cudaError_t e = io.o16 ? launch_tiles<kFinal>(opa, opb, xl[cur], p, n, c->rows, c->cols, sms, stream)
+                                     : launch_tiles<kUpdate>(opa, opb, xl[cur], p, n, c->rows, c->cols, sms, stream);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
       }
     }
   }
@@ -918,7 +973,7 @@ extern "C" {
 size_t moe_muon_workspace_bytes(const moe_muon_config* cfg, int32_t matrices) {
   if (!muon_config_ok(cfg) || !muon_size_ok(cfg)) return 0;
   const size_t n = matrices > 0 ? static_cast<size_t>(matrices) : 1;
-  return ns_layout(cfg).per_matrix * n + 8 * 256;
+  return ns_layout(cfg).per_matrix * n + 16 * 256;
 }
 
 moe_status moe_orthogonalize(const moe_muon_config* cfg, const void* x, moe_type x_type, void* out, void* workspace,
