@@ -1033,10 +1033,10 @@ moe_status moe_block_norm_forward(const moe_block_norm_config* cfg, const void* 
       !stride_ok(cfg->y_stride, cfg->d_model) || !stride_ok(cfg->h_stride, cfg->d_model))
     return MOE_ERR_INVALID_ARG;
   if (cfg->d_model > kMaxCols) return MOE_ERR_UNSUPPORTED;
+  if (cfg->tokens == 0) return MOE_OK;
   if (!branch && (gate || post_weight)) return MOE_ERR_INVALID_ARG;
   if (branch && (gate != nullptr) != (cfg->gate_mode != MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
   if ((pre_weight != nullptr) != (h != nullptr)) return MOE_ERR_INVALID_ARG;
-  if (cfg->tokens == 0) return MOE_OK;
   if (!x || (!y && !h)) return MOE_ERR_INVALID_ARG;
   for (const void* q : {x, branch, gate, post_weight, pre_weight, static_cast<const void*>(y),
                         static_cast<const void*>(h), static_cast<const void*>(stats)})
@@ -1075,6 +1075,17 @@ moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void*
       !stride_ok(cfg->y_stride, cfg->d_model) || !stride_ok(cfg->h_stride, cfg->d_model))
     return MOE_ERR_INVALID_ARG;
   if (cfg->d_model > kMaxCols) return MOE_ERR_UNSUPPORTED;
+  const int T = cfg->tokens, D = cfg->d_model;
+  if (T == 0) {   // no rows: the parameters' gradients are zero
+    if (!aligned16(dgate) || !aligned16(dpost_weight) || !aligned16(dpre_weight)) return MOE_ERR_INVALID_ARG;
+    auto zero = [&](void* q, size_t n) { return q ? cudaMemsetAsync(q, 0, n, stream) : cudaSuccess; };
+    const size_t gsz = (cfg->gate_type == MOE_TYPE_FP32 ? 4 : 2);
+    const size_t grows = cfg->gate_mode == MOE_GATE_CHANNEL ? 1 : (cfg->gate_mode == MOE_GATE_GROUP ? cfg->gate_rows : 0);
+    if (zero(dpost_weight, sizeof(float) * D) != cudaSuccess || zero(dpre_weight, sizeof(float) * D) != cudaSuccess ||
+        zero(grows ? dgate : nullptr, grows * D * gsz) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
   if (!branch && (gate || post_weight)) return MOE_ERR_INVALID_ARG;
   if (branch && (gate != nullptr) != (cfg->gate_mode != MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
   if ((branch != nullptr) != (dbranch != nullptr)) return MOE_ERR_INVALID_ARG;
@@ -1087,16 +1098,6 @@ moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void*
                         static_cast<const void*>(dpost_weight), static_cast<const void*>(dpre_weight),
                         static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
-  const int T = cfg->tokens, D = cfg->d_model;
-  if (T == 0) {   // no rows: the parameters' gradients are zero
-    auto zero = [&](void* q, size_t n) { return q ? cudaMemsetAsync(q, 0, n, stream) : cudaSuccess; };
-    const size_t gsz = (cfg->gate_type == MOE_TYPE_FP32 ? 4 : 2);
-    const size_t grows = cfg->gate_mode == MOE_GATE_CHANNEL ? 1 : (cfg->gate_mode == MOE_GATE_GROUP ? cfg->gate_rows : 0);
-    if (zero(dpost_weight, sizeof(float) * D) != cudaSuccess || zero(dpre_weight, sizeof(float) * D) != cudaSuccess ||
-        zero(grows ? dgate : nullptr, grows * D * gsz) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    return MOE_OK;
-  }
   if (!x || ((post_weight || pre_weight) && !stats)) return MOE_ERR_INVALID_ARG;
   const size_t need = moe_block_norm_workspace_bytes(cfg);
   if (need == 0) return MOE_ERR_CUDA;

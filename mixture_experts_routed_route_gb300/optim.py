@@ -55,6 +55,7 @@ def error_bits(device="cuda"):
     word = _error_word(device)
     bits = int(word.item())
     word.zero_()
+    torch.cuda.synchronize(device)   # cleared before another stream's kernel sets a bit
     return bits
 
 
