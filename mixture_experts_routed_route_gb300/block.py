@@ -11,6 +11,7 @@ it runs on.  Inputs that another stream still writes are the caller's to
 order, as with any torch operator.
 """
 
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -18,16 +19,21 @@ import torch
 from . import abi
 
 _TYPE = {torch.bfloat16: abi.MOE_TYPE_BF16, torch.float32: abi.MOE_TYPE_FP32}
+_NormConfig, _GateConfig = abi.moe_block_norm_config, abi.moe_topk_gate_config
 _SCORE = {"softmax": abi.MOE_SCORE_SOFTMAX, "sigmoid": abi.MOE_SCORE_SIGMOID}
 
 
 # the raw handle of a device's current stream (torch.cuda.current_stream builds a Stream object each time)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+_BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
+_empty, _empty_like, _byref = torch.empty, torch.empty_like, ctypes.byref
+_LIB = abi.LIB
 
 
 def on_stream(fn, device, stream):
     """fn(raw stream) with `device` current, on `stream` (None: the current one), which is then current too."""
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and device.index == _current_device():
         return fn(_raw_stream(device.index))
     with torch.cuda.device(device):
         if stream is None:
@@ -38,11 +44,15 @@ def on_stream(fn, device, stream):
             return fn(stream.cuda_stream)
 
 
-def _new(x, dtype=None):
-    """An uninitialised contiguous tensor of x's shape, of its type or another."""
-    if dtype is None or dtype == x.dtype:
-        return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    return torch.empty(x.shape, dtype=dtype, device=x.device)
+def _new(x, dtype):
+    """An uninitialised contiguous tensor of x's shape."""
+    if dtype is x.dtype and x.is_contiguous():
+        return _empty_like(x)
+    return _empty(x.shape, dtype=dtype, device=x.device)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need(ok, message):
@@ -57,56 +67,71 @@ def _wrong(name, t, dtype, shape, device, contiguous=""):
 
 def _rows(name, t, dtype, shape, device):
     """A [T, D] tensor whose rows are contiguous; its row stride."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         _wrong(name, t, dtype, shape, device)
-    T, D = shape
     row, col = t.stride()
-    if (col != 1 and D > 1 and T > 0) or (row < D and T > 1):
-        raise ValueError(f"{name}: rows have to be contiguous and apart (strides {row}, {col} for {D} columns)")
-    return row if T > 1 else D
+    T, D = shape
+    if col == 1 and row >= D:
+        return row
+    if T <= 1:
+        if col == 1 or D <= 1 or T == 0:
+            return D
+    elif D <= 1 and row >= D:
+        return row
+    raise ValueError(f"{name}: rows have to be contiguous and apart (strides {row}, {col} for {D} columns)")
 
 
 def _dense(name, t, dtype, shape, device):
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         _wrong(name, t, dtype, shape, device, "contiguous ")
 
 
 def _gate_shape(cfg, gate, T, D, device):
     shape = gate.shape
-    if gate.dtype not in _TYPE or gate.device != device or not gate.is_contiguous() or len(shape) not in (1, 2):
+    n = len(shape)
+    if gate.dtype not in _TYPE or gate.device != device or not gate.is_contiguous() or not 1 <= n <= 2:
         raise ValueError(f"gate: expected contiguous bfloat16 or float32 on {device}, got {gate.dtype} {list(shape)} on "
                          f"{gate.device}")
     cfg.gate_type = _TYPE[gate.dtype]
-    if len(shape) == 1 and shape[0] == D:
-        cfg.gate_mode = abi.MOE_GATE_CHANNEL
-    elif len(shape) == 2 and shape[1] == D and shape[0] > 0 and T % shape[0] == 0:
+    if n == 1:
+        if shape[0] == D:
+            cfg.gate_mode = abi.MOE_GATE_CHANNEL
+            return
+    elif shape[1] == D and shape[0] > 0 and T % shape[0] == 0:
         cfg.gate_mode, cfg.gate_rows = abi.MOE_GATE_GROUP, shape[0]
-    elif len(shape) == 2 and shape[0] == T and shape[1] == 1:
+        return
+    elif shape[0] == T and shape[1] == 1:
         cfg.gate_mode = abi.MOE_GATE_TOKEN
-    else:
-        raise ValueError(f"gate {list(shape)}: expected [{D}], [G, {D}] with G dividing {T}, or [{T}, 1]")
+        return
+    raise ValueError(f"gate {list(shape)}: expected [{D}], [G, {D}] with G dividing {T}, or [{T}, 1]")
 
 
 def _norm_config(x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, eps, weight_offset):
     """The checked configuration shared by block_norm and its backward."""
     xt, shape, dev = x.dtype, x.shape, x.device
-    if len(shape) != 2 or xt not in _TYPE or not x.is_cuda:
+    if len(shape) != 2 or xt not in _TYPE or dev.type != "cuda":
         raise ValueError("x: expected a CUDA bfloat16 or float32 [T, D] tensor")
     T, D = shape
-    cfg = abi.moe_block_norm_config(T, D, _TYPE[xt], 0, 0, abi.MOE_GATE_NONE, 0, residual_scale, branch_scale, eps,
-                                    weight_offset, _rows("x", x, xt, shape, dev), 0, 0, 0)
-    if branch is not None:
-        cfg.branch_stride = _rows("branch", branch, torch.bfloat16, shape, dev)
-    elif gate is not None or post_weight is not None:
-        raise ValueError("a gate or post_weight needs a branch")
-    kind = None
-    for w in (post_weight, pre_weight):
-        if w is not None:
-            kind = kind or w.dtype
-            if kind not in _TYPE:
-                raise ValueError("weights are bfloat16 or float32")
-            _dense("weight", w, kind, (D,), dev)
-            cfg.weight_type = _TYPE[kind]
+    kind = _FP32
+    if pre_weight is not None:
+        kind = pre_weight.dtype
+        if kind not in _TYPE:
+            raise ValueError("weights are bfloat16 or float32")
+        _dense("pre_weight", pre_weight, kind, (D,), dev)
+    if branch is None:
+        if gate is not None or post_weight is not None:
+            raise ValueError("a gate or post_weight needs a branch")
+        branch_row = 0
+    else:
+        branch_row = _rows("branch", branch, _BF16, shape, dev)
+        if post_weight is not None:
+            if pre_weight is None:
+                kind = post_weight.dtype
+                if kind not in _TYPE:
+                    raise ValueError("weights are bfloat16 or float32")
+            _dense("post_weight", post_weight, kind, (D,), dev)
+    cfg = _NormConfig(T, D, _TYPE[xt], _TYPE[kind], 0, 0, 0, residual_scale, branch_scale, eps, weight_offset,
+                      _rows("x", x, xt, shape, dev), branch_row, 0, 0)
     if gate is not None:
         _gate_shape(cfg, gate, T, D, dev)
     return cfg
@@ -132,17 +157,19 @@ def block_norm(x, branch=None, *, gate=None, post_weight=None, pre_weight=None, 
         cfg.y_stride = _rows("y", y, x.dtype, shape, dev)
     if h is not None:
         _need(pre_weight is not None, "h needs a pre_weight")
-        cfg.h_stride = _rows("h", h, torch.bfloat16, shape, dev)
+        cfg.h_stride = _rows("h", h, _BF16, shape, dev)
     if stats is not None:
-        _dense("stats", stats, torch.float32, (2, shape[0]), dev)
-    _need(branch is not None or pre_weight is not None or y is not None or residual_scale != 1.0,
-          "nothing to compute: no branch, no pre_weight")
+        _dense("stats", stats, _FP32, (2, shape[0]), dev)
     same = branch is None and y is None and residual_scale == 1.0
+    _need(not same or pre_weight is not None, "nothing to compute: no branch, no pre_weight")
 
     def run(s):
-        yy = y if y is not None or same else _new(x)
-        hh = h if h is not None or pre_weight is None else _new(x, torch.bfloat16)
-        abi.moe_block_norm_forward(cfg, x, branch, gate, post_weight, pre_weight, yy, hh, stats, s)
+        yy = y if y is not None or same else _new(x, x.dtype)
+        hh = h if h is not None or pre_weight is None else _new(x, _BF16)
+        status = _LIB.moe_block_norm_forward(_byref(cfg), x.data_ptr(), _at(branch), _at(gate), _at(post_weight),
+                                             _at(pre_weight), _at(yy), _at(hh), _at(stats), s)
+        if status:
+            raise abi.MoEError("moe_block_norm_forward", status)
         return (x if same else yy), hh
 
     return on_stream(run, dev, stream)
@@ -170,32 +197,38 @@ def block_norm_backward(x, branch, stats, dy, dh=None, *, gate=None, post_weight
     if dy is not None:
         cfg.y_stride = _rows("dy", dy, x.dtype, shape, dev)
     if dh is not None:
-        cfg.h_stride = _rows("dh", dh, torch.bfloat16, shape, dev)
+        cfg.h_stride = _rows("dh", dh, _BF16, shape, dev)
     if post_weight is not None or pre_weight is not None:
         _need(stats is not None, "the norms' backward needs the forward's stats")
-        _dense("stats", stats, torch.float32, (2, T), dev)
+        _dense("stats", stats, _FP32, (2, T), dev)
 
     def run(s):
-        dx = _new(x)
-        dbranch = None if branch is None else _new(branch)
-        dgate = None if gate is None else torch.empty_like(gate)
-        dpost = None if post_weight is None else torch.empty(D, dtype=torch.float32, device=dev)
-        dpre = None if pre_weight is None else torch.empty(D, dtype=torch.float32, device=dev)
-        nb = abi.moe_block_norm_workspace_bytes(cfg)
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-        abi.moe_block_norm_backward(cfg, x, branch, gate, post_weight, pre_weight, stats, dy, dh, dx, dbranch, dgate,
-                                    dpost, dpre, ws, nb, s)
+        dx = _new(x, x.dtype)
+        dbranch = None if branch is None else _new(branch, _BF16)
+        dgate = None if gate is None else _empty_like(gate)
+        dpost = None if post_weight is None else _empty(D, dtype=_FP32, device=dev)
+        dpre = None if pre_weight is None else _empty(D, dtype=_FP32, device=dev)
+        ref = _byref(cfg)
+        nb = _LIB.moe_block_norm_workspace_bytes(ref)
+        ws = _empty(nb, dtype=torch.uint8, device=dev)
+        status = _LIB.moe_block_norm_backward(ref, x.data_ptr(), _at(branch), _at(gate), _at(post_weight),
+                                              _at(pre_weight), _at(stats), _at(dy), _at(dh), dx.data_ptr(), _at(dbranch),
+                                              _at(dgate), _at(dpost), _at(dpre), ws.data_ptr(), nb, s)
+        if status:
+            raise abi.MoEError("moe_block_norm_backward", status)
         return BlockNormGrads(dx, dbranch, dgate, dpost, dpre)
 
     return on_stream(run, dev, stream)
 
 
 def _gate_config(logits, top_k, score, renormalize, scale):
-    kind, shape = logits.dtype, logits.shape
-    _need(len(shape) == 2 and kind in _TYPE and logits.is_cuda, "logits: expected a CUDA bfloat16 or float32 [T, E] tensor")
-    _need(score in _SCORE, "score: softmax or sigmoid")
-    return abi.moe_topk_gate_config(shape[0], shape[1], top_k, _TYPE[kind], _SCORE[score], 1 if renormalize else 0, scale,
-                                    _rows("logits", logits, kind, shape, logits.device))
+    kind, shape, dev = logits.dtype, logits.shape, logits.device
+    if len(shape) != 2 or kind not in _TYPE or dev.type != "cuda":
+        raise ValueError("logits: expected a CUDA bfloat16 or float32 [T, E] tensor")
+    if score not in _SCORE:
+        raise ValueError("score: softmax or sigmoid")
+    return _GateConfig(shape[0], shape[1], top_k, _TYPE[kind], _SCORE[score], 1 if renormalize else 0, scale,
+                       _rows("logits", logits, kind, shape, dev))
 
 
 def topk_gate(logits, top_k, *, score="softmax", renormalize=False, scale=1.0, select_bias=None, ids=None, scores=None,
@@ -209,16 +242,19 @@ def topk_gate(logits, top_k, *, score="softmax", renormalize=False, scale=1.0, s
     cfg = _gate_config(logits, top_k, score, renormalize, scale)
     dev, shape = logits.device, (logits.shape[0], top_k)
     if select_bias is not None:
-        _dense("select_bias", select_bias, torch.float32, (logits.shape[1],), dev)
+        _dense("select_bias", select_bias, _FP32, (logits.shape[1],), dev)
     if ids is not None:
-        _dense("ids", ids, torch.int32, shape, dev)
+        _dense("ids", ids, _INT32, shape, dev)
     if scores is not None:
-        _dense("scores", scores, torch.float32, shape, dev)
+        _dense("scores", scores, _FP32, shape, dev)
 
     def run(stream):
-        i = torch.empty(shape, dtype=torch.int32, device=dev) if ids is None else ids
-        s = torch.empty(shape, dtype=torch.float32, device=dev) if scores is None else scores
-        abi.moe_topk_gate_forward(cfg, logits, select_bias, i, s, stream)
+        i = _empty(shape, dtype=_INT32, device=dev) if ids is None else ids
+        s = _empty(shape, dtype=_FP32, device=dev) if scores is None else scores
+        status = _LIB.moe_topk_gate_forward(_byref(cfg), logits.data_ptr(), _at(select_bias), i.data_ptr(), s.data_ptr(),
+                                            stream)
+        if status:
+            raise abi.MoEError("moe_topk_gate_forward", status)
         return i, s
 
     return on_stream(run, dev, stream)
@@ -231,14 +267,17 @@ def topk_gate_backward(logits, ids, d_scores, *, score="softmax", renormalize=Fa
     _need(ids.dim() == 2, "ids: expected [T, top_k]")
     cfg = _gate_config(logits, ids.shape[1], score, renormalize, scale)
     dev, shape = logits.device, (logits.shape[0], ids.shape[1])
-    _dense("ids", ids, torch.int32, shape, dev)
-    _dense("d_scores", d_scores, torch.float32, shape, dev)
+    _dense("ids", ids, _INT32, shape, dev)
+    _dense("d_scores", d_scores, _FP32, shape, dev)
     if d_logits is not None:
         _dense("d_logits", d_logits, logits.dtype, logits.shape, dev)
 
     def run(stream):
-        d = _new(logits) if d_logits is None else d_logits
-        abi.moe_topk_gate_backward(cfg, logits, ids, d_scores, d, stream)
+        d = _new(logits, logits.dtype) if d_logits is None else d_logits
+        status = _LIB.moe_topk_gate_backward(_byref(cfg), logits.data_ptr(), ids.data_ptr(), d_scores.data_ptr(),
+                                             d.data_ptr(), stream)
+        if status:
+            raise abi.MoEError("moe_topk_gate_backward", status)
         return d
 
     return on_stream(run, dev, stream)
