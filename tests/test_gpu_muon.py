@@ -116,6 +116,28 @@ def test_runs_of_matrices_and_workspaces_do_not_change_bits():
     assert e.value.status == abi.MOE_ERR_CAPACITY
 
 
+# (smaller size at most 256) one to four CTA pairs a matrix, several rounds of
+# matrices, and batches between them that the tiled kernels take
+@pytest.mark.parametrize("E,N,K", [(1, 60, 250), (1, 200, 700), (1, 1000, 130), (9, 256, 513), (20, 900, 100), (37, 33, 65),
+                                   (40, 256, 1030), (80, 300, 64), (90, 96, 200), (160, 140, 136), (230, 20, 30)])
+def test_small_matrices_and_batches(E, N, K):
+    from mixture_experts_routed_route_gb300 import optim
+    g = gradient(E, N, K, seed=E).bfloat16()
+    out = optim.orthogonalize(g)
+    assert off(out, ns64(g)) <= BOUND
+    one = optim.workspace(E, N, K, matrices=1)
+    assert torch.equal(optim.orthogonalize(g, workspace=one), out)
+    assert torch.equal(optim.orthogonalize(g), out)
+    # the update's own tile walk, in place
+    w = torch.randn((E, N, K), device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    ref = 0.75 * w.double() - 0.5 * out.double()
+    mom = torch.zeros_like(w)
+    optim.muon_update(w, g, mom, lr=0.5, mu=0.0, nesterov=False, weight_decay=0.5, scale=1.0)
+    # W - 0.5 X with X before its BF16 rounding: 0.5 x 2^-8 |X|, and FP32's rounding of W
+    assert bool(((w.double() - ref).abs() <= 2.0 ** -9 * out.double().abs() + 2.0 ** -22 * (w.double().abs() + 1)).all())
+    assert optim.error_bits() == 0
+
+
 def test_tall_and_wide_agree():
     """The transposed input gives the transposed result, to the bound of each."""
     from mixture_experts_routed_route_gb300 import optim
