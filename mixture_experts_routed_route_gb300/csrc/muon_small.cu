@@ -478,7 +478,7 @@ int muon_small_pairs(int mats, int k) {
   if (!most) return 0;
   const int tiles = (k + 255) / 256;
   int i = tiles > 2 ? 2 : tiles > 1 ? 1 : 0;
-  while (i > 0 && mats > most[i]) --i;
+  for (; i > 0 && mats > most[i];) --i;
   if (most[i] < 1) return 0;
   const int pairs = 1 << i, per = (tiles + pairs - 1) / pairs, rounds = (mats + most[i] - 1) / most[i];
   if (rounds == 1 && per == 1) return pairs;
