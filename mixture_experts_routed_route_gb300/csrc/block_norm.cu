@@ -15,8 +15,8 @@
 //
 // Work layout: persistent CTAs, one per SM.  A group of W warps owns a row
 // (W = ceil(D / 1024) with 32 columns a thread in four pieces of 8, or twice
-// as many with half of that); as many
-// groups share a CTA as its registers and shared memory hold.  Rows come in
+// as many with half of that); as many groups share a CTA as its registers and
+// shared memory hold, and take rows in turns over the CTAs.  Rows come in
 // through shared memory, cp.async, and are read from there once per pass
 // over them (the row's sums separate the passes), so registers hold only
 // what a later pass needs: the FP32 y in the forward; in the backward the
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) block_norm_fwd_kernel(const __
   __shared__ __align__(16) float red_all[15][64];
   constexpr int P = kPiecesOf<V, false>;
   Group<V, P> g(p, shared, red_all);
-  const int first = blockIdx.x * p.groups + g.grp, step = gridDim.x * p.groups;
+  const int first = g.grp * gridDim.x + blockIdx.x, step = gridDim.x * p.groups;
   const int n = first < p.T ? (p.T - 1 - first) / step + 1 : 0;
   g.start(first, step, n);
   g.make_table(shared);
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) block_norm_bwd_kernel(const __
   __shared__ __align__(16) float red_all[15][64];
   constexpr int P = kPiecesOf<V, true>;
   Group<V, P> g(p, shared, red_all);
-  const int worker = blockIdx.x * p.groups + g.grp, workers = gridDim.x * p.groups;
+  const int worker = g.grp * gridDim.x + blockIdx.x, workers = gridDim.x * p.groups;
   if constexpr (GATE != MOE_GATE_GROUP) {
     g.start(worker, workers, worker < p.T ? (p.T - 1 - worker) / workers + 1 : 0);
   }
@@ -882,15 +882,23 @@ struct Shape {
   int warps, groups, stages, threads;
 };
 
-// How many groups share a CTA, and how many rows
-// each has in flight.
-Shape place(NormParams* p, bool fwd, bool vec) {
+// How many groups share a CTA, and how many rows each has in flight.  As many
+// groups as 16 warps and the memory hold (14 warps: backward 55 instead of 46
+// us at 4096 x 4096, 80.2 and 77.8 at 16384 x 2048), in the forward no third
+// one that leaves only two rows in flight (8192 x 5120: 58.3 instead of 55.7
+// us); of those no more than save a round of rows (1531 x 1411 backward: four
+// groups 23.3 us, five, in as many rounds, 25.8); where one round is enough, the
+// forward's idle groups still help to fill the table (1 x 7168: 6.2 and 7.3 us).
+Shape place(NormParams* p, bool fwd, bool vec, int sms) {
   Shape s;
   const int warp_cols = 256 * (fwd ? (vec ? kPiecesOf<8, false> : kPiecesOf<1, false>) : (vec ? kPiecesOf<8, true> : kPiecesOf<1, true>));
   s.warps = (p->D + warp_cols - 1) / warp_cols;
   p->table = (p->D * 4 + 15) / 16 * 16 * 2;
   const int room = kSharedMem - p->table;
-  s.groups = std::max(1, std::min({14 / s.warps, 15, room / p->slot}));   // named barriers 1 .. 15
+  int most = std::max(1, std::min({kWarps / s.warps, 15, room / p->slot}));   // named barriers 1 .. 15
+  if (fwd && most > 2) most = std::min(most, std::max(2, room / (3 * p->slot)));
+  const int rounds = (p->T - 1) / (sms * most) + 1;
+  s.groups = fwd && rounds == 1 ? most : (p->T - 1) / (sms * rounds) + 1;
   s.stages = std::max(1, std::min(4, room / (s.groups * p->slot)));
   s.threads = s.warps * s.groups * 32;
   p->warps = s.warps;
@@ -1049,10 +1057,10 @@ moe_status moe_block_norm_forward(const moe_block_norm_config* cfg, const void* 
   add_stream(&p, kO, branch, cfg->branch_stride, MOE_TYPE_BF16);
   if (p.gate_mode == kGateFull) add_stream(&p, kG, gate, 0, cfg->gate_type);
   const bool vec = lay_out(&p);
-  const Shape s = place(&p, true, vec);
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  const int ctas = std::min(sms, (p.T - 1) / s.groups + 1);
+  const Shape s = place(&p, true, vec, sms);
+  const int ctas = std::min(sms, p.T);
   return launch_norm(true, vec, ctas, s, p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1115,8 +1123,8 @@ moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void*
   add_stream(&p, kDh, dh, cfg->h_stride, MOE_TYPE_BF16);
   if (p.gate_mode == kGateFull) add_stream(&p, kG, gate, 0, cfg->gate_type);
   const bool vec = lay_out(&p);
-  const Shape s = place(&p, false, vec);
-  const int ctas = std::min(sms, (T - 1) / s.groups + 1);
+  const Shape s = place(&p, false, vec, sms);
+  const int ctas = std::min(sms, T);
   p.partial = static_cast<float*>(workspace);
   p.gate_partial = p.partial + 2ll * ctas * D;
   if (p.gate_mode == MOE_GATE_GROUP) {
@@ -1127,7 +1135,8 @@ moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void*
   if (launch_norm(false, vec, ctas, s, p, stream) != cudaSuccess) return MOE_ERR_CUDA;
   if (dpost_weight || dpre_weight || p.gate_mode == MOE_GATE_CHANNEL) {
     norm_param_grad_kernel<<<dim3((D + 31) / 32, 2), 256, 0, stream>>>(p, ctas, dpost_weight, dpre_weight);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   if (p.gate_mode == MOE_GATE_GROUP && p.slabs_per_group > 1) {
     gate_slab_sum_kernel<<<dim3((D + 255) / 256, cfg->gate_rows), 256, 0, stream>>>(p.gate_partial, p.slabs_per_group, D,

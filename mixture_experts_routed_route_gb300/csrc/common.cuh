@@ -555,4 +555,12 @@ __device__ __forceinline__ float warp_max_nonneg(float v) {
 __device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 __device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
+// In a kernel launched with programmatic dependence (launch_dependent): the
+// next one may be placed and set itself up while this one runs, and this one
+// waits here for the end of the one before it, and its results.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 }  // namespace moe

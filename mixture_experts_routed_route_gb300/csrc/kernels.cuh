@@ -40,6 +40,30 @@ struct PerDeviceOnce {
   }
 };
 
+// A launch with programmatic dependence on the kernel before it, which has to
+// wait for that one's results itself.  cluster: CTAs a cluster, where the
+// kernel does not say.
+inline cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                    void** args, int cluster = 0) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cluster) {
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
 // Device view of one routing state (the saved-state prefix or the
 // context's inference copy).  Layout and meaning of every array are those of
 // moe_saved_field in moe_gb300.h.

@@ -55,27 +55,6 @@
 
 namespace moe {
 
-cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, void** args,
-                             int cluster) {
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cluster) {
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = cluster;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  return cudaLaunchKernelExC(&cfg, kernel, args);
-}
-
 namespace {
 
 // Tile of BN = 256 or 128 columns (256 rows on the pair): stages of 128

@@ -298,14 +298,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// The kernels of a call are launched with programmatic dependence: the next
-// one may set itself up (barriers, tensor memory, tensor maps) while this one
-// runs, and waits here for its results.
-__device__ __forceinline__ void after_previous() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 }  // namespace
 
 // The small kernel: all steps of each matrix on a few CTA pairs (m <= 256).
@@ -334,10 +326,5 @@ struct SmallParams {
 // kernels are the faster ones.
 int muon_small_pairs(int mats, int k);
 cudaError_t launch_muon_small(const SmallMaps& maps, const SmallParams& p, cudaStream_t stream);
-
-// A launch with programmatic dependence on the one before it.  cluster: CTAs a
-// cluster, where the kernel itself does not say.
-cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, void** args,
-                             int cluster = 0);
 
 }  // namespace moe
