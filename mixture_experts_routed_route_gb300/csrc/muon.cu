@@ -46,8 +46,11 @@
 // 10 to 17 us each.
 //
 // Warp roles: warp 0 TMA producer, warp 1 TMEM allocation and (rank 0) MMA
-// issue for the pair, warps 2 .. 9 epilogue (lane quadrant w % 4, columns
-// 128 h .. 128 h + 127 of the tile).  Both CTAs' loads complete on rank 0's
+// issue for the pair, warps 2 .. 9 epilogue (lane quadrant w % 4, every
+// other 32 columns of the tile, so that both warps of a quadrant are at
+// neighbouring pieces of their rows; what a chunk reads besides the
+// accumulator is asked for one chunk ahead, over the tile's end too: the
+// update of 64 x 1408 x 2048 790 to 722 us).  Both CTAs' loads complete on rank 0's
 // barrier of the stage.
 #include <algorithm>
 
@@ -225,23 +228,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* ws = turn + (warp - 2) * 1024;
     const uint32_t tempty0 = cluster_addr(tempty, 0);
     uint32_t tc = 0;
+    ChunkIn<KIND> in;   // of the chunk at hand, from one chunk before it (of the tile before) on
+    if (cid < p.total) {
+      const NsTile t = ns_tile<KIND, BN>(p, cid, rank);
+      load_chunk_in<KIND>(p, t.mat, t.row0 + q * 32, t.col0 + 32 * h, lane, in);
+    }
     for (int tile = cid; tile < p.total; tile += ncl, ++tc) {
       const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
       const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-      const int r0 = t.row0 + q * 32, cw = t.col0 + BN / 2 * h;
-      ChunkIn<KIND> in;
-      load_chunk_in<KIND>(p, t, r0, cw, lane, in);
+      const int r0 = t.row0 + q * 32, cw = t.col0 + 32 * h;
+      auto load_next = [&](int ci) {
+        if (ci + 1 < kChunks) {
+          load_chunk_in<KIND>(p, t.mat, r0, cw + 64 * (ci + 1), lane, in);
+        } else if (tile + ncl < p.total) {
+          const NsTile tn = ns_tile<KIND, BN>(p, tile + ncl, rank);
+          load_chunk_in<KIND>(p, tn.mat, tn.row0 + q * 32, tn.col0 + 32 * h, lane, in);
+        }
+      };
       if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
       tc_fence_after();
-      const uint32_t tbase = tmem + acc * BN + (static_cast<uint32_t>(q * 32) << 16) + BN / 2 * h;
+      const uint32_t tbase = tmem + acc * BN + (static_cast<uint32_t>(q * 32) << 16) + 32 * h;
 #pragma unroll 1
       for (int ci = 0; ci < kChunks; ++ci) {
-        const int c0 = cw + 32 * ci;
+        const int c0 = cw + 64 * ci;
         // a symmetric output's blocks below the diagonal are their mirrors'
         const bool skip = c0 >= p.cols || ((KIND == kGram || KIND == kPoly) && (c0 >> 7) < (t.row0 >> 7));
         if (!skip) {
           uint32_t v[32];
-          tmem_ld32(tbase + 32 * ci, v);
+          tmem_ld32(tbase + 64 * ci, v);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -256,10 +270,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!skip) {
           __syncwarp();
           const ChunkIn<KIND> now = in;
-          if (ci + 1 < kChunks) load_chunk_in<KIND>(p, t, r0, c0 + 32, lane, in);
+          load_next(ci);
           ns_chunk<KIND>(p, t, r0, c0, lane, ws, now, p.diag + static_cast<long long>(t.mat) * p.diag_n);
-        } else if (ci + 1 < kChunks) {
-          load_chunk_in<KIND>(p, t, r0, c0 + 32, lane, in);
+        } else {
+          load_next(ci);
         }
       }
     }
@@ -372,8 +386,9 @@ __global__ void __launch_bounds__(kMixThreads) muon_mix_kernel(const MixParams p
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// X = U / (|U| + eps) as stored halves, zeros in the row padding.  N = 8: cols
-// % 8 == 0; else a thread takes single columns.
+// X = U / (|U| + eps) as stored halves, zeros in the row padding, 8 columns a
+// thread.  N = 8: cols % 8 == 0; N = 1: rows start anywhere, values are read
+// one by one (3 x 1000 x 1531: 10 us; a single column a thread 19).
 template <int N>
 __global__ void __launch_bounds__(kMixThreads) muon_start_kernel(const MixParams p, int parts) {
   __shared__ float red[kMixThreads / 32];
@@ -387,36 +402,39 @@ __global__ void __launch_bounds__(kMixThreads) muon_start_kernel(const MixParams
   s = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
   const float f = kSx / (sqrtf(s) + p.eps);
   const long long base = static_cast<long long>(blockIdx.y) * p.rows * p.cols;
-  const int groups = static_cast<int>(p.pitch / N);
+  const int groups = static_cast<int>(p.pitch / 8);
   // (row, group) pairs of the matrix, dealt to all its threads
   const long long all = static_cast<long long>(p.rows) * groups;
 #pragma unroll 2
   for (long long k = static_cast<long long>(blockIdx.x) * kMixThreads + threadIdx.x; k < all;
        k += static_cast<long long>(gridDim.x) * kMixThreads) {
-    const int r = static_cast<int>(k / groups), c = static_cast<int>(k - static_cast<long long>(r) * groups) * N;
+    const int r = static_cast<int>(k / groups), c = static_cast<int>(k - static_cast<long long>(r) * groups) * 8;
     const long long at = base + static_cast<long long>(r) * p.cols + c, out = blockIdx.y * p.mat + r * p.pitch + c;
-    float u[N];
-    if (c < p.cols) {
-      grad_at<N>(p, at, u);
-      if (p.momentum) {
-        float m[N];
-        momentum_at<N>(p.momentum + at, m);
+    float u[8];
+    if (c >= p.cols) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) u[j] = p.nesterov ? fmaf(p.mu, m[j], u[j]) : m[j];
+      for (int j = 0; j < 8; ++j) u[j] = 0.0f;
+    } else if constexpr (N == 8) {
+      grad_at<8>(p, at, u);
+      if (p.momentum) {
+        float m[8];
+        momentum_at<8>(p.momentum + at, m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = p.nesterov ? fmaf(p.mu, m[j], u[j]) : m[j];
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) u[j] = 0.0f;
+      for (int j = 0; j < 8; ++j) {
+        u[j] = 0.0f;
+        if (c + j < p.cols) {
+          grad_at<1>(p, at + j, reinterpret_cast<float(&)[1]>(u[j]));
+          if (p.momentum) u[j] = p.nesterov ? fmaf(p.mu, p.momentum[at + j], u[j]) : p.momentum[at + j];
+        }
+      }
     }
 #pragma unroll
-    for (int j = 0; j < N; ++j) u[j] *= f;
-    if constexpr (N == 8) {
-      store_hi_lo(p.hi + out, p.lo + out, u);
-    } else {
-      const __half hi = __float2half_rn(u[0]);
-      p.hi[out] = hi;
-      p.lo[out] = __float2half_rn(u[0] - __half2float(hi));
-    }
+    for (int j = 0; j < 8; ++j) u[j] *= f;
+    store_hi_lo(p.hi + out, p.lo + out, u);
   }
 }
 
@@ -615,7 +633,7 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     int parts_arg = parts;
     void* sargs[2] = {&mp, &parts_arg};
-    const long long pieces = L.mat_x / (vec_rows ? 8 : 1);
+    const long long pieces = L.mat_x / 8;
     const dim3 sgrid(static_cast<unsigned>(std::min<long long>(1024, (pieces + kMixThreads - 1) / kMixThreads)), n);
     if (launch_dependent(vec_rows ? reinterpret_cast<const void*>(muon_start_kernel<8>) : reinterpret_cast<const void*>(muon_start_kernel<1>),
                     sgrid, kMixThreads, 0, stream, sargs) != cudaSuccess)

@@ -167,6 +167,10 @@ __device__ __forceinline__ void put_update1(const NsParams& p, long long u, floa
 }
 
 // What a chunk needs besides the accumulator: 8 columns of rows lane / 4 + 8 it.
+// All of a chunk's loads are sent together: refilling the registers row by row
+// as they are used, two chunks ahead, was slower (an apply product of 8 x 7168
+// x 2048 404 instead of 310 us), since a warp waits on few counters of loads
+// in flight and then waits for the youngest of those that share one.
 template <int KIND>
 struct ChunkIn {
   uint4 hi[4], lo[4];
@@ -174,7 +178,7 @@ struct ChunkIn {
 };
 
 template <int KIND>
-__device__ __forceinline__ void load_chunk_in(const NsParams& p, const NsTile& t, int r0, int c0, int lane, ChunkIn<KIND>& in) {
+__device__ __forceinline__ void load_chunk_in(const NsParams& p, int mat, int r0, int c0, int lane, ChunkIn<KIND>& in) {
   if constexpr (KIND == kGram) return;
   const int c = c0 + (lane & 3) * 8;
 #pragma unroll
@@ -182,13 +186,13 @@ __device__ __forceinline__ void load_chunk_in(const NsParams& p, const NsTile& t
     const int r = r0 + it * 8 + (lane >> 2);
     in.hi[it] = in.lo[it] = make_uint4(0, 0, 0, 0);
     if (r < p.rows && c < p.cols) {
-      const long long at = t.mat * p.mat + r * p.pitch + c;
+      const long long at = mat * p.mat + r * p.pitch + c;
       in.hi[it] = *reinterpret_cast<const uint4*>(p.in_hi + at);
       if constexpr (KIND >= kApply) in.lo[it] = *reinterpret_cast<const uint4*>(p.in_lo + at);
     }
     if constexpr (KIND == kUpdate) {
       if (p.ucols % 8 == 0 && r < p.rows && c < p.ucols) {
-        const long long u = (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + c;
+        const long long u = (static_cast<long long>(mat) * p.rows + r) * p.ucols + c;
         if (p.weight_f32) {
           in.w[it][0] = reinterpret_cast<const uint4*>(static_cast<const float*>(p.weight) + u)[0];
           in.w[it][1] = reinterpret_cast<const uint4*>(static_cast<const float*>(p.weight) + u)[1];

@@ -93,19 +93,19 @@ __device__ __forceinline__ bool small_apply(const SmallParams& sp, const NsParam
     t.col0 = sp.tall ? 0 : tile * 256;
     t.n = 256;
     const uint32_t acc = tc & 1, par = (tc >> 1) & 1;
-    const int r0 = t.row0 + q * 32, cw = t.col0 + 128 * h;
+    const int r0 = t.row0 + q * 32, cw = t.col0 + 32 * h;
     ChunkIn<KIND> in;
-    load_chunk_in<KIND>(p, t, r0, cw, lane, in);
+    load_chunk_in<KIND>(p, t.mat, r0, cw, lane, in);
     if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], par, abort_flag, p.err))) return false;
     tc_fence_after();
-    const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + 128 * h;
+    const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + 32 * h;
 #pragma unroll 1
     for (int ci = 0; ci < 4; ++ci) {
-      const int c0 = cw + 32 * ci;
+      const int c0 = cw + 64 * ci;
       const bool skip = c0 >= p.cols || r0 >= p.rows;
       if (!skip) {
         uint32_t v[32];
-        tmem_ld32(tbase + 32 * ci, v);
+        tmem_ld32(tbase + 64 * ci, v);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -120,7 +120,7 @@ __device__ __forceinline__ bool small_apply(const SmallParams& sp, const NsParam
       if (!skip) {
         __syncwarp();
         const ChunkIn<KIND> now = in;
-        if (ci < 3) load_chunk_in<KIND>(p, t, r0, c0 + 32, lane, in);
+        if (ci < 3) load_chunk_in<KIND>(p, t.mat, r0, c0 + 64, lane, in);
         ns_chunk<KIND>(p, t, r0, c0, lane, ws, now, d);
       }
     }
@@ -360,13 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + 128 * h;
+          const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + 32 * h;
 #pragma unroll 1
           for (int ci = 0; ci < 4; ++ci) {
-            const int c0 = 128 * h + 32 * ci;
+            const int c0 = 64 * ci + 32 * h;
             if (c0 >= used) continue;
             uint32_t v[32];
-            tmem_ld32(tbase + 32 * ci, v);
+            tmem_ld32(tbase + 64 * ci, v);
             tmem_ld_wait();
             uint8_t* chunk = mine + (c0 >> 6) * 16384;
 #pragma unroll
