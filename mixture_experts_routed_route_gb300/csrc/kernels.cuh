@@ -40,6 +40,16 @@ struct PerDeviceOnce {
   }
 };
 
+// SMs of the current device; 0: the driver would not say.
+inline int device_sms() {
+  static PerDeviceOnce once;
+  static int sms[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const cudaError_t e = once.once([&] { return cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev); });
+  return e == cudaSuccess ? sms[dev] : 0;
+}
+
 // A launch with programmatic dependence on the kernel before it, which has to
 // wait for that one's results itself.  cluster: CTAs a cluster, where the
 // kernel does not say.

@@ -550,15 +550,6 @@ struct MuonIo {
   float decay, rate;
 };
 
-int device_sms() {
-  static PerDeviceOnce once;
-  static int sms[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  const cudaError_t e = once.once([&] { return cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev); });
-  return e == cudaSuccess ? sms[dev] : 0;
-}
-
 moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace, size_t bytes, uint32_t* err,
                     cudaStream_t stream) {
   const NsLayout L = ns_layout(c);
