@@ -33,8 +33,8 @@
 //
 // What it measures (BF16, channel gate or none, of 6.77 TB/s measured):
 // forward 2048 x 7168 24.4 us (4.8 TB/s), 8192 x 7168 82 us (5.7), FP32
-// residual with a token gate 16384 x 2048 70 us (5.8); backward 2048 x 7168
-// 46 us (3.8), 8192 x 7168 137 us (5.1), 1531 x 1411 in FP32 22 us (1.7).
+// residual with a gate row a sequence 16384 x 2048 70 us (5.8); backward 2048 x 7168
+// 46 us (3.8), 8192 x 7168 137 us (5.1), 1531 x 1411 in FP32 with a token gate 23 us (1.7).
 // Long inputs are bound by the stream; short ones by the fixed part (launch,
 // factors, column sums: 7 us forward, 15 us backward with its second kernel)
 // and the backward by latency inside a row: its three passes and two sums are

@@ -26,8 +26,8 @@
 // more than 32 keys reach the bound (ties) take them one by one.  What bounds
 // the pass is instruction issue, not the bytes: 16384 x 384, top 8, went from
 // 26 us with one pass over the lanes' keys per choice to 15.6 us (floor 3.9),
-// about 700 instructions a token, of which the softmax over all experts takes
-// a third.  A grid that stays and loads a token ahead took 16.5 to 18.9 us
+// about 700 instructions a token (sigmoid scores with a bias; a softmax over
+// all experts takes as long).  A grid that stays and loads a token ahead took 16.5 to 18.9 us
 // (more registers, fewer warps); 65536 x 64, top 6, takes 24 us, one token 3.4.
 // The backward reads and writes whole rows once: 4096 x 384 7.3 us (1.7 TB/s,
 // mostly the latency of one launch and one row).
