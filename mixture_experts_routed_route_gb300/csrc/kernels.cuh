@@ -40,7 +40,7 @@ struct PerDeviceOnce {
   }
 };
 
-// SMs of the current device; 0: the driver would not say.
+// SMs of the current device; 0: the query failed.
 inline int device_sms() {
   static PerDeviceOnce once;
   static int sms[kMaxDevices];

@@ -231,7 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ChunkIn<KIND> in;   // of the chunk at hand, from one chunk before it (of the tile before) on
     if (cid < p.total) {
       const NsTile t = ns_tile<KIND, BN>(p, cid, rank);
-      load_chunk_in<KIND>(p, t.mat, t.row0 + q * 32, t.col0 + 32 * h, lane, in);
+      load_chunk_in(p, t.mat, t.row0 + q * 32, t.col0 + 32 * h, lane, in);
     }
     for (int tile = cid; tile < p.total; tile += ncl, ++tc) {
       const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
@@ -239,10 +239,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int r0 = t.row0 + q * 32, cw = t.col0 + 32 * h;
       auto load_next = [&](int ci) {
         if (ci + 1 < kChunks) {
-          load_chunk_in<KIND>(p, t.mat, r0, cw + 64 * (ci + 1), lane, in);
+          load_chunk_in(p, t.mat, r0, cw + 64 * (ci + 1), lane, in);
         } else if (tile + ncl < p.total) {
           const NsTile tn = ns_tile<KIND, BN>(p, tile + ncl, rank);
-          load_chunk_in<KIND>(p, tn.mat, tn.row0 + q * 32, tn.col0 + 32 * h, lane, in);
+          load_chunk_in(p, tn.mat, tn.row0 + q * 32, tn.col0 + 32 * h, lane, in);
         }
       };
       if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
@@ -271,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           const ChunkIn<KIND> now = in;
           load_next(ci);
-          ns_chunk<KIND>(p, t, r0, c0, lane, ws, now, p.diag + static_cast<long long>(t.mat) * p.diag_n);
+          ns_chunk(p, t, r0, c0, lane, ws, now, p.diag + static_cast<long long>(t.mat) * p.diag_n);
         } else {
           load_next(ci);
         }

@@ -171,14 +171,28 @@ __device__ __forceinline__ void put_update1(const NsParams& p, long long u, floa
 // as they are used, two chunks ahead, was slower (an apply product of 8 x 7168
 // x 2048 404 instead of 310 us), since a warp waits on few counters of loads
 // in flight and then waits for the youngest of those that share one.
-template <int KIND>
+// LATE: the weight follows when the chunk is worked on.
+template <int KIND, bool LATE = false>
 struct ChunkIn {
   uint4 hi[4], lo[4];
-  uint4 w[KIND == kUpdate ? 4 : 1][2];   // the weight (rows that vectors divide)
+  uint4 w[KIND == kUpdate && !LATE ? 4 : 1][2];   // the weight (rows that vectors divide)
 };
 
-template <int KIND>
-__device__ __forceinline__ void load_chunk_in(const NsParams& p, int mat, int r0, int c0, int lane, ChunkIn<KIND>& in) {
+// 8 columns of the caller's weight.
+__device__ __forceinline__ void load_weight8(const NsParams& p, int mat, int r, int c, uint4 (&w)[2]) {
+  if (p.ucols % 8 == 0 && r < p.rows && c < p.ucols) {
+    const long long u = (static_cast<long long>(mat) * p.rows + r) * p.ucols + c;
+    if (p.weight_f32) {
+      w[0] = reinterpret_cast<const uint4*>(static_cast<const float*>(p.weight) + u)[0];
+      w[1] = reinterpret_cast<const uint4*>(static_cast<const float*>(p.weight) + u)[1];
+    } else {
+      w[0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.weight) + u);
+    }
+  }
+}
+
+template <int KIND, bool LATE>
+__device__ __forceinline__ void load_chunk_in(const NsParams& p, int mat, int r0, int c0, int lane, ChunkIn<KIND, LATE>& in) {
   if constexpr (KIND == kGram) return;
   const int c = c0 + (lane & 3) * 8;
 #pragma unroll
@@ -190,17 +204,7 @@ __device__ __forceinline__ void load_chunk_in(const NsParams& p, int mat, int r0
       in.hi[it] = *reinterpret_cast<const uint4*>(p.in_hi + at);
       if constexpr (KIND >= kApply) in.lo[it] = *reinterpret_cast<const uint4*>(p.in_lo + at);
     }
-    if constexpr (KIND == kUpdate) {
-      if (p.ucols % 8 == 0 && r < p.rows && c < p.ucols) {
-        const long long u = (static_cast<long long>(mat) * p.rows + r) * p.ucols + c;
-        if (p.weight_f32) {
-          in.w[it][0] = reinterpret_cast<const uint4*>(static_cast<const float*>(p.weight) + u)[0];
-          in.w[it][1] = reinterpret_cast<const uint4*>(static_cast<const float*>(p.weight) + u)[1];
-        } else {
-          in.w[it][0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.weight) + u);
-        }
-      }
-    }
+    if constexpr (KIND == kUpdate && !LATE) load_weight8(p, mat, r, c, in.w[it]);
   }
 }
 
@@ -208,9 +212,9 @@ __device__ __forceinline__ void load_chunk_in(const NsParams& p, int mat, int r0
 // ws.  Lanes take 8 columns of 8 rows at a time, so that the accesses of a
 // warp cover whole 64-byte (FP16) or 128-byte (FP32) pieces of rows.  d: the
 // matrix's diagonal of B (apply).
-template <int KIND>
+template <int KIND, bool LATE>
 __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int r0, int c0, int lane, float* ws,
-                                         const ChunkIn<KIND>& in, const float* d) {
+                                         const ChunkIn<KIND, LATE>& in, const float* d) {
   const int quad = (lane & 3) * 2, c = c0 + (lane & 3) * 8;
   const bool mirror = (KIND == kGram || KIND == kPoly) && (c0 >> 7) > (r0 >> 7);
 #pragma unroll
@@ -262,7 +266,13 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int
         if (inside && c < p.ucols) {
           const long long u = (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + c;
           if constexpr (KIND == kFinal) *reinterpret_cast<uint4*>(p.o16 + u) = pack_bf16x8(x, 1.0f / kSx);
-          else put_weight8(p, u, x, in.w[it]);
+          else if constexpr (!LATE) {
+            put_weight8(p, u, x, in.w[it]);
+          } else {
+            uint4 w[2];
+            load_weight8(p, t.mat, r, c, w);
+            put_weight8(p, u, x, w);
+          }
         }
       } else {
         chunk_quad(ws, rr, quad) = make_float4(x[0], x[1], x[2], x[3]);

@@ -43,9 +43,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kSlots = 4, kSlotBytes = 2 * 128 * 128;
+constexpr int kSlots = 3, kSlotBytes = 2 * 128 * 128;
+constexpr int kSmallWarps = 16, kSmallThreads = 32 * (2 + kSmallWarps);   // epilogue warps
 constexpr int kRegion = 4 * 128 * 128;   // A or B: 128 rows of 256 columns in 64-column chunks
-constexpr int kSmallSmem = 1024 + kSlots * kSlotBytes + kRegion + kEpiWarps * 4096 + 1024 + 256;
+constexpr int kSmallSmem = 1024 + kSlots * kSlotBytes + kRegion + kSmallWarps * 4096 + 1024 + 256;
 static_assert(kSmallSmem <= 232448, "shared memory per CTA");
 
 // Arrive on a barrier of CTA `rank`'s counterpart of `bar`, cluster-scope release.
@@ -80,8 +81,7 @@ __device__ __forceinline__ void st_cluster_f32(float* p, uint32_t rank, float v)
 }
 
 // A pair's tiles of the new X through its epilogue warps; KIND as in muon.cu.
-// Loads of X run one chunk ahead of their use (two ahead: registers spill, 120
-// instead of 97 us for 8 x 256 x 256).
+// Warp (q, h) has rows 32 q .. and columns 32 h .. and 128 + 32 h .. of a tile.
 template <int KIND>
 __device__ __forceinline__ bool small_apply(const SmallParams& sp, const NsParams& p, int mat, int rank, int pair, int q, int h,
                                             int lane, float* ws, uint64_t* tfull, uint32_t tempty0, uint32_t tmem,
@@ -94,47 +94,46 @@ __device__ __forceinline__ bool small_apply(const SmallParams& sp, const NsParam
     t.n = 256;
     const uint32_t acc = tc & 1, par = (tc >> 1) & 1;
     const int r0 = t.row0 + q * 32, cw = t.col0 + 32 * h;
-    ChunkIn<KIND> in;
-    load_chunk_in<KIND>(p, t.mat, r0, cw, lane, in);
+    ChunkIn<KIND, true> in;
+    load_chunk_in(p, mat, r0, cw, lane, in);
     if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], par, abort_flag, p.err))) return false;
     tc_fence_after();
     const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + 32 * h;
 #pragma unroll 1
-    for (int ci = 0; ci < 4; ++ci) {
-      const int c0 = cw + 64 * ci;
+    for (int ci = 0; ci < 2; ++ci) {
+      const int c0 = cw + 128 * ci;
       const bool skip = c0 >= p.cols || r0 >= p.rows;
       if (!skip) {
+        if (ci > 0) load_chunk_in(p, mat, r0, c0, lane, in);
         uint32_t v[32];
-        tmem_ld32(tbase + 64 * ci, v);
+        tmem_ld32(tbase + 128 * ci, v);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           chunk_quad(ws, lane, j) = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
                                                 __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
       }
-      if (ci == 3) {
+      if (ci == 1) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
       }
       if (!skip) {
         __syncwarp();
-        const ChunkIn<KIND> now = in;
-        if (ci < 3) load_chunk_in<KIND>(p, t.mat, r0, c0 + 64, lane, in);
-        ns_chunk<KIND>(p, t, r0, c0, lane, ws, now, d);
+        ns_chunk(p, t, r0, c0, lane, ws, in, d);
       }
     }
   }
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kSmallThreads, 1)
     muon_small_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant__ SmallParams sp) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* region = ring + kSlots * kSlotBytes;
   float* turn = reinterpret_cast<float*>(region + kRegion);
-  float* diag = turn + kEpiWarps * 1024;                                // [256]
+  float* diag = turn + kSmallWarps * 1024;                                // [256]
   uint64_t* full = reinterpret_cast<uint64_t*>(diag + 256);
   uint64_t* empty = full + kSlots;
   uint64_t* tfull = empty + kSlots;
@@ -158,11 +157,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpiWarps);
+      mbar_init(&tempty[a], 2 * kSmallWarps);
     }
-    mbar_init(ready, 2 * kEpiWarps);
-    mbar_init(dready, 2 * kEpiWarps);
-    mbar_init(xready, ctas * kEpiWarps);
+    mbar_init(ready, 2 * kSmallWarps);
+    mbar_init(dready, 2 * kSmallWarps);
+    mbar_init(xready, ctas * kSmallWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_fence_init();
@@ -362,13 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + 32 * h;
 #pragma unroll 1
-          for (int ci = 0; ci < 4; ++ci) {
-            const int c0 = 64 * ci + 32 * h;
+          for (int ci = 0; ci < 2; ++ci) {
+            const int c0 = 128 * ci + 32 * h;
             if (c0 >= used) continue;
             uint32_t v[32];
-            tmem_ld32(tbase + 64 * ci, v);
+            tmem_ld32(tbase + 128 * ci, v);
             tmem_ld_wait();
             uint8_t* chunk = mine + (c0 >> 6) * 16384;
+            float dv = 0.0f;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               uint4* at = reinterpret_cast<uint4*>(chunk + (((((c0 & 63) >> 3) + g) ^ (lr & 7)) << 4));
@@ -384,15 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                   x[j] = fmaf(cs, x[j], cb * a[j]);
-                  if (c0 + 8 * g + j == r) {   // the diagonal, in FP32 and in both CTAs
-                    const float dv = x[j] * (1.0f / kSb);
-                    st_cluster_f32(diag + r, lead, dv);
-                    st_cluster_f32(diag + r, lead + 1, dv);
-                    x[j] = 0.0f;
-                  }
+                  const bool on = c0 + 8 * g + j == r;   // the diagonal goes its own way
+                  dv = on ? x[j] : dv;
+                  x[j] = on ? 0.0f : x[j];
                 }
               }
               *at = make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+            }
+            if (product == 1 && c0 == r - lane) {   // in FP32 and in both CTAs
+              st_cluster_f32(diag + r, lead, dv * (1.0f / kSb));
+              st_cluster_f32(diag + r, lead + 1, dv * (1.0f / kSb));
             }
           }
           release(acc);
@@ -453,7 +454,7 @@ const int* small_clusters() {
       at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(2 << i);
-      cfg.blockDim = dim3(kThreads);
+      cfg.blockDim = dim3(kSmallThreads);
       cfg.dynamicSmemBytes = kSmallSmem;
       cfg.attrs = at;
       cfg.numAttrs = 1;
@@ -491,7 +492,7 @@ cudaError_t launch_muon_small(const SmallMaps& maps, const SmallParams& p, cudaS
   if (!most) return cudaErrorUnknown;
   void* args[2] = {const_cast<SmallMaps*>(&maps), const_cast<SmallParams*>(&p)};
   const int ctas = 2 * p.pairs, most_now = most[p.pairs == 4 ? 2 : p.pairs - 1];
-  return launch_dependent(small_kernel(), dim3(ctas * std::min(most_now, p.mats)), kThreads, kSmallSmem, stream, args, ctas);
+  return launch_dependent(small_kernel(), dim3(ctas * std::min(most_now, p.mats)), kSmallThreads, kSmallSmem, stream, args, ctas);
 }
 
 }  // namespace moe
