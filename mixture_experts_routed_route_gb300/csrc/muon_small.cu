@@ -14,13 +14,16 @@
 //
 // m x k, this kernel / tiled kernels, five steps and the two kernels before
 // them (results are equal bit by bit):
-//   8 x 256 x 256   97 / 119 us      64 x 256 x 256  107 / 183 us
-//   8 x 256 x 512  105 / 125         64 x 256 x 1024 262 / 380
-//   1 x 64 x 256    77 / 88          128 x 256 x 2048 1008 / 1224
-//   8 x 256 x 4096 284 / 275         40 x 256 x 2048  518 / 395   (not taken)
-// A step on one tile is about 17 us: loads, three products and three
-// epilogues one after the other, of which the last (hi and lo halves through
-// L2, 32 x 32 chunks) takes about 4 us a tile.
+//   8 x 256 x 256   85 / 119 us      64 x 256 x 256   95 / 180 us
+//   8 x 256 x 512   93 / 125         64 x 256 x 1024 237 / 369
+//   1 x 64 x 256    65 / 82          64 x 256 x 2048 447 / 614
+//   8 x 256 x 4096 263 / 271          1 x 256 x 4096 246 / 191  (not taken)
+// A step on one tile is about 34000 cycles: loads and the first product 3700,
+// A's epilogue 3000, the second product 3000, B's 4200, the diagonal's way to
+// both CTAs 1500, the third product (over hi and lo) 4500, X's epilogue 10000
+// (L2 latency of X, 32 x 32 chunks turned around in shared memory) and 2500
+// until its stores can be seen by the next step's loads.  Sixteen epilogue
+// warps: eight took 107 us instead of 96 at 8 x 512 x 256.
 //
 // Warp roles as in muon.cu.  Hand-overs:
 //   full / empty   ring of 32 KB operand boxes, loads of both CTAs complete on
@@ -470,10 +473,11 @@ const int* small_clusters() {
 // As many pairs as there are tiles, if the device runs clusters of that size
 // for all matrices at a time (a second round of clusters costs as much as the
 // first).  One tile a pair is always faster than the tiled kernels; with more
-// tiles a pair it is the share of busy SMs that decides, at about 0.6 of them
-// (0.4 with two tiles a pair): 24 x 256 x 2048, two pairs each, 257 us here and
-// 298 tiled; 16 x 256 x 2048 244 and 239; 16 x 256 x 1024 151 and 165; 90 x 256
-// x 2048, in two rounds, about 1010 and 940.
+// tiles a pair it is the share of busy SMs that decides: from 0.5 of them, or
+// 0.4 where up to four tiles a pair go through in one round.  Here and tiled:
+// 24 x 256 x 2048 (two pairs, 0.63) 236 and 295 us, 16 x 256 x 2048 (0.42) 223
+// and 235, 4 x 256 x 4096 (0.21) 252 and 218, 16 x 256 x 4096 (0.42, eight tiles
+// a pair) 392 and 388, 90 x 256 x 1024 (two rounds, 0.59) 444 and 518.
 int muon_small_pairs(int mats, int k) {
   const int* most = small_clusters();
   if (!most) return 0;
@@ -484,7 +488,7 @@ int muon_small_pairs(int mats, int k) {
   const int pairs = 1 << i, per = (tiles + pairs - 1) / pairs, rounds = (mats + most[i] - 1) / most[i];
   if (rounds == 1 && per == 1) return pairs;
   const float busy = static_cast<float>(mats) * pairs / (static_cast<float>(rounds) * most[0]);
-  return busy >= (rounds == 1 && per == 2 ? 0.4f : 0.6f) ? pairs : 0;
+  return busy >= (rounds == 1 && per <= 4 ? 0.4f : 0.5f) ? pairs : 0;
 }
 
 cudaError_t launch_muon_small(const SmallMaps& maps, const SmallParams& p, cudaStream_t stream) {
