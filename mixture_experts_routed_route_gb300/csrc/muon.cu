@@ -41,17 +41,16 @@
 // (8 x 7168 x 2048, 3.05 ms; the Gram product alone 1.8, the apply products
 // 1.5 with 320 us each), where a library product reaches 1.7 in a long run
 // under the power cap.  64 x 1408 x 2048 with the momentum and a float32
-// weight: 5.4 ms, of which 1.3 ms move gradient, momentum, X and weight.
-// Small ones (3 x 1000 x 1531, 228 us): the chain of 15 dependent launches of
+// weight: 5.3 ms, of which 1.3 ms move gradient, momentum, X and weight.
+// Small ones (3 x 1000 x 1531, 211 us): the chain of 15 dependent launches of
 // 10 to 17 us each.
 //
 // Warp roles: warp 0 TMA producer, warp 1 TMEM allocation and (rank 0) MMA
-// issue for the pair, warps 2 .. 9 epilogue (lane quadrant w % 4, every
-// other 32 columns of the tile, so that both warps of a quadrant are at
-// neighbouring pieces of their rows; what a chunk reads besides the
-// accumulator is asked for one chunk ahead, over the tile's end too: the
-// update of 64 x 1408 x 2048 790 to 722 us).  Both CTAs' loads complete on rank 0's
-// barrier of the stage.
+// issue for the pair, warps 2 .. 9 epilogue (lane quadrant w % 4; every other
+// 32 columns of the tile, or, of X, every other 64 in two halves of the rows).
+// What a chunk reads besides the accumulator is asked for one chunk ahead, over
+// the tile's end too: the update of 64 x 1408 x 2048 790 to 722 us.  Both
+// CTAs' loads complete on rank 0's barrier of the stage.
 #include <algorithm>
 
 #include "muon_core.cuh"
@@ -91,6 +90,17 @@ __device__ __forceinline__ NsTile ns_tile(const NsParams& p, int tile, int rank)
   t.col0 = i * BN;
   t.n = (BN == 256 && p.valid_cols - t.col0 <= 128) ? 128 : BN;
   return t;
+}
+
+// Chunk ci of epilogue warp (q, h).
+template <int KIND>
+__device__ __forceinline__ NsChunk ns_chunk_of(const NsTile& t, int q, int h, int ci) {
+  NsChunk k;
+  k.half = KIND >= kApply ? ci & 1 : 0;
+  k.tcol = KIND >= kApply ? 64 * (h + 2 * (ci >> 1)) : 32 * (h + 2 * ci);
+  k.row = t.row0 + 32 * q + 16 * k.half;
+  k.col = t.col0 + k.tcol;
+  return k;
 }
 
 template <int KIND, int BN>
@@ -231,37 +241,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ChunkIn<KIND> in;   // of the chunk at hand, from one chunk before it (of the tile before) on
     if (cid < p.total) {
       const NsTile t = ns_tile<KIND, BN>(p, cid, rank);
-      load_chunk_in(p, t.mat, t.row0 + q * 32, t.col0 + 32 * h, lane, in);
+      const NsChunk k = ns_chunk_of<KIND>(t, q, h, 0);
+      load_chunk_in(p, t.mat, k.row, k.col, lane, in);
     }
     for (int tile = cid; tile < p.total; tile += ncl, ++tc) {
       const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
       const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-      const int r0 = t.row0 + q * 32, cw = t.col0 + 32 * h;
       auto load_next = [&](int ci) {
         if (ci + 1 < kChunks) {
-          load_chunk_in(p, t.mat, r0, cw + 64 * (ci + 1), lane, in);
+          const NsChunk k = ns_chunk_of<KIND>(t, q, h, ci + 1);
+          load_chunk_in(p, t.mat, k.row, k.col, lane, in);
         } else if (tile + ncl < p.total) {
           const NsTile tn = ns_tile<KIND, BN>(p, tile + ncl, rank);
-          load_chunk_in(p, tn.mat, tn.row0 + q * 32, tn.col0 + 32 * h, lane, in);
+          const NsChunk k = ns_chunk_of<KIND>(tn, q, h, 0);
+          load_chunk_in(p, tn.mat, k.row, k.col, lane, in);
         }
       };
       if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
       tc_fence_after();
-      const uint32_t tbase = tmem + acc * BN + (static_cast<uint32_t>(q * 32) << 16) + 32 * h;
+      const uint32_t tbase = tmem + acc * BN + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
       for (int ci = 0; ci < kChunks; ++ci) {
-        const int c0 = cw + 64 * ci;
+        const NsChunk k = ns_chunk_of<KIND>(t, q, h, ci);
         // a symmetric output's blocks below the diagonal are their mirrors'
-        const bool skip = c0 >= p.cols || ((KIND == kGram || KIND == kPoly) && (c0 >> 7) < (t.row0 >> 7));
-        if (!skip) {
-          uint32_t v[32];
-          tmem_ld32(tbase + 64 * ci, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            chunk_quad(ws, lane, j) = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                                  __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-        }
+        const bool skip = k.col >= p.cols || ((KIND == kGram || KIND == kPoly) && (k.col >> 7) < (t.row0 >> 7));
+        if (!skip) chunk_in<KIND>(tbase + k.tcol, k.half, lane, ws);
         if (ci == kChunks - 1) {   // every column has been read: the accumulator is free
           tc_fence_before();
           __syncwarp();
@@ -271,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           const ChunkIn<KIND> now = in;
           load_next(ci);
-          ns_chunk(p, t, r0, c0, lane, ws, now, p.diag + static_cast<long long>(t.mat) * p.diag_n);
+          ns_chunk(p, t, k.row, k.col, lane, ws, now, p.diag + static_cast<long long>(t.mat) * p.diag_n);
         } else {
           load_next(ci);
         }
@@ -630,7 +634,7 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
                     sgrid, kMixThreads, 0, stream, sargs) != cudaSuccess)
       return MOE_ERR_CUDA;
 
-    const int pairs = L.split ? muon_small_pairs(n, L.k) : 0;
+    const int pairs = L.split ? muon_small_pairs(n, L.m, L.k) : 0;
     if (pairs > 0) {
       SmallParams q{};
       q.mats = n;

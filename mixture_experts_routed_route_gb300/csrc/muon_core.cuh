@@ -98,12 +98,46 @@ __device__ __forceinline__ void store_hi_lo(__half* hi, __half* lo, const float*
   *reinterpret_cast<uint4*>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// A 32 x 32 chunk of FP32 in a warp's 4 KB: float4 slot j of row r at slot
-// j ^ (r % 8), so that row writes, row reads and column reads spread over the
-// banks.
+// A chunk of FP32 in a warp's 4 KB: 32 rows x 32 columns, or (X) 16 rows x 64
+// columns, whose rows are whole 128-byte lines of X's halves: an L1 access
+// takes a cycle a line, which halves the loads' and stores' share (3 x 1000 x
+// 1531 217 to 210 us, 4 x 1408 x 2048 434 to 418 us).  float4
+// slots are spread over the banks: slot j of row r at j ^ (r % 8), or the even
+// slots at (j / 2) ^ (r % 8), the odd ones 8 further.
 __device__ __forceinline__ int chunk_at(int r, int c) { return r * 32 + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3)); }
 __device__ __forceinline__ float4& chunk_quad(float* ws, int r, int quad) {
   return *reinterpret_cast<float4*>(ws + r * 32 + ((quad ^ (r & 7)) << 2));
+}
+__device__ __forceinline__ int wide_slot(int r, int quad) { return (((quad >> 1) ^ (r & 7)) | ((quad & 1) << 3)) << 2; }
+__device__ __forceinline__ float4& wide_quad(float* ws, int r, int quad) {
+  return *reinterpret_cast<float4*>(ws + r * 64 + wide_slot(r, quad));
+}
+
+// A chunk in its tile.
+struct NsChunk {
+  int row, col, tcol;   // output row and column, column in the tile
+  int half;             // of the quadrant's 32 rows (X)
+};
+
+// The chunk's accumulators (tmem: lane quadrant and column of the chunk) to ws.
+template <int KIND>
+__device__ __forceinline__ void chunk_in(uint32_t tmem, int half, int lane, float* ws) {
+#pragma unroll 1
+  for (int part = 0; part < (KIND >= kApply ? 2 : 1); ++part) {
+    uint32_t v[32];
+    tmem_ld32(tmem + 32 * part, v);
+    tmem_ld_wait();
+    if (KIND < kApply || (lane >> 4) == half) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 x = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                     __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+        if (KIND >= kApply) wide_quad(ws, lane & 15, 8 * part + j) = x;
+        else chunk_quad(ws, lane, j) = x;
+      }
+    }
+    __syncwarp();
+  }
 }
 
 __device__ __forceinline__ void store_half8(__half* p, const float (&x)[8]) {
@@ -166,7 +200,7 @@ __device__ __forceinline__ void put_update1(const NsParams& p, long long u, floa
   if (p.w16) p.w16[u] = __float2bfloat16_rn(w);
 }
 
-// What a chunk needs besides the accumulator: 8 columns of rows lane / 4 + 8 it.
+// What a chunk needs besides the accumulator: 8 columns of four rows a lane.
 // All of a chunk's loads are sent together: refilling the registers row by row
 // as they are used, two chunks ahead, was slower (an apply product of 8 x 7168
 // x 2048 404 instead of 310 us), since a warp waits on few counters of loads
@@ -194,10 +228,11 @@ __device__ __forceinline__ void load_weight8(const NsParams& p, int mat, int r, 
 template <int KIND, bool LATE>
 __device__ __forceinline__ void load_chunk_in(const NsParams& p, int mat, int r0, int c0, int lane, ChunkIn<KIND, LATE>& in) {
   if constexpr (KIND == kGram) return;
-  const int c = c0 + (lane & 3) * 8;
+  constexpr int kLanes = KIND >= kApply ? 8 : 4;   // of a row
+  const int c = c0 + (lane % kLanes) * 8;
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
-    const int r = r0 + it * 8 + (lane >> 2);
+    const int r = r0 + it * (32 / kLanes) + lane / kLanes;
     in.hi[it] = in.lo[it] = make_uint4(0, 0, 0, 0);
     if (r < p.rows && c < p.cols) {
       const long long at = mat * p.mat + r * p.pitch + c;
@@ -208,19 +243,20 @@ __device__ __forceinline__ void load_chunk_in(const NsParams& p, int mat, int r0
   }
 }
 
-// The 32 x 32 chunk at rows r0, columns c0, whose accumulator values are in
-// ws.  Lanes take 8 columns of 8 rows at a time, so that the accesses of a
-// warp cover whole 64-byte (FP16) or 128-byte (FP32) pieces of rows.  d: the
-// matrix's diagonal of B (apply).
+// The chunk at rows r0, columns c0, whose accumulator values are in ws.  A
+// lane takes 8 columns of a row at a time.  d: the matrix's diagonal of B
+// (apply).
 template <int KIND, bool LATE>
 __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int r0, int c0, int lane, float* ws,
                                          const ChunkIn<KIND, LATE>& in, const float* d) {
-  const int quad = (lane & 3) * 2, c = c0 + (lane & 3) * 8;
+  constexpr int kLanes = KIND >= kApply ? 8 : 4;   // of a row
+  const int quad = (lane % kLanes) * 2, c = c0 + (lane % kLanes) * 8;
   const bool mirror = (KIND == kGram || KIND == kPoly) && (c0 >> 7) > (r0 >> 7);
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
-    const int rr = it * 8 + (lane >> 2), r = r0 + rr;
-    const float4 a = chunk_quad(ws, rr, quad), b = chunk_quad(ws, rr, quad + 1);
+    const int rr = it * (32 / kLanes) + lane / kLanes, r = r0 + rr;
+    const float4 a = KIND >= kApply ? wide_quad(ws, rr, quad) : chunk_quad(ws, rr, quad);
+    const float4 b = KIND >= kApply ? wide_quad(ws, rr, quad + 1) : chunk_quad(ws, rr, quad + 1);
     float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     const bool inside = r < p.rows && c < p.cols;
     const long long at = t.mat * p.mat + r * p.pitch + c;
@@ -275,19 +311,23 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int
           }
         }
       } else {
-        chunk_quad(ws, rr, quad) = make_float4(x[0], x[1], x[2], x[3]);
-        chunk_quad(ws, rr, quad + 1) = make_float4(x[4], x[5], x[6], x[7]);
+        wide_quad(ws, rr, quad) = make_float4(x[0], x[1], x[2], x[3]);
+        wide_quad(ws, rr, quad + 1) = make_float4(x[4], x[5], x[6], x[7]);
       }
     }
   }
-  if (KIND >= kFinal && p.ucols % 8 != 0) {   // rows that no vector divides: a lane a column
+  if (KIND >= kFinal && p.ucols % 8 != 0) {   // rows that no vector divides: a lane two columns
     __syncwarp();
-    const int cc = c0 + lane;
 #pragma unroll 4
-    for (int rr = 0; rr < 32; ++rr) {
+    for (int rr = 0; rr < 16; ++rr) {
       const int r = r0 + rr;
-      if (r < p.rows && cc < p.ucols)
-        put_update1(p, (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + cc, ws[chunk_at(rr, lane)]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c1 = lane + 32 * k, cc = c0 + c1;
+        if (r < p.rows && cc < p.ucols)
+          put_update1(p, (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + cc,
+                      ws[rr * 64 + wide_slot(rr, c1 >> 2) + (c1 & 3)]);
+      }
     }
   }
   if (mirror) {   // rows c0 .. c0 + 31 of the image, columns r0 .. r0 + 31
@@ -336,9 +376,9 @@ struct SmallParams {
   float decay, rate;
   uint32_t* err;
 };
-// Pairs per matrix for `mats` matrices whose larger size is k, or 0: the tiled
+// Pairs per matrix for `mats` matrices of sizes m <= k, or 0: the tiled
 // kernels are the faster ones.
-int muon_small_pairs(int mats, int k);
+int muon_small_pairs(int mats, int m, int k);
 cudaError_t launch_muon_small(const SmallMaps& maps, const SmallParams& p, cudaStream_t stream);
 
 }  // namespace moe

@@ -14,15 +14,15 @@
 //
 // m x k, this kernel / tiled kernels, five steps and the two kernels before
 // them (results are equal bit by bit):
-//   8 x 256 x 256   85 / 119 us      64 x 256 x 256   95 / 180 us
-//   8 x 256 x 512   93 / 125         64 x 256 x 1024 237 / 369
+//   8 x 256 x 256   83 / 119 us      64 x 256 x 256   92 / 180 us
+//   8 x 256 x 512   90 / 125         64 x 256 x 1024 231 / 369
 //   1 x 64 x 256    65 / 82          64 x 256 x 2048 447 / 614
-//   8 x 256 x 4096 263 / 271          1 x 256 x 4096 246 / 191  (not taken)
-// A step on one tile is about 34000 cycles: loads and the first product 3700,
+//   8 x 256 x 4096 259 / 271          1 x 256 x 4096 246 / 191  (not taken)
+// A step on one tile is about 33000 cycles: loads and the first product 3700,
 // A's epilogue 3000, the second product 3000, B's 4200, the diagonal's way to
-// both CTAs 1500, the third product (over hi and lo) 4500, X's epilogue 10000
-// (L2 latency of X, 32 x 32 chunks turned around in shared memory) and 2500
-// until its stores can be seen by the next step's loads.  Sixteen epilogue
+// both CTAs 1500, the third product (over hi and lo) 4500, X's epilogue 9000
+// (X through L2, a cycle of L1 a line, the chunks turned around in shared
+// memory) and 1500 until its stores can be seen by the next step's loads.  Sixteen epilogue
 // warps: eight took 107 us instead of 96 at 8 x 512 x 256.
 //
 // Warp roles as in muon.cu.  Hand-overs:
@@ -84,11 +84,15 @@ __device__ __forceinline__ void st_cluster_f32(float* p, uint32_t rank, float v)
 }
 
 // A pair's tiles of the new X through its epilogue warps; KIND as in muon.cu.
-// Warp (q, h) has rows 32 q .. and columns 32 h .. and 128 + 32 h .. of a tile.
+// Of a tile, warp (q, h) has rows 32 q .. and columns 64 h .., in two halves of
+// the rows; where X has no more than 64 or 128 columns the warps of a quadrant
+// share those.
 template <int KIND>
 __device__ __forceinline__ bool small_apply(const SmallParams& sp, const NsParams& p, int mat, int rank, int pair, int q, int h,
                                             int lane, float* ws, uint64_t* tfull, uint32_t tempty0, uint32_t tmem,
                                             uint32_t& tc, const float* d, volatile int* abort_flag) {
+  const int share = !sp.tall || p.cols > 128 ? 2 : p.cols > 64 ? 1 : 0;
+  const int tcol = 64 * (h & ((1 << share) - 1)), half0 = h >> share;
   for (int tile = pair; tile < sp.tiles; tile += sp.pairs, ++tc) {
     NsTile t;
     t.mat = mat;
@@ -96,26 +100,17 @@ __device__ __forceinline__ bool small_apply(const SmallParams& sp, const NsParam
     t.col0 = sp.tall ? 0 : tile * 256;
     t.n = 256;
     const uint32_t acc = tc & 1, par = (tc >> 1) & 1;
-    const int r0 = t.row0 + q * 32, cw = t.col0 + 32 * h;
     ChunkIn<KIND, true> in;
-    load_chunk_in(p, mat, r0, cw, lane, in);
+    const int r0 = t.row0 + 32 * q + 16 * half0, c0 = t.col0 + tcol;
+    load_chunk_in(p, mat, r0, c0, lane, in);
     if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], par, abort_flag, p.err))) return false;
     tc_fence_after();
-    const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + 32 * h;
+    const uint32_t tbase = tmem + acc * 256 + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
     for (int ci = 0; ci < 2; ++ci) {
-      const int c0 = cw + 128 * ci;
-      const bool skip = c0 >= p.cols || r0 >= p.rows;
-      if (!skip) {
-        if (ci > 0) load_chunk_in(p, mat, r0, c0, lane, in);
-        uint32_t v[32];
-        tmem_ld32(tbase + 128 * ci, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          chunk_quad(ws, lane, j) = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                                __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-      }
+      const bool skip = c0 >= p.cols || r0 + 16 * ci >= p.rows || half0 + ci > (share == 2 ? 1 : half0 & 1);
+      if (!skip && ci > 0) load_chunk_in(p, mat, r0 + 16, c0, lane, in);
+      if (!skip) chunk_in<KIND>(tbase + tcol, half0 + ci, lane, ws);
       if (ci == 1) {
         tc_fence_before();
         __syncwarp();
@@ -123,7 +118,7 @@ __device__ __forceinline__ bool small_apply(const SmallParams& sp, const NsParam
       }
       if (!skip) {
         __syncwarp();
-        ns_chunk(p, t, r0, c0, lane, ws, in, d);
+        ns_chunk(p, t, r0 + 16 * ci, c0, lane, ws, in, d);
       }
     }
   }
@@ -473,12 +468,13 @@ const int* small_clusters() {
 // As many pairs as there are tiles, if the device runs clusters of that size
 // for all matrices at a time (a second round of clusters costs as much as the
 // first).  One tile a pair is always faster than the tiled kernels; with more
-// tiles a pair it is the share of busy SMs that decides: from 0.5 of them, or
-// 0.4 where up to four tiles a pair go through in one round.  Here and tiled:
-// 24 x 256 x 2048 (two pairs, 0.63) 236 and 295 us, 16 x 256 x 2048 (0.42) 223
-// and 235, 4 x 256 x 4096 (0.21) 252 and 218, 16 x 256 x 4096 (0.42, eight tiles
-// a pair) 392 and 388, 90 x 256 x 1024 (two rounds, 0.59) 444 and 518.
-int muon_small_pairs(int mats, int k) {
+// tiles a pair it is the share of busy SMs that decides: from 0.4 of them where
+// up to four tiles a pair go through in one round, else from 0.5, or 0.6 where
+// m leaves half of the epilogue warps without rows.  Here and tiled: 24 x 256 x
+// 2048 (two pairs, 0.63) 231 and 295 us, 16 x 256 x 2048 (0.42) 218 and 235,
+// 4 x 256 x 4096 (0.21) 252 and 218, 90 x 256 x 1024 (two rounds, 0.59) 432 and
+// 518, 40 x 64 x 4096 (0.53, sixteen tiles a pair) 525 and 462.
+int muon_small_pairs(int mats, int m, int k) {
   const int* most = small_clusters();
   if (!most) return 0;
   const int tiles = (k + 255) / 256;
@@ -488,7 +484,7 @@ int muon_small_pairs(int mats, int k) {
   const int pairs = 1 << i, per = (tiles + pairs - 1) / pairs, rounds = (mats + most[i] - 1) / most[i];
   if (rounds == 1 && per == 1) return pairs;
   const float busy = static_cast<float>(mats) * pairs / (static_cast<float>(rounds) * most[0]);
-  return busy >= (rounds == 1 && per <= 4 ? 0.4f : 0.5f) ? pairs : 0;
+  return busy >= (rounds == 1 && per <= 4 ? 0.4f : m > 128 ? 0.5f : 0.6f) ? pairs : 0;
 }
 
 cudaError_t launch_muon_small(const SmallMaps& maps, const SmallParams& p, cudaStream_t stream) {
