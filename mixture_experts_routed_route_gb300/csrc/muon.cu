@@ -264,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int ci = 0; ci < kChunks; ++ci) {
         const NsChunk k = ns_chunk_of<KIND>(t, q, h, ci);
         // a symmetric output's blocks below the diagonal are their mirrors'
-        const bool skip = k.col >= p.cols || ((KIND == kGram || KIND == kPoly) && (k.col >> 7) < (t.row0 >> 7));
+        const bool skip = k.col >= p.cols || (KIND >= kApply ? k.row >= p.rows : (k.col >> 7) < (t.row0 >> 7));
         if (!skip) chunk_in<KIND>(tbase + k.tcol, k.half, lane, ws);
         if (ci == kChunks - 1) {   // every column has been read: the accumulator is free
           tc_fence_before();

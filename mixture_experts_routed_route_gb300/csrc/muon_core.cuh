@@ -181,22 +181,11 @@ __device__ __forceinline__ void put_weight8(const NsParams& p, long long u, cons
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.weight) + u) = pack_bf16x8(w, 1.0f);
   }
 }
-__device__ __forceinline__ void put_update1(const NsParams& p, long long u, float x) {
-  if (p.o16) {
-    p.o16[u] = __float2bfloat16_rn(x * (1.0f / kSx));
-    return;
-  }
-  const float rate = -p.rate * (1.0f / kSx);
-  float w;
-  if (p.weight_f32) {
-    float* q = static_cast<float*>(p.weight) + u;
-    w = fmaf(p.decay, *q, rate * x);
-    *q = w;
-  } else {
-    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.weight) + u;
-    w = fmaf(p.decay, __bfloat162float(*q), rate * x);
-    *q = __float2bfloat16_rn(w);
-  }
+// One value, where rows start anywhere; w: the weight there.
+__device__ __forceinline__ void put_update1(const NsParams& p, long long u, float x, float w) {
+  w = fmaf(p.decay, w, -p.rate * (1.0f / kSx) * x);
+  if (p.weight_f32) static_cast<float*>(p.weight)[u] = w;
+  else static_cast<__nv_bfloat16*>(p.weight)[u] = __float2bfloat16_rn(w);
   if (p.w16) p.w16[u] = __float2bfloat16_rn(w);
 }
 
@@ -316,17 +305,36 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, int
       }
     }
   }
-  if (KIND >= kFinal && p.ucols % 8 != 0) {   // rows that no vector divides: a lane two columns
+  if (KIND >= kFinal && p.ucols % 8 != 0) {
+    // rows that no vector divides: a lane two columns of four rows at a time,
+    // whose weights are all asked for before the first is written (one by one
+    // the last product of 40 x 63 x 7169 took 1027 us instead of 552)
     __syncwarp();
-#pragma unroll 4
-    for (int rr = 0; rr < 16; ++rr) {
-      const int r = r0 + rr;
+#pragma unroll 1
+    for (int rb = 0; rb < 16; rb += 4) {
+      float w[8];
+      auto weights = [&](const auto* from) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c1 = lane + 32 * k, cc = c0 + c1;
-        if (r < p.rows && cc < p.ucols)
-          put_update1(p, (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + cc,
-                      ws[rr * 64 + wide_slot(rr, c1 >> 2) + (c1 & 3)]);
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + rb + (k >> 1), cc = c0 + lane + 32 * (k & 1);
+          w[k] = 0.0f;
+          if (r < p.rows && cc < p.ucols)
+            w[k] = static_cast<float>(from[(static_cast<long long>(t.mat) * p.rows + r) * p.ucols + cc]);
+        }
+      };
+      if constexpr (KIND == kUpdate) {
+        if (p.weight_f32) weights(static_cast<const float*>(p.weight));
+        else weights(static_cast<const __nv_bfloat16*>(p.weight));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int rr = rb + (k >> 1), r = r0 + rr, c1 = lane + 32 * (k & 1), cc = c0 + c1;
+        if (r < p.rows && cc < p.ucols) {
+          const long long u = (static_cast<long long>(t.mat) * p.rows + r) * p.ucols + cc;
+          const float x1 = ws[rr * 64 + wide_slot(rr, c1 >> 2) + (c1 & 3)];
+          if constexpr (KIND == kUpdate) put_update1(p, u, x1, w[k]);
+          else p.o16[u] = __float2bfloat16_rn(x1 * (1.0f / kSx));
+        }
       }
     }
   }
