@@ -711,10 +711,15 @@ MOE_API moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const
  * which moves every singular value s through a s + b s^3 + c s^5.
  * Precision: FP16 tensor-core products with FP32 accumulation; X is kept to
  * 22 bits and the polynomial's diagonal in FP32 between them.  After five
- * steps the result is within about 1e-3 of the exact one in norm.  Singular
- * values have to stay below 8 on the way (they do for polynomials that map
- * [0, 1] into itself or a little above); beyond that the result is NaN or
- * infinite.  A zero matrix gives zeros.  |U|_F is an FP32 sum of squares.
+ * steps the result is within about 1e-3 of the exact one in norm.
+ * Range of those formats: before each step every element of X has to be below
+ * 15.9 in magnitude, every element of A below 127, and every element of b A +
+ * c A A off its diagonal below 127; beyond that the result is NaN or infinite.
+ * Singular values s of X up to 11 keep X and A within it, and b s^2 + c s^4
+ * with values less than 250 apart over them and 0 keeps B (polynomials that
+ * map [0, 1] into itself or a little above stay far below).  The last step's
+ * result has no such limit.
+ * A zero matrix gives zeros.  |U|_F is an FP32 sum of squares.
  *
  * moe_orthogonalize: out (bf16 [batch, rows, cols]) from x (x_type).
  * moe_muon_update, in place on weight and momentum:

@@ -21,10 +21,12 @@
 // the other regime, X near orthogonal: there A is close to a multiple of
 // the identity, and one rounding of B's almost equal diagonal entries
 // scales the whole of X (Gaussian matrices: 1.6e-3 without, 7e-4 with).
-// X is stored times 2^12, A and B times 2^11 (exact powers of two), so that
-// FP16 keeps its 11 bits down to elements of 1.5e-8 of X, and B's
-// off-diagonal elements (below 32 for |coefficients| of this kind of
-// polynomial) stay in range.
+// X is stored times 2^12, A and B times 2^9 (exact powers of two), so that
+// FP16 keeps its 11 bits down to elements of 1.5e-8 of X and 1.2e-7 of A and
+// B (with 2^11 for these the errors above are the same to three digits), and
+// has room for elements of X up to 15.9, of A up to 127 (X's singular values
+// up to 11, as A_ij <= s^2) and of B off its diagonal up to 127 (half the
+// spread of B's eigenvalues b s^2 + c s^4 at most).
 //
 // Matrices with m <= 256 may go through all steps in one launch instead
 // (muon_small.cu).  Otherwise each product is one persistent launch over

@@ -14,7 +14,7 @@ namespace moe {
 namespace {
 
 constexpr float kSx = 4096.0f;   // stored X = X * kSx
-constexpr float kSb = 2048.0f;   // stored A, B = A, B * kSb
+constexpr float kSb = 512.0f;    // stored A, B = A, B * kSb
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kMaxSteps = MOE_MUON_MAX_STEPS;
