@@ -718,7 +718,9 @@ MOE_API moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const
  * Singular values s of X up to 11 keep X and A within it, and b s^2 + c s^4
  * with values less than 250 apart over them and 0 keeps B (polynomials that
  * map [0, 1] into itself or a little above stay far below).  The last step's
- * result has no such limit.
+ * result has no such limit.  Coefficients of up to 16 in magnitude are taken
+ * as they are; a schedule with larger ones is taken if it keeps all of [0, 1]
+ * in that range with half a percent to spare after each step.
  * A zero matrix gives zeros.  |U|_F is an FP32 sum of squares.
  *
  * moe_orthogonalize: out (bf16 [batch, rows, cols]) from x (x_type).
@@ -737,9 +739,10 @@ MOE_API moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const
  * device_error_word: as for moe_forward_static_scratch (a device wait that
  * ran out of time sets MOE_DEV_ERR_TIMEOUT; never cleared here).
  * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, batch < 0, sizes
- * < 1, steps outside [1, MOE_MUON_MAX_STEPS], |coefficient| > 16, eps not
- * finite and positive, unknown types, rates not finite), MOE_ERR_UNSUPPORTED
- * (rows or cols above 65536).  batch may be 0.
+ * < 1, steps outside [1, MOE_MUON_MAX_STEPS], coefficients not finite or
+ * above 16 and not known to stay in range, eps not finite and positive,
+ * unknown types, rates not finite), MOE_ERR_UNSUPPORTED (rows or cols above
+ * 65536).  batch may be 0.
  */
 #define MOE_MUON_MAX_STEPS 16
 typedef struct {

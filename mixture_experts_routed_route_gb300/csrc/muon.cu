@@ -54,6 +54,7 @@
 // the tile's end too: the update of 64 x 1408 x 2048 790 to 722 us.  Both
 // CTAs' loads complete on rank 0's barrier of the stage.
 #include <algorithm>
+#include <cmath>
 
 #include "muon_core.cuh"
 
@@ -479,14 +480,47 @@ NsLayout ns_layout(const moe_muon_config* c) {
   return L;
 }
 
+// Whether the steps keep every matrix's X, A and B within their formats: the
+// singular values start in [0, 1] (1 for a matrix of rank one), X's and A's
+// elements are at most s and s^2, and B's off its diagonal half the spread of
+// b s^2 + c s^4.  The limits leave 6 % to FP16's, and each step's range half a
+// percent for rounding: hi and A move A by 3 x 2^-12, X by that times b s^2 +
+// 2 c s^4, 0.4 % at the end of steep steps.
+bool schedule_in_range(const moe_muon_config* c) {
+  double top = 1.0;   // largest singular value before the step
+  for (int s = 0; s < c->steps; ++s) {
+    const double a = c->coefficients[s][0], b = c->coefficients[s][1], q = c->coefficients[s][2], t = top * top;
+    if (!(top <= 15.0 && t <= 120.0)) return false;
+    const double peak = q != 0.0 ? -b / (2.0 * q) : 0.0;   // of b t + c t^2
+    const double end = (b + q * t) * t, turn = peak > 0.0 && peak < t ? (b + q * peak) * peak : 0.0;
+    if (!(std::max({0.0, end, turn}) - std::min({0.0, end, turn}) <= 240.0)) return false;
+    auto value = [&](double x2) { return std::fabs((a + (b + q * x2) * x2) * std::sqrt(x2)); };
+    double most = value(t);
+    // turning points: a + 3 b x^2 + 5 c x^4 = 0
+    const double d = 9.0 * b * b - 20.0 * a * q;
+    if (q != 0.0 && d >= 0.0) {
+      for (double sign : {-1.0, 1.0}) {
+        const double x2 = (-3.0 * b + sign * std::sqrt(d)) / (10.0 * q);
+        if (x2 > 0.0 && x2 < t) most = std::max(most, value(x2));
+      }
+    } else if (q == 0.0 && b != 0.0) {
+      const double x2 = -a / (3.0 * b);
+      if (x2 > 0.0 && x2 < t) most = std::max(most, value(x2));
+    }
+    if (!std::isfinite(most)) return false;
+    top = 1.005 * most;
+  }
+  return true;
+}
+
 bool muon_config_ok(const moe_muon_config* c) {
   if (!c || c->batch < 0 || c->rows < 1 || c->cols < 1) return false;
   if (c->steps < 1 || c->steps > kMaxSteps) return false;
   if (!(c->eps > 0.0f) || c->eps > 3.0e38f) return false;
+  bool small = true;
   for (int s = 0; s < c->steps; ++s)
-    for (int j = 0; j < 3; ++j)
-      if (!(c->coefficients[s][j] >= -16.0f && c->coefficients[s][j] <= 16.0f)) return false;
-  return true;
+    for (int j = 0; j < 3; ++j) small = small && c->coefficients[s][j] >= -16.0f && c->coefficients[s][j] <= 16.0f;
+  return small || schedule_in_range(c);
 }
 
 // A CTA pair's matrix sizes: box coordinates and chunk counts are ints.

@@ -1,5 +1,6 @@
 """The range of the orthogonalised updates: singular values up to the stated
-limits on the way, on the tiled and the small kernel, wide and tall.
+limits on the way, and schedules with steep polynomials, on the tiled and the
+small kernel, wide and tall.
 
 Bounds.  Where every product is exact in the kernel's formats (powers of two
 and small whole numbers) the result has to be the exact value rounded to
@@ -8,7 +9,7 @@ BF16.  Else as in test_gpu_muon.py."""
 import pytest
 import torch
 
-from test_gpu_muon import BOUND, ns64, off
+from test_gpu_muon import BOUND, gradient, ns64, off
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,22 @@ def test_polynomials_with_large_elements_off_the_diagonal(E, N, K):
     want = torch.zeros_like(u)
     want[:, 3:5, 8:10] = 0.5 * 4.0 * (1 + 15.0 * 16.0)
     assert torch.equal(out, want.bfloat16())
+
+
+# 0 to 1 goes to 1.96 at most on the way, and to 1.12 at most in the end
+STEEP = [(8.205, -22.902, 16.461), (4.066, -2.861, 0.518), (3.91, -2.823, 0.525), (3.286, -2.415, 0.485), (2.278, -1.62, 0.398)]
+
+
+@pytest.mark.parametrize("E,N,K", SHAPES + [(3, 1000, 1531), (8, 512, 256)])
+def test_schedule_with_a_steep_first_step(E, N, K):
+    """Coefficients beyond 16 where the schedule keeps [0, 1] in range."""
+    from mixture_experts_routed_route_gb300 import optim
+    for u in (gradient(E, N, K, seed=4), torch.randn((E, N, K), device="cuda", generator=torch.Generator("cuda").manual_seed(5))):
+        assert off(optim.orthogonalize(u, steps=5, coefficients=STEEP), ns64(u, 5, STEEP)) <= BOUND
+    # a singular value at the end of [0, 1]: rounding X's hi half and A moves A by up to 3 x 2^-12 of itself and X by
+    # that times s (b s^2 + 2 c s^4); with the slopes of the steps after it 0.006 from the second step (s = 1.76), 0.004
+    # from the others, and the result's own rounding is 0.004
+    u = one_entry(E, N, K)
+    out = optim.orthogonalize(u, steps=5, coefficients=STEEP, eps=1e-30)
+    assert float((out.double() - ns64(u, 5, STEEP, 1e-30)).abs().max()) <= 0.02
+    assert optim.error_bits() == 0
