@@ -721,7 +721,8 @@ MOE_API moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const
  * result has no such limit.  Coefficients of up to 16 in magnitude are taken
  * as they are; a schedule with larger ones is taken if it keeps all of [0, 1]
  * in that range with half a percent to spare after each step.
- * A zero matrix gives zeros.  |U|_F is an FP32 sum of squares.
+ * A zero matrix gives zeros.  |U|_F is an FP32 sum of squares: norms from
+ * 1e-18 to 1e18 are told apart from zero and infinity.
  *
  * moe_orthogonalize: out (bf16 [batch, rows, cols]) from x (x_type).
  * moe_muon_update, in place on weight and momentum:

@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(kMixThreads) muon_start_kernel(const MixParams
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
   s = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
-  const float f = kSx / (sqrtf(s) + p.eps);
+  float f = kSx / (sqrtf(s) + p.eps);
+  if (f > 3.4e38f) f = 3.4e38f;   // so that zeros stay zeros at any eps (a NaN stays one)
   const long long base = static_cast<long long>(blockIdx.y) * p.rows * p.cols;
   const int groups = static_cast<int>(p.pitch / 8);
   // (row, group) pairs of the matrix, dealt to all its threads

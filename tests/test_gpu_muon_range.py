@@ -1,6 +1,6 @@
 """The range of the orthogonalised updates: singular values up to the stated
-limits on the way, and schedules with steep polynomials, on the tiled and the
-small kernel, wide and tall.
+limits on the way, schedules with steep polynomials, and zero matrices at any
+eps, on the tiled and the small kernel, wide and tall.
 
 Bounds.  Where every product is exact in the kernel's formats (powers of two
 and small whole numbers) the result has to be the exact value rounded to
@@ -80,3 +80,18 @@ def test_schedule_with_a_steep_first_step(E, N, K):
     out = optim.orthogonalize(u, steps=5, coefficients=STEEP, eps=1e-30)
     assert float((out.double() - ns64(u, 5, STEEP, 1e-30)).abs().max()) <= 0.02
     assert optim.error_bits() == 0
+
+
+@pytest.mark.parametrize("N,K", [(64, 96), (300, 280), (33, 7)])
+@pytest.mark.parametrize("eps", [1e-7, 1e-36, 1e-38])
+def test_zero_matrix_at_any_eps(N, K, eps):
+    from mixture_experts_routed_route_gb300 import optim
+    u = gradient(3, N, K, seed=6)
+    u[1] = 0.0
+    out = optim.orthogonalize(u, eps=eps)
+    assert float(out[1].abs().max()) == 0.0
+    assert bool(torch.isfinite(out).all())
+    w = torch.randn((3, N, K), device="cuda")
+    w1 = w[1].clone()
+    optim.muon_update(w, u, torch.zeros_like(w), lr=0.5, scale=1.0, eps=eps)
+    assert torch.equal(w[1], w1) and bool(torch.isfinite(w).all())
