@@ -739,6 +739,11 @@ MOE_API moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const
  * (0 for an invalid cfg); less than one matrix's is MOE_ERR_CAPACITY.
  * device_error_word: as for moe_forward_static_scratch (a device wait that
  * ran out of time sets MOE_DEV_ERR_TIMEOUT; never cleared here).
+ * moe_muon_error_word gives the address of a word that the library keeps on
+ * the current device for callers without one of their own; it is zero when the
+ * library is loaded, so no call has to clear it first, and asking for it is
+ * fine inside graph capture.  moe_muon_get_error synchronises the device,
+ * returns that word's bits and clears it (not inside graph capture).
  * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, batch < 0, sizes
  * < 1, steps outside [1, MOE_MUON_MAX_STEPS], coefficients not finite or
  * above 16 and not known to stay in range, eps not finite and positive,
@@ -758,6 +763,8 @@ typedef struct {
   int32_t nesterov;       /* 0 or 1 */
 } moe_muon_rates;
 
+MOE_API moe_status moe_muon_error_word(uint32_t** device_error_word);
+MOE_API moe_status moe_muon_get_error(uint32_t* bits);
 MOE_API size_t moe_muon_workspace_bytes(const moe_muon_config* cfg, int32_t matrices);
 MOE_API moe_status moe_orthogonalize(const moe_muon_config* cfg, const void* x, moe_type x_type, void* out,
                                      void* workspace, size_t workspace_bytes, uint32_t* device_error_word,

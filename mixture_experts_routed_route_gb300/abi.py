@@ -167,6 +167,8 @@ _SIGNATURES = {
                                 + [ctypes.c_size_t, _P]),
     "moe_topk_gate_forward": (ctypes.c_int, [ctypes.POINTER(moe_topk_gate_config), _P, _P, _P, _P, _P]),
     "moe_topk_gate_backward": (ctypes.c_int, [ctypes.POINTER(moe_topk_gate_config), _P, _P, _P, _P, _P]),
+    "moe_muon_error_word": (ctypes.c_int, [ctypes.POINTER(_P)]),
+    "moe_muon_get_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "moe_muon_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_muon_config), ctypes.c_int32]),
     "moe_orthogonalize": (ctypes.c_int, [ctypes.POINTER(moe_muon_config), _P, ctypes.c_int, _P, _P, ctypes.c_size_t, _P,
                                          _P]),
@@ -412,6 +414,18 @@ def moe_topk_gate_backward(cfg, logits, ids, d_scores, d_logits, stream=None):
     _check("moe_topk_gate_backward",
            LIB.moe_topk_gate_backward(ctypes.byref(cfg), _ptr(logits), _ptr(ids), _ptr(d_scores), _ptr(d_logits),
                                       _stream(stream)))
+
+
+def moe_muon_error_word():
+    word = _P()
+    _check("moe_muon_error_word", LIB.moe_muon_error_word(ctypes.byref(word)))
+    return word.value
+
+
+def moe_muon_get_error():
+    bits = ctypes.c_uint32()
+    _check("moe_muon_get_error", LIB.moe_muon_get_error(ctypes.byref(bits)))
+    return bits.value
 
 
 def moe_muon_workspace_bytes(cfg, matrices):

@@ -62,6 +62,10 @@ namespace moe {
 
 namespace {
 
+// The error word of callers without one of their own: a device's copy is zero
+// from the library's load on, so a first call may be inside a graph capture.
+__device__ uint32_t g_error_word;
+
 // Tile of BN = 256 or 128 columns (256 rows on the pair): stages of 128
 // contraction elements, in two 64-element chunks of 128 (A) and BN / 2 (B)
 // rows per CTA; 4 KB an epilogue warp to turn its 32 x 32 chunks around.
@@ -768,6 +772,19 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
 using namespace moe;
 
 extern "C" {
+
+moe_status moe_muon_error_word(uint32_t** device_error_word) {
+  if (!device_error_word) return MOE_ERR_INVALID_ARG;
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(device_error_word), g_error_word) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_muon_get_error(uint32_t* bits) {
+  if (!bits) return MOE_ERR_INVALID_ARG;
+  const uint32_t none = 0;
+  const bool ok = cudaDeviceSynchronize() == cudaSuccess && cudaMemcpyFromSymbol(bits, g_error_word, sizeof none) == cudaSuccess &&
+                  cudaMemcpyToSymbol(g_error_word, &none, sizeof none) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
+  return ok ? MOE_OK : MOE_ERR_CUDA;
+}
 
 size_t moe_muon_workspace_bytes(const moe_muon_config* cfg, int32_t matrices) {
   if (!muon_config_ok(cfg) || !muon_size_ok(cfg)) return 0;

@@ -39,24 +39,17 @@ def _config(shape, steps, coefficients, eps):
 
 
 def _error_word(device):
+    """The address of the library's error word on `device`, which is current."""
     word = _error_words.get(device)
     if word is None:
-        word = _error_words[device] = torch.zeros(1, dtype=torch.int32, device=device)
-        torch.cuda.synchronize(device)   # zeroed before any stream's kernel sets a bit
+        word = _error_words[device] = abi.moe_muon_error_word()
     return word
 
 
 def error_bits(device="cuda"):
     """The MOE_DEV_ERR_* bits that updates on `device` have set (0: none); synchronises and clears them."""
-    device = torch.device(device)
-    if device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    torch.cuda.synchronize(device)
-    word = _error_word(device)
-    bits = int(word.item())
-    word.zero_()
-    torch.cuda.synchronize(device)   # cleared before another stream's kernel sets a bit
-    return bits
+    with torch.cuda.device(torch.device(device)):
+        return abi.moe_muon_get_error()
 
 
 def workspace(E, rows, cols, *, matrices=None, device="cuda"):
