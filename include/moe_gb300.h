@@ -739,6 +739,10 @@ MOE_API moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const
  * (0 for an invalid cfg); less than one matrix's is MOE_ERR_CAPACITY.
  * device_error_word: as for moe_forward_static_scratch (a device wait that
  * ran out of time sets MOE_DEV_ERR_TIMEOUT; never cleared here).
+ * A call whose waits ran out of time updates nothing from unfinished products:
+ * momentum has taken its step, each element of weight, weight_bf16 or out is
+ * either as it was or completely the new one, and a run of matrices that lost
+ * a product before its last one is as it was.
  * moe_muon_error_word gives the address of a word that the library keeps on
  * the current device for callers without one of their own; it is zero when the
  * library is loaded, so no call has to clear it first, and asking for it is

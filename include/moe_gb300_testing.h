@@ -80,6 +80,12 @@ MOE_API moe_status moe_ctx_test_fused_stall(moe_ctx* ctx, int stall, int64_t wai
  * later calls; no device access. */
 MOE_API moe_status moe_ctx_test_tile_mode(moe_ctx* ctx, int mode);
 
+/* Failure test of the weight updates: in later calls on the tiled kernels,
+ * product `product` of each run of matrices (3 s, 3 s + 1, 3 s + 2 of step s;
+ * the last one excepted) counts as one whose waits ran out of time.  The mark
+ * is set from the host, between the launches.  -1 restores the default. */
+MOE_API moe_status moe_test_muon_lost(int product);
+
 #ifdef __cplusplus
 }
 #endif

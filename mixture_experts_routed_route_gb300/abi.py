@@ -167,6 +167,7 @@ _SIGNATURES = {
                                 + [ctypes.c_size_t, _P]),
     "moe_topk_gate_forward": (ctypes.c_int, [ctypes.POINTER(moe_topk_gate_config), _P, _P, _P, _P, _P]),
     "moe_topk_gate_backward": (ctypes.c_int, [ctypes.POINTER(moe_topk_gate_config), _P, _P, _P, _P, _P]),
+    "moe_test_muon_lost": (ctypes.c_int, [ctypes.c_int]),
     "moe_muon_error_word": (ctypes.c_int, [ctypes.POINTER(_P)]),
     "moe_muon_get_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "moe_muon_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_muon_config), ctypes.c_int32]),
@@ -414,6 +415,10 @@ def moe_topk_gate_backward(cfg, logits, ids, d_scores, d_logits, stream=None):
     _check("moe_topk_gate_backward",
            LIB.moe_topk_gate_backward(ctypes.byref(cfg), _ptr(logits), _ptr(ids), _ptr(d_scores), _ptr(d_logits),
                                       _stream(stream)))
+
+
+def moe_test_muon_lost(product):
+    _check("moe_test_muon_lost", LIB.moe_test_muon_lost(int(product)))
 
 
 def moe_muon_error_word():

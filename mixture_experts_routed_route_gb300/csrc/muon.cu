@@ -54,8 +54,10 @@
 // the tile's end too: the update of 64 x 1408 x 2048 790 to 722 us.  Both
 // CTAs' loads complete on rank 0's barrier of the stage.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
+#include "moe_gb300_testing.h"
 #include "muon_core.cuh"
 
 namespace moe {
@@ -155,12 +157,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   cluster_sync();   // the other CTA's barriers exist before anything arrives on them
   after_previous();
+  int total = p.total;
+  if constexpr (KIND >= kFinal) {
+    // unfinished products: the caller's tensors stay as they are
+    const uint32_t lost = *p.lost;
+    if (lost != 0) {
+      total = 0;
+      if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, lost);
+    }
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     uint32_t it = 0;
     bool ok = true;
-    for (int tile = cid; ok && tile < p.total; tile += ncl) {
+    for (int tile = cid; ok && tile < total; tile += ncl) {
       const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
       const int brow = t.col0 + t.n / 2 * rank;   // this CTA's half of the N rows
       const int ks_all = p.split ? 2 * p.kstages : p.kstages;
@@ -202,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t idesc0 = (1u << 4) | ((256u >> 4) << 24) | (p.a_mn ? kIdescAMnMajor : 0u) | (p.b_mn ? (1u << 16) : 0u);
       uint32_t it = 0, tc = 0;
       bool ok = true;
-      for (int tile = cid; ok && tile < p.total; tile += ncl, ++tc) {
+      for (int tile = cid; ok && tile < total; tile += ncl, ++tc) {
         const uint32_t idesc = idesc0 | ((static_cast<uint32_t>(ns_tile<KIND, BN>(p, tile, rank).n) >> 3) << 17);
         const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) break;
@@ -232,7 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) tc_commit_pair_mc(&tfull[acc], 3);
         __syncwarp();
       }
-      if (lane == 0) {
+      if (lane == 0 && it > 0) {
         tc_commit_pair(drain);
         drain_wait(drain, 0);
       }
@@ -246,19 +257,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tempty0 = cluster_addr(tempty, 0);
     uint32_t tc = 0;
     ChunkIn<KIND> in;   // of the chunk at hand, from one chunk before it (of the tile before) on
-    if (cid < p.total) {
+    if (cid < total) {
       const NsTile t = ns_tile<KIND, BN>(p, cid, rank);
       const NsChunk k = ns_chunk_of<KIND>(t, q, h, 0);
       load_chunk_in(p, t.mat, k.row, k.col, lane, in);
     }
-    for (int tile = cid; tile < p.total; tile += ncl, ++tc) {
+    for (int tile = cid; tile < total; tile += ncl, ++tc) {
       const NsTile t = ns_tile<KIND, BN>(p, tile, rank);
       const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
       auto load_next = [&](int ci) {
         if (ci + 1 < kChunks) {
           const NsChunk k = ns_chunk_of<KIND>(t, q, h, ci + 1);
           load_chunk_in(p, t.mat, k.row, k.col, lane, in);
-        } else if (tile + ncl < p.total) {
+        } else if (tile + ncl < total) {
           const NsTile tn = ns_tile<KIND, BN>(p, tile + ncl, rank);
           const NsChunk k = ns_chunk_of<KIND>(tn, q, h, 0);
           load_chunk_in(p, tn.mat, k.row, k.col, lane, in);
@@ -310,6 +321,7 @@ struct MixParams {
   int rows, cols;
   float eps;
   float* partial;          // [matrix][gridDim.x]
+  uint32_t* lost;          // cleared here for the products that follow
   __half* hi;
   __half* lo;
   long long pitch, mat;    // stored X
@@ -351,6 +363,7 @@ __global__ void __launch_bounds__(kMixThreads) muon_mix_kernel(const MixParams p
   __shared__ float red[kMixThreads / 32];
   const long long elems = static_cast<long long>(p.rows) * p.cols, base = blockIdx.y * elems;
   const long long hop = static_cast<long long>(gridDim.x) * kMixThreads * N;
+  if ((blockIdx.x | blockIdx.y | threadIdx.x) == 0) *p.lost = 0;
   float s = 0.0f;
   for (long long i0 = (static_cast<long long>(blockIdx.x) * kMixThreads + threadIdx.x) * N; i0 < elems; i0 += kBatch * hop) {
     float u[kBatch][N], m[M ? kBatch : 1][N];
@@ -595,6 +608,14 @@ struct MuonIo {
   float decay, rate;
 };
 
+// moe_test_muon_lost: the product after which a run's word is set from the host.
+std::atomic<int> g_test_lost{-1};
+
+bool test_lost(int product, uint32_t* lost, cudaStream_t stream) {
+  if (product != g_test_lost.load(std::memory_order_relaxed)) return true;
+  return cudaMemsetAsync(lost, kErrTimeout, 1, stream) == cudaSuccess;
+}
+
 moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace, size_t bytes, uint32_t* err,
                     cudaStream_t stream) {
   const NsLayout L = ns_layout(c);
@@ -618,6 +639,7 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
   __half* B = reinterpret_cast<__half*>(take(na));
   float* diag = reinterpret_cast<float*>(take(sizeof(float) * L.m * chunk));
   float* partial = reinterpret_cast<float*>(take(sizeof(float) * kMixBlocks * chunk));
+  uint32_t* lost = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t)));
 
   // tensor maps of X (both buffers), A and B: as the A operand, and as the B
   // operand of 256- and 128-column tiles (B's rows, or X's columns if wide)
@@ -655,6 +677,7 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
     mp.cols = c->cols;
     mp.eps = c->eps;
     mp.partial = partial;
+    mp.lost = lost;
     mp.hi = hi[0];
     mp.lo = lo[0];
     mp.pitch = L.pitch_x;
@@ -713,7 +736,7 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
       const int cur = s & 1;
       const float* co = c->coefficients[s];
       NsParams p{};
-      p.err = err;
+      p.err = lost;
       p.rows = L.m;
       p.cols = static_cast<int>(L.pitch_a);
       p.pitch = L.pitch_a;
@@ -728,11 +751,13 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
       p.out_hi = A;
       if (launch_tiles<kGram>(xa[cur], L.tall ? xb[cur] : xk[cur], xl[cur], p, n, L.m, L.m, sms, stream) != cudaSuccess)
         return MOE_ERR_CUDA;
+      if (!test_lost(3 * s, lost, stream)) return MOE_ERR_CUDA;
       p.a_mn = p.b_mn = 0;
       p.kstages = (L.m + 127) / 128;
       p.in_hi = A;
       p.out_hi = B;
       if (launch_tiles<kPoly>(aa, ab, xl[cur], p, n, L.m, L.m, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+      if (!test_lost(3 * s + 1, lost, stream)) return MOE_ERR_CUDA;
       p.rows = c->rows;
       p.cols = static_cast<int>(L.pitch_x);
       p.pitch = L.pitch_x;
@@ -748,7 +773,10 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
       const CUtensorMap (&opb)[2] = L.tall ? bb : xb[cur];
       if (s + 1 < c->steps) {
         if (launch_tiles<kApply>(opa, opb, xl[cur], p, n, c->rows, c->cols, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        if (!test_lost(3 * s + 2, lost, stream)) return MOE_ERR_CUDA;
       } else {
+        p.err = err;
+        p.lost = lost;
         p.ucols = c->cols;
         if (io.o16) p.o16 = io.o16 + u0;
         else p.weight = static_cast<uint8_t*>(io.weight) + u0 * (io.weight_f32 ? 4 : 2);
@@ -784,6 +812,11 @@ moe_status moe_muon_get_error(uint32_t* bits) {
   const bool ok = cudaDeviceSynchronize() == cudaSuccess && cudaMemcpyFromSymbol(bits, g_error_word, sizeof none) == cudaSuccess &&
                   cudaMemcpyToSymbol(g_error_word, &none, sizeof none) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
   return ok ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_test_muon_lost(int product) {
+  g_test_lost.store(product, std::memory_order_relaxed);
+  return MOE_OK;
 }
 
 size_t moe_muon_workspace_bytes(const moe_muon_config* cfg, int32_t matrices) {

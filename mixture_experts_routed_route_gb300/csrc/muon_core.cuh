@@ -47,7 +47,8 @@ struct NsParams {
   int weight_f32;
   int ucols;
   float decay, rate;    // W <- decay W - rate X
-  uint32_t* err;
+  uint32_t* err;              // a wait that ran out of time; of the products before the last, the run's own word
+  const uint32_t* lost;       // last product: that word, nonzero if one of them left its output unfinished
 };
 
 // Both CTAs' loads of a stage complete on rank 0's barrier (the address of

@@ -99,7 +99,9 @@ def muon_update(weight, grad, momentum, *, lr, mu=0.95, nesterov=True, weight_de
 
     (without nesterov: of the momentum).  scale: default 0.2 sqrt(max(rows,
     cols)), which gives updates the RMS of an Adam step.  weight_bf16: a
-    bfloat16 copy of a float32 weight to refresh, as the layer reads it."""
+    bfloat16 copy of a float32 weight to refresh, as the layer reads it.
+    Where a device wait runs out of time (error_bits), weights whose products
+    were not finished stay as they were; the momentum has taken its step."""
     _need(weight.is_cuda and weight.dtype in _TYPE and weight.is_contiguous(),
           "weight: expected a contiguous CUDA bfloat16 or float32 stack")
     _need(grad.dtype in _TYPE, "grad: bfloat16 or float32")
@@ -125,7 +127,9 @@ def muon_update(weight, grad, momentum, *, lr, mu=0.95, nesterov=True, weight_de
 class Muon:
     """The optimiser of a list of stacked weights: FP32 momenta (and, with
     master=True, FP32 master copies of bfloat16 weights) and one workspace
-    that every step shares, so steps of one object run on one stream."""
+    that every step shares, so steps of one object run on one stream.  A step
+    only enqueues: error_bits() tells, whenever the program asks, whether a
+    device wait ran out of time and left weights without their update."""
 
     def __init__(self, weights, *, lr, mu=0.95, nesterov=True, weight_decay=0.0, steps=5, coefficients=COEFFICIENTS,
                  eps=1e-7, master=False):
