@@ -8,7 +8,10 @@ library (``moe_block_norm_*`` and ``moe_topk_gate_*`` of the C ABI).  Calls
 enqueue on the current stream of the inputs' device, or on ``stream`` (a torch
 stream or a raw handle); buffers that a call makes are allocated on the stream
 it runs on.  Inputs that another stream still writes are the caller's to
-order, as with any torch operator.
+order, as with any torch operator.  The library wants tensors that start at a
+16-byte boundary; where one does not (a slice of tokens of an odd width, a view
+into a flat buffer), the call works on an aligned copy of it and copies results
+back, one more pass over that tensor.
 """
 
 import ctypes
@@ -28,7 +31,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
 _BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
 _empty, _empty_like, _byref = torch.empty, torch.empty_like, ctypes.byref
-_LIB = abi.LIB
+_LIB, _INVALID = abi.LIB, abi.MOE_ERR_INVALID_ARG
 
 
 def on_stream(fn, device, stream):
@@ -49,6 +52,28 @@ def _new(x, dtype):
     if dtype is x.dtype and x.is_contiguous():
         return _empty_like(x)
     return _empty(x.shape, dtype=dtype, device=x.device)
+
+
+def unaligned(*tensors):
+    """Whether one of the tensors (or Nones) does not start at a 16-byte boundary."""
+    return any(t is not None and t.data_ptr() & 15 for t in tensors)
+
+
+def aligned(t):
+    """t, or a contiguous copy of it where it does not start at a 16-byte boundary."""
+    return t.clone(memory_format=torch.contiguous_format) if unaligned(t) else t
+
+
+def _room(t):
+    """t, or an uninitialised tensor to fill in its place where it does not start at a 16-byte boundary."""
+    return _empty(t.shape, dtype=t.dtype, device=t.device) if unaligned(t) else t
+
+
+def put_back(*pairs):
+    """Copy each (tensor, what was filled in its place) back."""
+    for t, filled in pairs:
+        if filled is not t:
+            t.copy_(filled)
 
 
 def _at(t):
@@ -169,8 +194,18 @@ def block_norm(x, branch=None, *, gate=None, post_weight=None, pre_weight=None, 
         status = _LIB.moe_block_norm_forward(_byref(cfg), x.data_ptr(), _at(branch), _at(gate), _at(post_weight),
                                              _at(pre_weight), _at(yy), _at(hh), _at(stats), s)
         if status:
+            if status == _INVALID and unaligned(x, branch, gate, post_weight, pre_weight, y, h, stats):
+                return realigned()
             raise abi.MoEError("moe_block_norm_forward", status)
         return (x if same else yy), hh
+
+    def realigned():
+        filled = _room(y), _room(h), aligned(stats)
+        yy, hh = block_norm(aligned(x), aligned(branch), gate=aligned(gate), post_weight=aligned(post_weight),
+                            pre_weight=aligned(pre_weight), residual_scale=residual_scale, branch_scale=branch_scale, eps=eps,
+                            weight_offset=weight_offset, y=filled[0], h=filled[1], stats=filled[2])
+        put_back((y, filled[0]), (h, filled[1]), (stats, filled[2]))
+        return x if same else yy if y is None else y, hh if h is None else h
 
     return on_stream(run, dev, stream)
 
@@ -215,6 +250,11 @@ def block_norm_backward(x, branch, stats, dy, dh=None, *, gate=None, post_weight
                                               _at(pre_weight), _at(stats), _at(dy), _at(dh), dx.data_ptr(), _at(dbranch),
                                               _at(dgate), _at(dpost), _at(dpre), ws.data_ptr(), nb, s)
         if status:
+            if status == _INVALID and unaligned(x, branch, stats, dy, dh, gate, post_weight, pre_weight):
+                return block_norm_backward(aligned(x), aligned(branch), aligned(stats), aligned(dy), aligned(dh),
+                                           gate=aligned(gate), post_weight=aligned(post_weight),
+                                           pre_weight=aligned(pre_weight), residual_scale=residual_scale,
+                                           branch_scale=branch_scale, weight_offset=weight_offset)
             raise abi.MoEError("moe_block_norm_backward", status)
         return BlockNormGrads(dx, dbranch, dgate, dpost, dpre)
 
@@ -254,6 +294,12 @@ def topk_gate(logits, top_k, *, score="softmax", renormalize=False, scale=1.0, s
         status = _LIB.moe_topk_gate_forward(_byref(cfg), logits.data_ptr(), _at(select_bias), i.data_ptr(), s.data_ptr(),
                                             stream)
         if status:
+            if status == _INVALID and unaligned(logits, select_bias, i, s):
+                filled = _room(i), _room(s)
+                topk_gate(aligned(logits), top_k, score=score, renormalize=renormalize, scale=scale,
+                          select_bias=aligned(select_bias), ids=filled[0], scores=filled[1])
+                put_back((i, filled[0]), (s, filled[1]))
+                return i, s
             raise abi.MoEError("moe_topk_gate_forward", status)
         return i, s
 
@@ -277,6 +323,12 @@ def topk_gate_backward(logits, ids, d_scores, *, score="softmax", renormalize=Fa
         status = _LIB.moe_topk_gate_backward(_byref(cfg), logits.data_ptr(), ids.data_ptr(), d_scores.data_ptr(),
                                              d.data_ptr(), stream)
         if status:
+            if status == _INVALID and unaligned(logits, ids, d_scores, d):
+                filled = _room(d)
+                topk_gate_backward(aligned(logits), aligned(ids), aligned(d_scores), score=score, renormalize=renormalize,
+                                   scale=scale, d_logits=filled)
+                put_back((d, filled))
+                return d
             raise abi.MoEError("moe_topk_gate_backward", status)
         return d
 

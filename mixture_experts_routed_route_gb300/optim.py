@@ -7,6 +7,8 @@ CUDA library (``moe_orthogonalize``, ``moe_muon_update`` of the C ABI).
 
 Weights are stacks [E, rows, cols], such as W2 [E, D, F].  W13 [E, 2F, D]
 holds two matrices an expert: its view [2E, F, D] updates gate and up apart.
+Tensors that do not start at a 16-byte boundary (views into a flat buffer) are
+worked on in aligned copies, as in ``block``.
 """
 
 import math
@@ -14,7 +16,7 @@ import math
 import torch
 
 from . import abi
-from .block import _TYPE, _dense, _need, on_stream
+from .block import _TYPE, _dense, _need, aligned, on_stream, put_back
 
 # a s + b s^3 + c s^5: a steep start for small singular values; five steps take [1e-3, 1] near 1
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
@@ -65,8 +67,8 @@ def workspace(E, rows, cols, *, matrices=None, device="cuda"):
 def _workspace(given, shape, device):
     if given is None:
         return workspace(*shape, device=device)
-    _need(given.dtype == torch.uint8 and given.is_contiguous() and given.device == device,
-          "workspace: expected a contiguous uint8 tensor on the weights' device")
+    _need(given.dtype == torch.uint8 and given.is_contiguous() and given.device == device and given.data_ptr() % 256 == 0,
+          "workspace: expected a contiguous uint8 tensor on the weights' device that starts at a 256-byte boundary")
     return given
 
 
@@ -81,8 +83,10 @@ def orthogonalize(x, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, 
 
     def run(s):
         o = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        filled = aligned(o)
         ws = _workspace(workspace, x.shape, dev)
-        abi.moe_orthogonalize(cfg, x, _TYPE[x.dtype], o, ws, ws.numel(), _error_word(dev), s)
+        abi.moe_orthogonalize(cfg, aligned(x), _TYPE[x.dtype], filled, ws, ws.numel(), _error_word(dev), s)
+        put_back((o, filled))
         return o
 
     return on_stream(run, dev, stream)
@@ -118,8 +122,10 @@ def muon_update(weight, grad, momentum, *, lr, mu=0.95, nesterov=True, weight_de
 
     def run(s):
         ws = _workspace(workspace, shape, dev)
-        abi.moe_muon_update(cfg, rates, weight, _TYPE[weight.dtype], grad, _TYPE[grad.dtype], momentum, weight_bf16, ws,
-                            ws.numel(), _error_word(dev), s)
+        w, m, copy = aligned(weight), aligned(momentum), aligned(weight_bf16)
+        abi.moe_muon_update(cfg, rates, w, _TYPE[w.dtype], aligned(grad), _TYPE[grad.dtype], m, copy, ws, ws.numel(),
+                            _error_word(dev), s)
+        put_back((weight, w), (momentum, m), (weight_bf16, copy))
 
     on_stream(run, dev, stream)
 
