@@ -122,8 +122,9 @@ def _gate_shape(cfg, gate, T, D, device):
         if shape[0] == D:
             cfg.gate_mode = abi.MOE_GATE_CHANNEL
             return
-    elif shape[1] == D and shape[0] > 0 and T % shape[0] == 0:
-        cfg.gate_mode, cfg.gate_rows = abi.MOE_GATE_GROUP, shape[0]
+    elif shape[1] == D and (T % shape[0] == 0 if shape[0] else T == 0):
+        # no gate rows go with no tokens; a group count is at least one
+        cfg.gate_mode, cfg.gate_rows = abi.MOE_GATE_GROUP, shape[0] or 1
         return
     elif shape[0] == T and shape[1] == 1:
         cfg.gate_mode = abi.MOE_GATE_TOKEN
