@@ -664,8 +664,8 @@ moe_status run_muon(const moe_muon_config* c, const MuonIo& io, void* workspace,
   if (!ok) return MOE_ERR_CUDA;
 
   const long long elems = static_cast<long long>(c->rows) * c->cols;
-  for (int e0 = 0; e0 < c->batch; e0 += chunk) {
-    const int n = std::min(chunk, c->batch - e0);
+  for (long long e0 = 0; e0 < c->batch; e0 += chunk) {
+    const int n = static_cast<int>(std::min<long long>(chunk, c->batch - e0));
     const long long u0 = e0 * elems;
     MixParams mp{};
     mp.grad = static_cast<const uint8_t*>(io.grad) + u0 * (io.grad_f32 ? 4 : 2);

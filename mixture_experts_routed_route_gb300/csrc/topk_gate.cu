@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kGateThreads) topk_gate_bwd_kernel(const GateP
 template <typename X, int L>
 void launch_gate(bool fwd, const GateParams& p, cudaStream_t stream) {
   const int per = kGateThreads / 32;
-  const int ctas = (p.T + per - 1) / per;
+  const int ctas = (p.T - 1) / per + 1;
   if (fwd) topk_gate_fwd_kernel<X, L><<<ctas, kGateThreads, 0, stream>>>(p);
   else topk_gate_bwd_kernel<X, L><<<ctas, kGateThreads, 0, stream>>>(p);
 }
