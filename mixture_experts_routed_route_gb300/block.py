@@ -26,6 +26,9 @@ _NormConfig, _GateConfig = abi.moe_block_norm_config, abi.moe_topk_gate_config
 _SCORE = {"softmax": abi.MOE_SCORE_SOFTMAX, "sigmoid": abi.MOE_SCORE_SIGMOID}
 
 
+# sizes are int32 in the C structs
+_MOST = 1 << 31
+
 # the raw handle of a device's current stream (torch.cuda.current_stream builds a Stream object each time)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
@@ -138,6 +141,7 @@ def _norm_config(x, branch, gate, post_weight, pre_weight, residual_scale, branc
     if len(shape) != 2 or xt not in _TYPE or dev.type != "cuda":
         raise ValueError("x: expected a CUDA bfloat16 or float32 [T, D] tensor")
     T, D = shape
+    _need(T < _MOST and D < _MOST, "x: sizes have to be below 2^31")
     kind = _FP32
     if pre_weight is not None:
         kind = pre_weight.dtype
@@ -268,6 +272,7 @@ def _gate_config(logits, top_k, score, renormalize, scale):
         raise ValueError("logits: expected a CUDA bfloat16 or float32 [T, E] tensor")
     if score not in _SCORE:
         raise ValueError("score: softmax or sigmoid")
+    _need(shape[0] < _MOST and shape[1] < _MOST, "logits: sizes have to be below 2^31")
     return _GateConfig(shape[0], shape[1], top_k, _TYPE[kind], _SCORE[score], 1 if renormalize else 0, scale,
                        _rows("logits", logits, kind, shape, dev))
 

@@ -29,6 +29,7 @@ _error_words = {}
 
 def _config(shape, steps, coefficients, eps):
     _need(len(shape) == 3, "expected a stack of matrices [E, rows, cols]")
+    _need(max(shape) < 1 << 31, "sizes have to be below 2^31")
     _need(1 <= steps <= abi.MOE_MUON_MAX_STEPS, "steps: 1 to 16")
     cfg = abi.moe_muon_config(shape[0], shape[1], shape[2], steps)
     cfg.eps = eps
