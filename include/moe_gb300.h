@@ -630,8 +630,8 @@ typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_FP32 = 1 } moe_type;
  *   dbranch       bf16 [T, D] contiguous (with branch)
  *   dgate         the gate's shape and type (with gate)
  *   dpost_weight, dpre_weight   float [D] (with the weights)
- * y is rebuilt from x and branch in FP32, so x must be the forward's input
- * (not overwritten by an in-place y).  Each parameter's gradient is
+ * y is rebuilt from x and branch in FP32, so both must be the forward's inputs
+ * (not overwritten by an in-place y or h).  Each parameter's gradient is
  * overwritten; with T = 0 it is zero.  `workspace`: at least
  * moe_block_norm_workspace_bytes (16-byte aligned, contents need not be
  * kept or cleared; MOE_ERR_CAPACITY if too small).  That size depends on the

@@ -179,8 +179,11 @@ def block_norm(x, branch=None, *, gate=None, post_weight=None, pre_weight=None, 
     residual is scaled).  post_weight None: no norm after the block;
     pre_weight None: no h (None is returned in its place).  gate: [D] (a
     channel), [G, D] (row t takes gate row t // (T / G)) or [T, 1] (a token).
-    ``y`` may be x and ``h`` may be branch (in place).  ``stats``: a float32
-    [2, T] tensor for the backward to read."""
+    ``y`` may be x and ``h`` may be branch (in place): for serving only, as the
+    backward reads the x and branch that came in and would give wrong
+    gradients from what replaced them.  ``stats``: a float32 [2, T] tensor for
+    the backward to read (r of the branch with post_weight, r of y with
+    pre_weight; the other row is left as it is)."""
     cfg = _norm_config(x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, eps, weight_offset)
     shape, dev = x.shape, x.device
     if y is not None:
@@ -227,7 +230,8 @@ def block_norm_backward(x, branch, stats, dy, dh=None, *, gate=None, post_weight
                         residual_scale=1.0, branch_scale=1.0, weight_offset=0.0, stream=None):
     """Gradients (BlockNormGrads) of block_norm's inputs from ``dy`` (x's
     type; None: zero) and ``dh`` (bfloat16; given with pre_weight), with the
-    forward's inputs and ``stats``.  dx has x's type, dbranch is bfloat16,
+    forward's inputs (not overwritten since, by a call in place or otherwise)
+    and ``stats``.  dx has x's type, dbranch is bfloat16,
     dgate has the gate's shape and type, the weights' gradients are float32."""
     cfg = _norm_config(x, branch, gate, post_weight, pre_weight, residual_scale, branch_scale, 1.0, weight_offset)
     shape, dev = x.shape, x.device
