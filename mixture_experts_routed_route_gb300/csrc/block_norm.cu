@@ -94,7 +94,7 @@ struct NormParams {
   void* dx;                   // or NULL
   __nv_bfloat16* do_;
   void* dgate;
-  float* partial;             // [3][gridDim.x][D]: sum s n (times g: grouped, token gates), dw_pre
+  float* partial;             // [2][gridDim.x][D]: sum s n (times g: grouped, token gates, gates of every element), sum dh z
   float* gate_partial;        // [slabs][D] (grouped gates cut into several slabs a group)
   int slabs_per_group, slabs;
 };
@@ -1014,8 +1014,8 @@ void add_stream(NormParams* p, int k, const void* base, int64_t ld, moe_type typ
   s.end = s.base + (p->T - 1) * s.ld + s.row_bytes;
 }
 
-// Choose the vector path and lay out a row's slot; a gate of every element
-// that leaves no room for one row is read from global memory instead.
+// Choose the vector path and lay out a row's slot: with FP32 x, dy and gate at
+// 8192 columns 128 KB, which fit beside the table's 64.
 bool lay_out(NormParams* p) {
   bool vec = p->D % 8 == 0 && p->ldy % 8 == 0 && p->ldh % 8 == 0;
   for (const Stream& s : p->in) vec = vec && (s.base == nullptr || (s.ld / s.esz) % 8 == 0);
@@ -1023,9 +1023,7 @@ bool lay_out(NormParams* p) {
   for (Stream& s : p->in) {
     if (s.base == nullptr) continue;
     s.off = p->slot;
-    const int need = (s.row_bytes + 15) / 16 * 16 + (vec ? 0 : 16);
-    if (&s == &p->in[kG] && p->slot + need + 8 * p->D + 32 > kSharedMem) s.base = nullptr;
-    else p->slot += need;
+    p->slot += (s.row_bytes + 15) / 16 * 16 + (vec ? 0 : 16);
   }
   return vec;
 }
