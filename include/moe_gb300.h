@@ -711,7 +711,9 @@ MOE_API moe_status moe_topk_gate_backward(const moe_topk_gate_config* cfg, const
  * which moves every singular value s through a s + b s^3 + c s^5.
  * Precision: FP16 tensor-core products with FP32 accumulation; X is kept to
  * 22 bits and the polynomial's diagonal in FP32 between them.  After five
- * steps the result is within about 1e-3 of the exact one in norm.
+ * steps X is within about 1e-3 of the exact one in norm (a few rows or columns:
+ * 3e-3) before it is rounded: to BF16 (1.7e-3 in norm) by moe_orthogonalize,
+ * with the weight by moe_muon_update.
  * Range of those formats: before each step every element of X has to be below
  * 15.9 in magnitude, every element of A below 127, and every element of b A +
  * c A A off its diagonal below 127; beyond that the result is NaN or infinite.
