@@ -141,7 +141,8 @@ def _norm_config(x, branch, gate, post_weight, pre_weight, residual_scale, branc
     if len(shape) != 2 or xt not in _TYPE or dev.type != "cuda":
         raise ValueError("x: expected a CUDA bfloat16 or float32 [T, D] tensor")
     T, D = shape
-    _need(T < _MOST and D < _MOST, "x: sizes have to be below 2^31")
+    if T >= _MOST or D >= _MOST:
+        raise ValueError("x: sizes have to be below 2^31")
     kind = _FP32
     if pre_weight is not None:
         kind = pre_weight.dtype
@@ -203,19 +204,21 @@ def block_norm(x, branch=None, *, gate=None, post_weight=None, pre_weight=None, 
                                              _at(pre_weight), _at(yy), _at(hh), _at(stats), s)
         if status:
             if status == _INVALID and unaligned(x, branch, gate, post_weight, pre_weight, y, h, stats):
-                return realigned()
+                return _block_norm_realigned(cfg, x, branch, gate, post_weight, pre_weight, y, h, stats, same)
             raise abi.MoEError("moe_block_norm_forward", status)
         return (x if same else yy), hh
 
-    def realigned():
-        filled = _room(y), _room(h), aligned(stats)
-        yy, hh = block_norm(aligned(x), aligned(branch), gate=aligned(gate), post_weight=aligned(post_weight),
-                            pre_weight=aligned(pre_weight), residual_scale=residual_scale, branch_scale=branch_scale, eps=eps,
-                            weight_offset=weight_offset, y=filled[0], h=filled[1], stats=filled[2])
-        put_back((y, filled[0]), (h, filled[1]), (stats, filled[2]))
-        return x if same else yy if y is None else y, hh if h is None else h
-
     return on_stream(run, dev, stream)
+
+
+def _block_norm_realigned(cfg, x, branch, gate, post_weight, pre_weight, y, h, stats, same):
+    """block_norm on aligned copies, on the current stream."""
+    filled = _room(y), _room(h), aligned(stats)
+    yy, hh = block_norm(aligned(x), aligned(branch), gate=aligned(gate), post_weight=aligned(post_weight),
+                        pre_weight=aligned(pre_weight), residual_scale=cfg.residual_scale, branch_scale=cfg.branch_scale,
+                        eps=cfg.eps, weight_offset=cfg.weight_offset, y=filled[0], h=filled[1], stats=filled[2])
+    put_back((y, filled[0]), (h, filled[1]), (stats, filled[2]))
+    return x if same else yy if y is None else y, hh if h is None else h
 
 
 class BlockNormGrads(NamedTuple):
@@ -262,8 +265,8 @@ def block_norm_backward(x, branch, stats, dy, dh=None, *, gate=None, post_weight
             if status == _INVALID and unaligned(x, branch, stats, dy, dh, gate, post_weight, pre_weight):
                 return block_norm_backward(aligned(x), aligned(branch), aligned(stats), aligned(dy), aligned(dh),
                                            gate=aligned(gate), post_weight=aligned(post_weight),
-                                           pre_weight=aligned(pre_weight), residual_scale=residual_scale,
-                                           branch_scale=branch_scale, weight_offset=weight_offset)
+                                           pre_weight=aligned(pre_weight), residual_scale=cfg.residual_scale,
+                                           branch_scale=cfg.branch_scale, weight_offset=cfg.weight_offset)
             raise abi.MoEError("moe_block_norm_backward", status)
         return BlockNormGrads(dx, dbranch, dgate, dpost, dpre)
 
@@ -276,9 +279,15 @@ def _gate_config(logits, top_k, score, renormalize, scale):
         raise ValueError("logits: expected a CUDA bfloat16 or float32 [T, E] tensor")
     if score not in _SCORE:
         raise ValueError("score: softmax or sigmoid")
-    _need(shape[0] < _MOST and shape[1] < _MOST, "logits: sizes have to be below 2^31")
+    if shape[0] >= _MOST or shape[1] >= _MOST:
+        raise ValueError("logits: sizes have to be below 2^31")
     return _GateConfig(shape[0], shape[1], top_k, _TYPE[kind], _SCORE[score], 1 if renormalize else 0, scale,
                        _rows("logits", logits, kind, shape, dev))
+
+
+def _gate_options(cfg):
+    return {"score": "sigmoid" if cfg.score == abi.MOE_SCORE_SIGMOID else "softmax", "renormalize": bool(cfg.renormalize),
+            "scale": cfg.scale}
 
 
 def topk_gate(logits, top_k, *, score="softmax", renormalize=False, scale=1.0, select_bias=None, ids=None, scores=None,
@@ -306,8 +315,8 @@ def topk_gate(logits, top_k, *, score="softmax", renormalize=False, scale=1.0, s
         if status:
             if status == _INVALID and unaligned(logits, select_bias, i, s):
                 filled = _room(i), _room(s)
-                topk_gate(aligned(logits), top_k, score=score, renormalize=renormalize, scale=scale,
-                          select_bias=aligned(select_bias), ids=filled[0], scores=filled[1])
+                topk_gate(aligned(logits), shape[1], **_gate_options(cfg), select_bias=aligned(select_bias), ids=filled[0],
+                          scores=filled[1])
                 put_back((i, filled[0]), (s, filled[1]))
                 return i, s
             raise abi.MoEError("moe_topk_gate_forward", status)
@@ -335,8 +344,7 @@ def topk_gate_backward(logits, ids, d_scores, *, score="softmax", renormalize=Fa
         if status:
             if status == _INVALID and unaligned(logits, ids, d_scores, d):
                 filled = _room(d)
-                topk_gate_backward(aligned(logits), aligned(ids), aligned(d_scores), score=score, renormalize=renormalize,
-                                   scale=scale, d_logits=filled)
+                topk_gate_backward(aligned(logits), aligned(ids), aligned(d_scores), **_gate_options(cfg), d_logits=filled)
                 put_back((d, filled))
                 return d
             raise abi.MoEError("moe_topk_gate_backward", status)

@@ -16,7 +16,7 @@ import math
 import torch
 
 from . import abi
-from .block import _TYPE, _dense, _need, aligned, on_stream, put_back
+from .block import _TYPE, _dense, _need, aligned, on_stream, put_back, unaligned
 
 # a s + b s^3 + c s^5: a steep start for small singular values; five steps take [1e-3, 1] near 1
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
@@ -84,10 +84,19 @@ def orthogonalize(x, *, steps=5, coefficients=COEFFICIENTS, eps=1e-7, out=None, 
 
     def run(s):
         o = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if out is None else out
-        filled = aligned(o)
         ws = _workspace(workspace, x.shape, dev)
-        abi.moe_orthogonalize(cfg, aligned(x), _TYPE[x.dtype], filled, ws, ws.numel(), _error_word(dev), s)
-        put_back((o, filled))
+
+        def call(u, filled):
+            abi.moe_orthogonalize(cfg, u, _TYPE[x.dtype], filled, ws, ws.numel(), _error_word(dev), s)
+
+        try:
+            call(x, o)
+        except abi.MoEError:
+            if not unaligned(x, o):
+                raise
+            filled = aligned(o)
+            call(aligned(x), filled)
+            put_back((o, filled))
         return o
 
     return on_stream(run, dev, stream)
@@ -123,10 +132,19 @@ def muon_update(weight, grad, momentum, *, lr, mu=0.95, nesterov=True, weight_de
 
     def run(s):
         ws = _workspace(workspace, shape, dev)
-        w, m, copy = aligned(weight), aligned(momentum), aligned(weight_bf16)
-        abi.moe_muon_update(cfg, rates, w, _TYPE[w.dtype], aligned(grad), _TYPE[grad.dtype], m, copy, ws, ws.numel(),
-                            _error_word(dev), s)
-        put_back((weight, w), (momentum, m), (weight_bf16, copy))
+
+        def call(w, g, m, copy):
+            abi.moe_muon_update(cfg, rates, w, _TYPE[weight.dtype], g, _TYPE[grad.dtype], m, copy, ws, ws.numel(),
+                                _error_word(dev), s)
+
+        try:
+            call(weight, grad, momentum, weight_bf16)
+        except abi.MoEError:
+            if not unaligned(weight, grad, momentum, weight_bf16):
+                raise
+            filled = aligned(weight), aligned(momentum), aligned(weight_bf16)
+            call(filled[0], aligned(grad), *filled[1:])
+            put_back((weight, filled[0]), (momentum, filled[1]), (weight_bf16, filled[2]))
 
     on_stream(run, dev, stream)
 
