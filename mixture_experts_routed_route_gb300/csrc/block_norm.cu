@@ -35,6 +35,13 @@
 // forward 2048 x 7168 24.4 us (4.8 TB/s), 8192 x 7168 82 us (5.7), FP32
 // residual with a gate row a sequence 16384 x 2048 70 us (5.8); backward 2048 x 7168
 // 46 us (3.8), 8192 x 7168 137 us (5.1), 1531 x 1411 in FP32 with a token gate 23 us (1.7).
+// Gates that change by the row keep more of it alive, and their backward
+// spills (208 to 224 bytes of stores with vector rows, 472 without, and 52 to
+// 60, 268 for a gate of every element): 2048 x 7168 with eight gate rows 70 us
+// and with a gate of every element 83, FP32 16384 x 2048 with eight gate rows
+// 143 us where a channel gate takes 112, 1532 x 1411 with four 60 us.  Widths
+// that no vector divides, forward: 1531 x 1411 in FP32 12.4 us (2.1 TB/s),
+// BF16 16384 x 1411 78 us (2.4).
 // Long inputs are bound by the stream; short ones by the fixed part (launch,
 // factors, column sums: 7 us forward, 15 us backward with its second kernel)
 // and the backward by latency inside a row: its three passes and two sums are

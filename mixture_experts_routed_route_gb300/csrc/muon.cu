@@ -39,13 +39,16 @@
 // map (64-column chunks as an axis of their own).
 //
 // What bounds it.  Large matrices: operands and epilogues together draw about
-// 14 TB/s from L2, and the tensor cores run at 1.3 PFLOP/s over a whole call
-// (8 x 7168 x 2048, 3.05 ms; the Gram product alone 1.8, the apply products
-// 1.5 with 320 us each), where a library product reaches 1.7 in a long run
-// under the power cap.  64 x 1408 x 2048 with the momentum and a float32
-// weight: 5.3 ms, of which 1.3 ms move gradient, momentum, X and weight.
-// Small ones (3 x 1000 x 1531, 211 us): the chain of 15 dependent launches of
-// 10 to 17 us each.
+// 14 TB/s from L2.  8 x 7168 x 2048, 3.05 ms, is 1.3 PFLOP/s over the call and
+// 1.5 over its products (the Gram product 1.6, the apply products 1.5 with 315
+// us each), where a library product reaches 1.7 in a long run under the power
+// cap.  64 x 1408 x 2048 with the momentum and a float32 weight, 5.25 ms: the
+// products run at 1.06 PFLOP/s (4.5 ms, 11.6 us an apply tile of 11 stages; no
+// counters were taken at this shape), momentum and start kernels take 0.54 ms
+// and the weight 0.25 ms of the last product; a BF16 weight 5.2 ms.
+// Stacks in several runs of matrices: 96 x 7168 x 2048 39 ms, its step 42 ms.
+// Small ones (3 x 1000 x 1531, 209 us): the chain of 15 dependent launches of
+// 10 to 28 us each.
 //
 // Warp roles: warp 0 TMA producer, warp 1 TMEM allocation and (rank 0) MMA
 // issue for the pair, warps 2 .. 9 epilogue (lane quadrant w % 4; every other
