@@ -39,6 +39,6 @@ def test_schedules_that_do_not(table):
     assert not taken(table)
 
 
-def test_coefficients_up_to_16_are_the_callers_to_judge():
+def test_coefficients_up_to_16_are_up_to_the_caller():
     """They may grow the small singular values of a matrix that has no large one."""
     assert taken([(16.0, -16.0, 16.0)] * 16)
