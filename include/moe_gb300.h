@@ -780,6 +780,92 @@ MOE_API moe_status moe_muon_update(const moe_muon_config* cfg, const moe_muon_ra
                                    void* weight_bf16, void* workspace, size_t workspace_bytes,
                                    uint32_t* device_error_word, cudaStream_t stream);
 
+/*
+ * Dropout from a counter-based generator, whose mask is never stored:
+ *   out = keep * x / (1 - p) + residual
+ * Element e = t * d_model + d of the [T, D] tensor takes 16 bits of the
+ * Philox4x32 block (ten rounds) with counter (e / 8 low word, e / 8 high word,
+ * site, step) under the 64-bit key `seed`: half e % 2 (0: low) of word (e % 8) / 2.
+ * It is kept if those bits are at least p * 2^16, rounded; p is then that
+ * number times 2^-16, also in 1 / (1 - p).  A dropped element gives 0 (plus
+ * the residual), whatever x holds there; p = 1 drops everything.
+ * The gradient of x is the same call on the gradient of out (without
+ * residual) with the same rng and site.
+ *   x, residual, out  [T, D] of `type`; out may be x or residual; residual may
+ *                     be NULL.  Strides are elements between rows (0: D).
+ *   rng               device int64 [2]: seed, step (of which the low 32 bits
+ *                     count), read when the kernel runs, so that a captured
+ *                     graph draws a new mask where the program advances the
+ *                     step between replays; may be NULL with p = 0
+ *   site              tells calls of one step apart (a layer's number)
+ * T may be 0.  Pointers 16-byte aligned.  Errors: MOE_ERR_INVALID_ARG,
+ * MOE_ERR_UNSUPPORTED (more than 2^31 blocks of 8192 elements).
+ */
+typedef struct {
+  int32_t tokens;          /* T */
+  int32_t d_model;         /* D */
+  moe_type type;
+  uint32_t site;
+  double p;                /* in [0, 1] */
+  int64_t x_stride, residual_stride, out_stride;
+} moe_dropout_config;
+
+MOE_API moe_status moe_dropout(const moe_dropout_config* cfg, const void* x, const void* residual, const int64_t* rng,
+                               void* out, cudaStream_t stream);
+
+/*
+ * Layer norm at a block boundary: the scaled residual with dropout on the
+ * branch, and the norm before the next block, in one pass over [T, D] rows:
+ *   y = residual_scale * x + branch_scale * dropout(branch)
+ *   h = (y - m) * r * weight + bias,  m = mean_d y,  r = 1/sqrt(mean_d (y - m)^2 + eps)
+ * branch NULL: y = residual_scale * x (no dropout then); weight NULL: 1; bias
+ * NULL: 0; y NULL: not written.  h is formed from the unrounded y.  The mask is
+ * that of moe_dropout on the contiguous [T, D] branch.
+ *   x, y          [T, D] of residual_type; y may be x (in place)
+ *   branch, h     bf16 [T, D]; h may be branch
+ *   weight, bias  [D] of weight_type
+ *   stats         float [2, T] or NULL: m and r, which the backward reads
+ *   rng           as for moe_dropout; may be NULL with dropout = 0
+ * Strides are elements between rows (0: D).  Rows are read in 16-byte pieces
+ * if a stride differs from D by a multiple of 8, whatever D is, else element
+ * by element.  D <= 8192.  A row of zeros gives its bias.  T may be 0.
+ *
+ * moe_layer_norm_backward: from dy (residual_type, y_stride; NULL = 0) and dh
+ * (bf16, h_stride), the gradients of y and h, with the y that the forward wrote
+ * (x_stride is its stride here) and its stats:
+ *   dx        [T, D] of residual_type, contiguous, or NULL
+ *   dbranch   bf16 [T, D] contiguous, or NULL (with dropout: not NULL)
+ *   dweight, dbias   float [D], overwritten, or NULL; zero with T = 0
+ * The gradient is that at the stored y: a BF16 residual stream's rounding of y
+ * is part of it.  `workspace`: at least moe_layer_norm_workspace_bytes
+ * (16-byte aligned, contents need not be kept or cleared; MOE_ERR_CAPACITY if
+ * too small).  That size depends on the current device's SM count; 0 for an
+ * invalid cfg.  The parameters' gradients are summed in a fixed order on one device.
+ * Errors: MOE_ERR_INVALID_ARG (null cfg, T < 0, D < 1, unknown types, eps not
+ * finite and positive, scales not finite, dropout outside [0, 1] or without rng
+ * or branch, a stride in (0, D), null or misaligned pointers),
+ * MOE_ERR_UNSUPPORTED (D > 8192).
+ */
+typedef struct {
+  int32_t tokens;          /* T */
+  int32_t d_model;         /* D */
+  moe_type residual_type;  /* x, y, dy, dx */
+  moe_type weight_type;    /* weight, bias */
+  float residual_scale, branch_scale, eps;
+  uint32_t site;
+  double dropout;          /* p, in [0, 1] */
+  int64_t x_stride, branch_stride, y_stride, h_stride;
+} moe_layer_norm_config;
+
+MOE_API moe_status moe_layer_norm_forward(const moe_layer_norm_config* cfg, const void* x, const void* branch,
+                                          const void* weight, const void* bias, const int64_t* rng, void* y, void* h,
+                                          float* stats, cudaStream_t stream);
+MOE_API size_t moe_layer_norm_workspace_bytes(const moe_layer_norm_config* cfg);
+MOE_API moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, const void* y, const void* weight,
+                                           const float* stats, const int64_t* rng, const void* dy, const void* dh,
+                                           void* dx, void* dbranch, float* dweight, float* dbias, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream);
+
 /* Library version string. */
 MOE_API const char* moe_version(void);
 

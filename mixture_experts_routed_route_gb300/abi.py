@@ -102,6 +102,20 @@ class moe_topk_gate_config(ctypes.Structure):
                 ("scale", ctypes.c_float), ("logits_stride", ctypes.c_int64)]
 
 
+class moe_dropout_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("d_model", ctypes.c_int32), ("type", ctypes.c_int), ("site", ctypes.c_uint32),
+                ("p", ctypes.c_double), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64)]
+
+
+class moe_layer_norm_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("d_model", ctypes.c_int32), ("residual_type", ctypes.c_int),
+                ("weight_type", ctypes.c_int), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("site", ctypes.c_uint32), ("dropout", ctypes.c_double),
+                ("x_stride", ctypes.c_int64), ("branch_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("h_stride", ctypes.c_int64)]
+
+
 class moe_muon_config(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
                 ("steps", ctypes.c_int32), ("coefficients", ctypes.c_float * 3 * MOE_MUON_MAX_STEPS),
@@ -167,6 +181,11 @@ _SIGNATURES = {
                                 + [ctypes.c_size_t, _P]),
     "moe_topk_gate_forward": (ctypes.c_int, [ctypes.POINTER(moe_topk_gate_config), _P, _P, _P, _P, _P]),
     "moe_topk_gate_backward": (ctypes.c_int, [ctypes.POINTER(moe_topk_gate_config), _P, _P, _P, _P, _P]),
+    "moe_dropout": (ctypes.c_int, [ctypes.POINTER(moe_dropout_config), _P, _P, _P, _P, _P]),
+    "moe_layer_norm_forward": (ctypes.c_int, [ctypes.POINTER(moe_layer_norm_config)] + [_P] * 9),
+    "moe_layer_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_layer_norm_config)]),
+    "moe_layer_norm_backward": (ctypes.c_int, [ctypes.POINTER(moe_layer_norm_config)] + [_P] * 11
+                                + [ctypes.c_size_t, _P]),
     "moe_test_muon_lost": (ctypes.c_int, [ctypes.c_int]),
     "moe_muon_error_word": (ctypes.c_int, [ctypes.POINTER(_P)]),
     "moe_muon_get_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
@@ -415,6 +434,29 @@ def moe_topk_gate_backward(cfg, logits, ids, d_scores, d_logits, stream=None):
     _check("moe_topk_gate_backward",
            LIB.moe_topk_gate_backward(ctypes.byref(cfg), _ptr(logits), _ptr(ids), _ptr(d_scores), _ptr(d_logits),
                                       _stream(stream)))
+
+
+def moe_dropout(cfg, x, residual, rng, out, stream=None):
+    _check("moe_dropout", LIB.moe_dropout(ctypes.byref(cfg), _ptr(x), _ptr(residual), _ptr(rng), _ptr(out),
+                                          _stream(stream)))
+
+
+def moe_layer_norm_forward(cfg, x, branch, weight, bias, rng, y, h, stats=None, stream=None):
+    _check("moe_layer_norm_forward",
+           LIB.moe_layer_norm_forward(ctypes.byref(cfg), _ptr(x), _ptr(branch), _ptr(weight), _ptr(bias), _ptr(rng),
+                                      _ptr(y), _ptr(h), _ptr(stats), _stream(stream)))
+
+
+def moe_layer_norm_workspace_bytes(cfg):
+    return LIB.moe_layer_norm_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_layer_norm_backward(cfg, y, weight, stats, rng, dy, dh, dx, dbranch, dweight, dbias, workspace, workspace_bytes,
+                            stream=None):
+    _check("moe_layer_norm_backward",
+           LIB.moe_layer_norm_backward(ctypes.byref(cfg), _ptr(y), _ptr(weight), _ptr(stats), _ptr(rng), _ptr(dy),
+                                       _ptr(dh), _ptr(dx), _ptr(dbranch), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                       workspace_bytes, _stream(stream)))
 
 
 def moe_test_muon_lost(product):

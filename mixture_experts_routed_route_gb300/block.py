@@ -1,10 +1,12 @@
 """What a transformer block runs around the routed layer, on torch tensors:
 the norms before and after a block with its gate and scaled residual
-(``block_norm``), and the router's choice of experts with its scores
-(``topk_gate``), each with its backward.
+(``block_norm``), layer norm with the scaled residual and dropout on the branch
+(``layer_norm``), dropout alone (``dropout``), and the router's choice of
+experts with its scores (``topk_gate``), each with its backward.
 
 Argument checks and buffers are here; every computation runs in the CUDA
-library (``moe_block_norm_*`` and ``moe_topk_gate_*`` of the C ABI).  Calls
+library (``moe_block_norm_*``, ``moe_layer_norm_*``, ``moe_dropout`` and
+``moe_topk_gate_*`` of the C ABI).  Calls
 enqueue on the current stream of the inputs' device, or on ``stream`` (a torch
 stream or a raw handle); buffers that a call makes are allocated on the stream
 it runs on.  Inputs that another stream still writes are the caller's to
@@ -23,6 +25,7 @@ from . import abi
 
 _TYPE = {torch.bfloat16: abi.MOE_TYPE_BF16, torch.float32: abi.MOE_TYPE_FP32}
 _NormConfig, _GateConfig = abi.moe_block_norm_config, abi.moe_topk_gate_config
+_LayerNormConfig, _DropoutConfig = abi.moe_layer_norm_config, abi.moe_dropout_config
 _SCORE = {"softmax": abi.MOE_SCORE_SOFTMAX, "sigmoid": abi.MOE_SCORE_SIGMOID}
 
 
@@ -32,7 +35,7 @@ _MOST = 1 << 31
 # the raw handle of a device's current stream (torch.cuda.current_stream builds a Stream object each time)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
-_BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _FP32, _INT32, _INT64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _empty, _empty_like, _byref = torch.empty, torch.empty_like, ctypes.byref
 _LIB, _INVALID = abi.LIB, abi.MOE_ERR_INVALID_ARG
 
@@ -349,5 +352,169 @@ def topk_gate_backward(logits, ids, d_scores, *, score="softmax", renormalize=Fa
                 return d
             raise abi.MoEError("moe_topk_gate_backward", status)
         return d
+
+    return on_stream(run, dev, stream)
+
+
+def _check_rng(p, rng, site, device):
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"dropout: expected a probability, got {p}")
+    if not 0 <= site < 1 << 32:
+        raise ValueError("site: expected an integer of 32 bits")
+    if rng is None:
+        _need(p == 0.0, "dropout needs rng, an int64 tensor [seed, step] on the device")
+    else:
+        _dense("rng", rng, _INT64, (2,), device)
+
+
+def dropout(x, p, rng, *, site=0, residual=None, out=None, stream=None):
+    """keep * x / (1 - p) (+ residual) of a [T, D] bfloat16 or float32 tensor,
+    x's type.  The mask is a function of rng (an int64 [2] tensor on x's
+    device: seed and step), ``site`` (which call of a step this is) and the
+    element's place in [T, D] alone; it is not stored, and ``dropout_backward``
+    (or the same call on the gradient) draws it again.  rng is read on the
+    device: a program, also within a captured graph, advances its step in place
+    (``rng[1] += 1``) for new masks.  p counts in steps of 2^-16.  Dropped
+    elements give 0 whatever x holds there.  ``out`` may be x or residual."""
+    kind, shape, dev = x.dtype, x.shape, x.device
+    if len(shape) != 2 or kind not in _TYPE or dev.type != "cuda":
+        raise ValueError("x: expected a CUDA bfloat16 or float32 [T, D] tensor")
+    if shape[0] >= _MOST or shape[1] >= _MOST:
+        raise ValueError("x: sizes have to be below 2^31")
+    _check_rng(p, rng, site, dev)
+    cfg = _DropoutConfig(shape[0], shape[1], _TYPE[kind], site, p, _rows("x", x, kind, shape, dev))
+    if residual is not None:
+        cfg.residual_stride = _rows("residual", residual, kind, shape, dev)
+    if out is not None:
+        cfg.out_stride = _rows("out", out, kind, shape, dev)
+
+    def run(s):
+        o = _new(x, kind) if out is None else out
+        status = _LIB.moe_dropout(_byref(cfg), x.data_ptr(), _at(residual), _at(rng), o.data_ptr(), s)
+        if status:
+            if status == _INVALID and unaligned(x, residual, rng, out):
+                filled = _room(o)
+                dropout(aligned(x), p, aligned(rng), site=site, residual=aligned(residual), out=filled)
+                put_back((o, filled))
+                return o
+            raise abi.MoEError("moe_dropout", status)
+        return o
+
+    return on_stream(run, dev, stream)
+
+
+def dropout_backward(dout, p, rng, *, site=0, dx=None, stream=None):
+    """The gradient of dropout's x from that of its result, at the forward's
+    p, rng and site (a residual's gradient is dout itself)."""
+    return dropout(dout, p, rng, site=site, out=dx, stream=stream)
+
+
+def _layer_norm_config(name, x, weight, bias, residual_scale, branch_scale, dropout, rng, site, eps):
+    kind, shape, dev = x.dtype, x.shape, x.device
+    if len(shape) != 2 or kind not in _TYPE or dev.type != "cuda":
+        raise ValueError(f"{name}: expected a CUDA bfloat16 or float32 [T, D] tensor")
+    T, D = shape
+    if T >= _MOST or D >= _MOST:
+        raise ValueError(f"{name}: sizes have to be below 2^31")
+    par = _FP32
+    for which, w in (("weight", weight), ("bias", bias)):
+        if w is not None:
+            if w.dtype not in _TYPE:
+                raise ValueError("weight and bias are bfloat16 or float32")
+            _dense(which, w, w.dtype if which == "weight" or weight is None else weight.dtype, (D,), dev)
+            par = w.dtype
+    _check_rng(dropout, rng, site, dev)
+    return _LayerNormConfig(T, D, _TYPE[kind], _TYPE[par], residual_scale, branch_scale, eps, site, dropout,
+                            _rows(name, x, kind, shape, dev), 0, 0, 0)
+
+
+def layer_norm(x, branch=None, *, weight=None, bias=None, residual_scale=1.0, branch_scale=1.0, dropout=0.0, rng=None,
+               site=0, eps=1e-5, y=None, h=None, stats=None, stream=None):
+    """(y, h) of one block boundary:
+
+        y = residual_scale * x + branch_scale * dropout(branch)
+        h = (y - mean(y)) / sqrt(var(y) + eps) * weight + bias
+
+    x: [T, D] bfloat16 or float32; branch: [T, D] bfloat16 or None (a norm
+    alone: y is then x, and is written only where a ``y`` is given or the
+    residual is scaled).  h is bfloat16.  weight, bias: [D] of one type, or
+    None.  dropout, rng and site as in ``dropout``, whose mask on the branch
+    this is.  ``y`` may be x and ``h`` may be branch (in place; the backward
+    reads y alone).  ``stats``: a float32 [2, T] tensor for the backward to
+    read (mean and 1 / sqrt(var + eps))."""
+    cfg = _layer_norm_config("x", x, weight, bias, residual_scale, branch_scale, dropout, rng, site, eps)
+    shape, dev = x.shape, x.device
+    if branch is not None:
+        cfg.branch_stride = _rows("branch", branch, _BF16, shape, dev)
+    else:
+        _need(dropout == 0.0, "dropout needs a branch")
+    if y is not None:
+        cfg.y_stride = _rows("y", y, x.dtype, shape, dev)
+    if h is not None:
+        cfg.h_stride = _rows("h", h, _BF16, shape, dev)
+    if stats is not None:
+        _dense("stats", stats, _FP32, (2, shape[0]), dev)
+    same = branch is None and y is None and residual_scale == 1.0
+
+    def run(s):
+        yy = y if y is not None or same else _new(x, x.dtype)
+        hh = h if h is not None else _new(x, _BF16)
+        status = _LIB.moe_layer_norm_forward(_byref(cfg), x.data_ptr(), _at(branch), _at(weight), _at(bias), _at(rng),
+                                             _at(yy), hh.data_ptr(), _at(stats), s)
+        if status:
+            if status == _INVALID and unaligned(x, branch, weight, bias, rng, y, h, stats):
+                filled = _room(y), _room(h), aligned(stats)
+                yy, hh = layer_norm(aligned(x), aligned(branch), weight=aligned(weight), bias=aligned(bias),
+                                    residual_scale=cfg.residual_scale, branch_scale=cfg.branch_scale, dropout=dropout,
+                                    rng=aligned(rng), site=site, eps=cfg.eps, y=filled[0], h=filled[1], stats=filled[2])
+                put_back((y, filled[0]), (h, filled[1]), (stats, filled[2]))
+                return x if same else yy if y is None else y, hh if h is None else h
+            raise abi.MoEError("moe_layer_norm_forward", status)
+        return (x if same else yy), hh
+
+    return on_stream(run, dev, stream)
+
+
+class LayerNormGrads(NamedTuple):
+    dx: torch.Tensor
+    dbranch: Optional[torch.Tensor]
+    dweight: Optional[torch.Tensor]
+    dbias: Optional[torch.Tensor]
+
+
+def layer_norm_backward(y, stats, dh, dy=None, *, weight=None, bias=None, branch=True, residual_scale=1.0,
+                        branch_scale=1.0, dropout=0.0, rng=None, site=0, stream=None):
+    """Gradients (LayerNormGrads) of layer_norm's inputs from ``dh`` (bfloat16)
+    and ``dy`` (y's type; None: zero), with the forward's y and ``stats``.
+    branch: whether the forward had one (dbranch is bfloat16).  weight and
+    bias: the forward's; each that is given gets its gradient, float32.  dropout,
+    rng and site: the forward's."""
+    cfg = _layer_norm_config("y", y, weight, bias, residual_scale, branch_scale, dropout, rng, site, 1.0)
+    shape, dev = y.shape, y.device
+    T, D = shape
+    cfg.h_stride = _rows("dh", dh, _BF16, shape, dev)
+    if dy is not None:
+        cfg.y_stride = _rows("dy", dy, y.dtype, shape, dev)
+    _dense("stats", stats, _FP32, (2, T), dev)
+    _need(branch or dropout == 0.0, "dropout needs a branch")
+
+    def run(s):
+        dx = _new(y, y.dtype)
+        dbranch = _new(y, _BF16) if branch else None
+        dweight = None if weight is None else _empty(D, dtype=_FP32, device=dev)
+        dbias = None if bias is None else _empty(D, dtype=_FP32, device=dev)
+        ref = _byref(cfg)
+        nb = _LIB.moe_layer_norm_workspace_bytes(ref)
+        ws = _empty(nb, dtype=torch.uint8, device=dev)
+        status = _LIB.moe_layer_norm_backward(ref, y.data_ptr(), _at(weight), stats.data_ptr(), _at(rng), _at(dy),
+                                              dh.data_ptr(), dx.data_ptr(), _at(dbranch), _at(dweight), _at(dbias),
+                                              ws.data_ptr(), nb, s)
+        if status:
+            if status == _INVALID and unaligned(y, stats, dh, dy, weight, rng):
+                return layer_norm_backward(aligned(y), aligned(stats), aligned(dh), aligned(dy), weight=aligned(weight),
+                                           bias=bias, branch=branch, residual_scale=cfg.residual_scale,
+                                           branch_scale=cfg.branch_scale, dropout=dropout, rng=aligned(rng), site=site)
+            raise abi.MoEError("moe_layer_norm_backward", status)
+        return LayerNormGrads(dx, dbranch, dweight, dbias)
 
     return on_stream(run, dev, stream)
