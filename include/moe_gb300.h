@@ -866,6 +866,61 @@ MOE_API moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, con
                                            void* dx, void* dbranch, float* dweight, float* dbias, void* workspace,
                                            size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Softmax cross entropy of logits = logit_scale * h W^T over a large
+ * vocabulary, whose logits are never in memory as a whole:
+ *   lse = log sum_v exp(logits),  loss = lse - logits[target] + z_weight * lse^2
+ * A target equal to ignore_index does not count: loss 0, lse 0, no gradient,
+ * whatever h holds in that row, and its row costs no product.  Any other
+ * target outside [0, V) gives loss NaN (lse 0) and no gradient.
+ *   h        bf16 [T, D], rows h_stride elements apart (0: D)
+ *   weight   bf16 [V, D]
+ *   targets  int32 or int64 [T] (target_bytes 4 or 8)
+ *   loss, lse  float [T]
+ * Operands are BF16, products are summed in FP32, and so are the softmax's sums.
+ *
+ * moe_linear_ce_backward: from d_loss (float [T], gradient of each loss) and the
+ * forward's inputs and lse:
+ *   dh       bf16 [T, D] contiguous, or NULL; zeros in rows that do not count
+ *   dweight  bf16 [V, D], overwritten, or NULL; zeros with T = 0
+ * It forms the logits again, a piece of the vocabulary at a time; the gradient
+ * of the logits is rounded to BF16 (at most 2^-8 relative) between the products.
+ *
+ * workspace: 256-byte aligned, contents need not be kept or cleared, at least
+ * moe_linear_ce_workspace_bytes(cfg, backward, piece) for pieces of `piece`
+ * vocabulary entries (rounded up to a multiple of 256; the forward takes any piece).
+ * The backward works in the largest pieces that the workspace holds; less than
+ * one of 256 is MOE_ERR_CAPACITY.  The size depends on the current device's SM
+ * count; 0 for a cfg that the calls refuse.  Sums run in a fixed order for one
+ * device and workspace size.
+ * device_error_word: as for moe_muon_update (moe_muon_error_word is fine): a
+ * device wait that ran out of time sets MOE_DEV_ERR_TIMEOUT, and the outputs of
+ * that call are not to be used.
+ * T may be 0.  Pointers 16-byte aligned.  Errors: MOE_ERR_INVALID_ARG (null or
+ * misaligned pointers, sizes < 1 or T < 0, target_bytes, logit_scale not finite
+ * and positive, z_weight negative or not finite, h_stride in (0, D)),
+ * MOE_ERR_UNSUPPORTED (D not a multiple of 8 or above 65536, T or V above 2^24,
+ * 2^30 or more tiles of 256 x 256), MOE_ERR_CAPACITY.
+ */
+typedef struct {
+  int32_t tokens;          /* T */
+  int32_t d_model;         /* D */
+  int32_t vocab;           /* V */
+  int32_t target_bytes;    /* 4 or 8 */
+  float logit_scale, z_weight;
+  int64_t ignore_index;
+  int64_t h_stride;
+} moe_linear_ce_config;
+
+MOE_API size_t moe_linear_ce_workspace_bytes(const moe_linear_ce_config* cfg, int backward, int32_t piece);
+MOE_API moe_status moe_linear_ce_forward(const moe_linear_ce_config* cfg, const void* h, const void* weight,
+                                         const void* targets, float* loss, float* lse, void* workspace,
+                                         size_t workspace_bytes, uint32_t* device_error_word, cudaStream_t stream);
+MOE_API moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h, const void* weight,
+                                          const void* targets, const float* lse, const float* d_loss, void* dh,
+                                          void* dweight, void* workspace, size_t workspace_bytes,
+                                          uint32_t* device_error_word, cudaStream_t stream);
+
 /* Library version string. */
 MOE_API const char* moe_version(void);
 

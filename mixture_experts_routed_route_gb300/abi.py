@@ -116,6 +116,12 @@ class moe_layer_norm_config(ctypes.Structure):
                 ("h_stride", ctypes.c_int64)]
 
 
+class moe_linear_ce_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("d_model", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("target_bytes", ctypes.c_int32), ("logit_scale", ctypes.c_float), ("z_weight", ctypes.c_float),
+                ("ignore_index", ctypes.c_int64), ("h_stride", ctypes.c_int64)]
+
+
 class moe_muon_config(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
                 ("steps", ctypes.c_int32), ("coefficients", ctypes.c_float * 3 * MOE_MUON_MAX_STEPS),
@@ -186,6 +192,11 @@ _SIGNATURES = {
     "moe_layer_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_layer_norm_config)]),
     "moe_layer_norm_backward": (ctypes.c_int, [ctypes.POINTER(moe_layer_norm_config)] + [_P] * 11
                                 + [ctypes.c_size_t, _P]),
+    "moe_linear_ce_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_linear_ce_config), ctypes.c_int,
+                                                        ctypes.c_int32]),
+    "moe_linear_ce_forward": (ctypes.c_int, [ctypes.POINTER(moe_linear_ce_config)] + [_P] * 6 + [ctypes.c_size_t, _P, _P]),
+    "moe_linear_ce_backward": (ctypes.c_int, [ctypes.POINTER(moe_linear_ce_config)] + [_P] * 8 + [ctypes.c_size_t, _P,
+                                                                                                  _P]),
     "moe_test_muon_lost": (ctypes.c_int, [ctypes.c_int]),
     "moe_muon_error_word": (ctypes.c_int, [ctypes.POINTER(_P)]),
     "moe_muon_get_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
@@ -457,6 +468,24 @@ def moe_layer_norm_backward(cfg, y, weight, stats, rng, dy, dh, dx, dbranch, dwe
            LIB.moe_layer_norm_backward(ctypes.byref(cfg), _ptr(y), _ptr(weight), _ptr(stats), _ptr(rng), _ptr(dy),
                                        _ptr(dh), _ptr(dx), _ptr(dbranch), _ptr(dweight), _ptr(dbias), _ptr(workspace),
                                        workspace_bytes, _stream(stream)))
+
+
+def moe_linear_ce_workspace_bytes(cfg, backward, piece):
+    return LIB.moe_linear_ce_workspace_bytes(ctypes.byref(cfg), int(backward), piece)
+
+
+def moe_linear_ce_forward(cfg, h, weight, targets, loss, lse, workspace, workspace_bytes, device_error_word, stream=None):
+    _check("moe_linear_ce_forward",
+           LIB.moe_linear_ce_forward(ctypes.byref(cfg), _ptr(h), _ptr(weight), _ptr(targets), _ptr(loss), _ptr(lse),
+                                     _ptr(workspace), workspace_bytes, _ptr(device_error_word), _stream(stream)))
+
+
+def moe_linear_ce_backward(cfg, h, weight, targets, lse, d_loss, dh, dweight, workspace, workspace_bytes,
+                           device_error_word, stream=None):
+    _check("moe_linear_ce_backward",
+           LIB.moe_linear_ce_backward(ctypes.byref(cfg), _ptr(h), _ptr(weight), _ptr(targets), _ptr(lse), _ptr(d_loss),
+                                      _ptr(dh), _ptr(dweight), _ptr(workspace), workspace_bytes, _ptr(device_error_word),
+                                      _stream(stream)))
 
 
 def moe_test_muon_lost(product):

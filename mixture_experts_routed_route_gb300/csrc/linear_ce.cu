@@ -1,0 +1,845 @@
+// Softmax cross entropy of logits = scale h W^T over a large vocabulary
+// without the logits in memory, and its gradient (moe_linear_ce_forward /
+// _backward).
+//
+//   lse_t = log sum_v exp l_tv,   loss_t = lse_t - l_t,target + z lse_t^2
+//   g_tv = dl_t ((1 + 2 z lse_t) softmax_tv - [v = target]) scale
+//   dh = g W,   dW = g^T h
+//
+// Rows whose target is ignored take no part: the rows that count are packed
+// into a copy of h (zeros up to a multiple of 256 rows), and every product
+// runs over that many rows, read on the device.  So ignored tokens cost
+// nothing, and what their rows of h hold (a NaN, infinities) reaches no sum.
+//
+// Products, on the tensor cores (tcgen05.mma kind::f16, BF16 operands, FP32
+// accumulators), 256 x 256 output tiles on CTA pairs, one persistent launch
+// each:
+//   lse    h W^T:   a tile's epilogue keeps each row's maximum and sum of
+//                   exponentials over its columns; a small kernel joins them
+//   grad   h W^T again, for a piece of the vocabulary: the epilogue turns the
+//                   logits into g, rounded to BF16
+//   dh     g W:     W read MN-major; partial sums over the vocabulary in FP32,
+//                   one store or one reduce-add by TMA a piece
+//   dW     g^T h:   both operands read MN-major
+// g is the one rounding between the accumulators and the results: 2^-8 at most,
+// relative, as much as the results' own.
+// Exponentials are in base 2 with one fused product, exp2(l k - m), k = scale
+// log2 e: the rounding is relative to the small difference.
+//
+// Warp roles: warp 0 TMA producer, warp 1 TMEM allocation and (rank 0) MMA
+// issue for the pair, warps 2 .. 9 epilogue (lane quadrant w % 4, half of the
+// tile's columns each).  A thread has its own row of the accumulator, so the
+// softmax needs no exchange between threads.
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "moe_gb300.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kTile = 256;         // rows and columns of a pair's tile
+constexpr int kBk = 64;            // contraction elements a stage: 128 bytes
+constexpr int kOperand = 128 * kBk * 2;
+constexpr int kStage = 2 * kOperand;
+constexpr int kStages = 6;
+constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * 4096 + 256;
+static_assert(kSmem <= 232448, "shared memory per CTA");
+constexpr int kGroup = 8;          // row tiles that share the columns' operand before the next ones
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+constexpr float kLowest = -1.0e30f;
+
+enum CeKind { kLse, kGrad, kDh, kDw };
+
+struct CeParams {
+  const int* count;      // rows that count
+  int rows_cap;          // their capacity, a multiple of 256
+  int D, V;
+  int v0, vn;            // piece of the vocabulary: first, number (backward)
+  int splits;            // dh: parts of the contraction
+  int first;             // dh: store (else add)
+  float k;               // scale log2 e
+  const int* target;     // [rows_cap], -1 past the rows
+  float2* part;          // lse: [2 column tiles][rows_cap]: maximum of l k, sum of exp2(l k - maximum)
+  float* hit;            // lse: l_target (before the scale)
+  const float* lse2;     // grad: lse log2 e
+  const float2* coef;    // grad: scale dl (1 + 2 z lse), scale dl
+  uint32_t* err;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Both CTAs' loads of a stage complete on rank 0's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* tm, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+// MN-major tile in the 128-byte swizzle: groups of 64 elements along M (or N),
+// each 64 rows (contraction elements) of 128 bytes; 8-row atoms 1024 bytes
+// apart along the contraction, groups 8 KB apart.
+__device__ __forceinline__ uint64_t sdesc_mn_bf16(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192 >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kWaitTimeoutCycles / 8) return;
+  }
+}
+
+// The products' sizes and the order of their tiles.
+template <int KIND>
+struct CeWork {
+  int m, n;              // output rows and columns
+  int mt, nt, total;
+  int k, split_steps;    // contraction, stages of 64 of a split
+  int splits;
+
+  __device__ __forceinline__ CeWork(const CeParams& p, int rows) {
+    m = KIND == kDw ? p.vn : rows;
+    n = KIND == kLse ? p.V : KIND == kGrad ? p.vn : p.D;
+    k = KIND == kDh ? p.vn : KIND == kDw ? rows : p.D;
+    mt = (m + kTile - 1) / kTile;
+    nt = (n + kTile - 1) / kTile;
+    splits = KIND == kDh ? p.splits : 1;
+    total = mt * nt * splits;
+    split_steps = ((k + kBk - 1) / kBk + splits - 1) / splits;
+  }
+};
+struct CeTile {
+  int row0, col0, n, split, ks0, ks;
+};
+// Groups of kGroup row tiles; within one, column after column.
+template <int KIND>
+__device__ __forceinline__ CeTile ce_tile(const CeWork<KIND>& w, int tile) {
+  CeTile t;
+  const int per = w.mt * w.nt;
+  t.split = KIND == kDh ? tile / per : 0;
+  int i = tile - t.split * per;
+  const int g = i / (kGroup * w.nt);
+  i -= g * kGroup * w.nt;
+  const int rows = min(kGroup, w.mt - g * kGroup);
+  const int c = i / rows;
+  t.row0 = (g * kGroup + i - c * rows) * kTile;
+  t.col0 = c * kTile;
+  t.n = w.n - t.col0 <= 128 ? 128 : 256;
+  t.ks0 = t.split * w.split_steps;
+  t.ks = max(0, min(w.split_steps, (w.k + kBk - 1) / kBk - t.ks0));
+  return t;
+}
+
+// One 16-byte piece of a warp's 32 rows x 128 bytes, in the 128-byte swizzle.
+__device__ __forceinline__ void stage16(uint8_t* ws, int lane, int piece, uint4 v) {
+  *reinterpret_cast<uint4*>(ws + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
+}
+
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmC, const CeParams p) {
+  constexpr bool kAMn = KIND == kDw, kBMn = KIND == kDh || KIND == kDw;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* turn = smem + kStages * kStage;    // [8 warps][32 rows x 128 bytes]
+  uint64_t* full = reinterpret_cast<uint64_t*>(turn + kEpiWarps * 4096);   // rank 0: both CTAs' operands landed
+  uint64_t* empty = full + kStages;    // the stage's MMAs are done
+  uint64_t* tfull = empty + kStages;   // [2] an accumulator is complete
+  uint64_t* tempty = tfull + 2;        // [2] rank 0: both CTAs drained it
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch(&tmA);
+    tma_prefetch(&tmB);
+    if (KIND != kLse) tma_prefetch(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc_cg<2>(tmem_slot, 512);
+    tmem_relinquish_cg<2>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  cluster_sync();   // the other CTA's barriers exist before anything arrives on them
+  after_previous();
+  const CeWork<KIND> w(p, *p.count);
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = cid; ok && tile < w.total; tile += ncl) {
+      const CeTile t = ce_tile<KIND>(w, tile);
+      const int arow = t.row0 + 128 * rank;                                  // this CTA's rows of A
+      const int brow = t.col0 + t.n / 2 * rank + (KIND == kGrad ? p.v0 : 0);   // its half of the N rows
+      for (int ks = 0; ks < t.ks; ++ks, ++it) {
+        const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&empty[slot], ph ^ 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          uint8_t* sa = smem + slot * kStage;
+          uint8_t* sb = sa + kOperand;
+          const uint32_t bar = cluster_addr(&full[slot], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * kStage);
+          const int k0 = (t.ks0 + ks) * kBk;
+          if constexpr (kAMn) {
+            tma_load_2d_pair(sa, &tmA, bar, arow, k0);
+            tma_load_2d_pair(sa + kOperand / 2, &tmA, bar, arow + 64, k0);
+          } else {
+            tma_load_2d_pair(sa, &tmA, bar, k0, arow);
+          }
+          if constexpr (kBMn) {
+            const int kb = k0 + (KIND == kDh ? p.v0 : 0);
+            tma_load_2d_pair(sb, &tmB, bar, brow, kb);
+            tma_load_2d_pair(sb + kOperand / 2, &tmB, bar, brow + 64, kb);
+          } else {
+            tma_load_2d_pair(sb, &tmB, bar, k0, brow);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // no load of either CTA may still be landing when the cluster exits
+    if (lane == 0 && rank == 0) {
+      const uint32_t pend = it < static_cast<uint32_t>(kStages) ? it : static_cast<uint32_t>(kStages);
+      for (uint32_t j = 0; j < pend; ++j) {
+        const uint32_t i2 = it - 1 - j;
+        drain_wait(&full[i2 % kStages], (i2 / kStages) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ----------------------------------------------------- MMA issuer
+      // BF16 operands, FP32 accumulators; bits 15, 16: A, B MN-major
+      const uint32_t idesc0 = idesc_bf16(0, 256) | (kAMn ? kIdescAMnMajor : 0u) | (kBMn ? (1u << 16) : 0u);
+      uint32_t it = 0, tc = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < w.total; tile += ncl, ++tc) {
+        const CeTile t = ce_tile<KIND>(w, tile);
+        const uint32_t idesc = idesc0 | ((static_cast<uint32_t>(t.n) >> 3) << 17);
+        const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + acc * 256;
+        for (int ks = 0; ks < t.ks; ++ks, ++it) {
+          const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&full[slot], ph, abort_flag, p.err))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t sa = smem_u32(smem + slot * kStage), sb = sa + kOperand;
+#pragma unroll
+            for (int j = 0; j < kBk / 16; ++j) {
+              const uint64_t ad = kAMn ? sdesc_mn_bf16(sa + j * 2048) : sdesc_k_sw128(sa + j * 32);
+              const uint64_t bd = kBMn ? sdesc_mn_bf16(sb + j * 2048) : sdesc_k_sw128(sb + j * 32);
+              mma_bf16_pair(d_tmem, ad, bd, idesc, (ks | j) ? 1u : 0u);
+            }
+            tc_commit_pair_mc(&empty[slot], 3);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) tc_commit_pair_mc(&tfull[acc], 3);
+        __syncwarp();
+      }
+      if (lane == 0 && it > 0) {
+        tc_commit_pair(drain);
+        drain_wait(drain, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    // --------------------------------------------------------- epilogue
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    uint8_t* ws = turn + (warp - 2) * 4096;
+    const uint32_t tempty0 = cluster_addr(tempty, 0);
+    uint32_t tc = 0;
+    for (int tile = cid; tile < w.total; tile += ncl, ++tc) {
+      const CeTile t = ce_tile<KIND>(w, tile);
+      const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+      const int row = t.row0 + 128 * rank + 32 * q + lane;     // this thread's
+      const int row_w = row - lane;
+      const int cols = t.n / 2, c0 = t.col0 + h * cols;        // this warp's columns
+      int target = -1;
+      float top = kLowest, sum = 0.0f, hit = 0.0f;
+      float lse2 = 0.0f;
+      float2 coef = make_float2(0.0f, 0.0f);
+      if constexpr (KIND == kLse || KIND == kGrad) {
+        target = p.target[row] - (KIND == kGrad ? p.v0 : 0);
+        if constexpr (KIND == kGrad) {
+          lse2 = p.lse2[row];
+          coef = p.coef[row];
+        }
+      }
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int ci = 0; ci < cols / 32; ++ci) {
+        uint32_t v[32];
+        tmem_ld32(tbase + 32 * ci, v);
+        tmem_ld_wait();
+        if (ci == cols / 32 - 1) {   // every column has been read: the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
+        }
+        const int c = c0 + 32 * ci;
+        if constexpr (KIND == kLse) {
+          if (c + 32 > w.n) {   // past the vocabulary
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j >= w.n) v[j] = __float_as_uint(-INFINITY);
+          }
+          if (static_cast<unsigned>(target - c) < 32u) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (target - c == j) hit = __uint_as_float(v[j]);
+            p.hit[row] = hit;
+          }
+          float m = __uint_as_float(v[0]);
+#pragma unroll
+          for (int j = 1; j < 32; ++j) m = fmaxf(m, __uint_as_float(v[j]));
+          m = fmaxf(top, m * p.k);
+          sum *= exp2_fast(top - m);
+          top = m;
+          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast(fmaf(__uint_as_float(v[j]), p.k, -m));
+          sum += (s[0] + s[1]) + (s[2] + s[3]);
+        } else {
+          constexpr int kHalves = KIND == kDh ? 1 : 2;   // chunks of 32 columns in 128 bytes
+          float x[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+          if (KIND != kGrad && t.ks == 0) {   // an empty contraction
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+          }
+          if constexpr (KIND == kGrad) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = coef.x * exp2_fast(fmaf(x[j], p.k, -lse2));
+            if (static_cast<unsigned>(target - c) < 32u) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (target - c == j) x[j] -= coef.y;
+            }
+            if (c + 32 > w.n) {   // past the piece, whose end is the vocabulary's
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (c + j >= w.n) x[j] = 0.0f;
+            }
+          }
+          if (ci % kHalves == 0) {   // the stores that read the buffer before are done
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+          }
+          if constexpr (KIND == kDh) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              stage16(ws, lane, j, make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                                              __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              stage16(ws, lane, 4 * (ci % kHalves) + j,
+                      make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
+                                 pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7])));
+          }
+          if (ci % kHalves == kHalves - 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int cs = c - 32 * (kHalves - 1);
+              if constexpr (KIND == kGrad) {
+                tma_store_2d(&tmC, ws, cs, row_w);
+              } else if constexpr (KIND == kDh) {
+                if (cs < p.D) {
+                  if (p.first) tma_store_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
+                  else tma_reduce_add_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
+                }
+              } else {
+                if (cs < p.D && p.v0 + row_w < p.V) tma_store_2d(&tmC, ws, cs, p.v0 + row_w);
+              }
+              bulk_commit();
+            }
+          }
+        }
+      }
+      if constexpr (KIND == kLse) p.part[static_cast<long long>(2 * (t.col0 / kTile) + h) * p.rows_cap + row] = make_float2(top, sum);
+    }
+    if (KIND != kLse && lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();
+  if (warp == 1) tmem_dealloc_cg<2>(tmem, 512);
+}
+
+// ----------------------------------------------------- rows that count
+
+struct RowParams {
+  int T, D, V;
+  int rows_cap;
+  const void* targets;
+  int wide;              // int64 targets
+  long long ignore;
+  const __nv_bfloat16* h;
+  long long ldh;
+  int* count;
+  int* list;             // [rows_cap] token of each packed row, -1 past them
+  int* target;           // [rows_cap], -1 past them
+  int* inv;              // [T] packed row of each token, -1 (backward)
+  __nv_bfloat16* packed; // [rows_cap, D]
+  // forward
+  float* loss;
+  float* lse;
+  // backward
+  const float* lse_in;
+  const float* dloss;
+  float scale, z;
+  float* lse2;           // [rows_cap]
+  float2* coef;          // [rows_cap]
+};
+
+// The packed rows' tokens in order, one CTA: 1024 tokens a turn.  Tokens that
+// do not count get their results here: loss 0 (NaN for a target outside the
+// vocabulary), lse 0.
+__global__ void __launch_bounds__(1024) ce_rows_kernel(const __grid_constant__ RowParams p) {
+  __shared__ int warp_count[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int base = 0;
+  for (int t0 = 0, turn = 0; t0 < p.T; t0 += 1024, turn ^= 1) {
+    const int t = t0 + threadIdx.x;
+    long long target = p.ignore;
+    if (t < p.T) target = p.wide ? static_cast<const long long*>(p.targets)[t] : static_cast<const int*>(p.targets)[t];
+    const bool on = target != p.ignore && target >= 0 && target < p.V;
+    const unsigned vote = __ballot_sync(0xFFFFFFFFu, on);
+    if (lane == 0) warp_count[turn][warp] = __popc(vote);
+    __syncthreads();
+    const int mine = warp_count[turn][lane];
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int c = __shfl_sync(0xFFFFFFFFu, mine, i);
+      if (i < warp) before += c;
+      all += c;
+    }
+    const int at = base + before + __popc(vote & ((1u << lane) - 1));
+    if (on) {
+      p.list[at] = t;
+      p.target[at] = static_cast<int>(target);
+      if (p.coef) {
+        const float lse = p.lse_in[t], d = p.dloss[t] * p.scale;
+        p.lse2[at] = lse * kLog2e;
+        p.coef[at] = make_float2(d * fmaf(2.0f * p.z, lse, 1.0f), d);
+      }
+    } else if (t < p.T && p.loss) {
+      p.loss[t] = target == p.ignore ? 0.0f : NAN;
+      p.lse[t] = 0.0f;
+    }
+    if (t < p.T && p.inv) p.inv[t] = on ? at : -1;
+    base += all;
+  }
+  if (threadIdx.x == 0) *p.count = base;
+  const int end = (base + kTile - 1) / kTile * kTile;
+  for (int i = base + threadIdx.x; i < end; i += 1024) {
+    p.list[i] = -1;
+    p.target[i] = -1;
+    if (p.coef) {
+      p.lse2[i] = 0.0f;
+      p.coef[i] = make_float2(0.0f, 0.0f);
+    }
+  }
+}
+
+// Packed copy of h, one row a block, zeros from the last row to a multiple of 256.
+__global__ void __launch_bounds__(256) ce_pack_kernel(const __grid_constant__ RowParams p) {
+  after_previous();
+  const int count = *p.count, end = (count + kTile - 1) / kTile * kTile;
+  for (int i = blockIdx.x; i < end; i += gridDim.x) {
+    const int t = p.list[i];
+    uint4* out = reinterpret_cast<uint4*>(p.packed + static_cast<long long>(i) * p.D);
+    const __nv_bfloat16* in = p.h + static_cast<long long>(t) * p.ldh;
+    for (int c = threadIdx.x; c < p.D / 8; c += 256) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (t >= 0) {
+        if (p.ldh % 8 == 0) {
+          v = reinterpret_cast<const uint4*>(in)[c];
+        } else {
+          const unsigned short* s = reinterpret_cast<const unsigned short*>(in) + 8 * c;
+          v.x = s[0] | static_cast<uint32_t>(s[1]) << 16;
+          v.y = s[2] | static_cast<uint32_t>(s[3]) << 16;
+          v.z = s[4] | static_cast<uint32_t>(s[5]) << 16;
+          v.w = s[6] | static_cast<uint32_t>(s[7]) << 16;
+        }
+      }
+      out[c] = v;
+    }
+  }
+}
+
+// loss and lse of the packed rows from the tiles' maxima and sums: 32 rows a
+// block, 32 threads a row.
+__global__ void __launch_bounds__(1024) ce_join_kernel(const float2* part, const float* hit, const int* list,
+                                                       const int* count, int parts, int rows_cap, float k, float z,
+                                                       float* loss, float* lse) {
+  __shared__ float2 s[32][33];
+  after_previous();
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + x, n = *count;
+  if (static_cast<int>(blockIdx.x) * 32 >= n) return;
+  float top = kLowest, sum = 0.0f;
+  if (row < n) {
+#pragma unroll 4
+    for (int i = y; i < parts; i += 32) {
+      const float2 q = part[static_cast<long long>(i) * rows_cap + row];
+      const float m = fmaxf(top, q.x);
+      sum = sum * exp2_fast(top - m) + q.y * exp2_fast(q.x - m);
+      top = m;
+    }
+  }
+  s[y][x] = make_float2(top, sum);
+  __syncthreads();
+  if (y == 0 && row < n) {
+    for (int i = 1; i < 32; ++i) {
+      const float2 q = s[i][x];
+      const float m = fmaxf(top, q.x);
+      sum = sum * exp2_fast(top - m) + q.y * exp2_fast(q.x - m);
+      top = m;
+    }
+    // in base 2 until the end: the loss is rounded relative to itself
+    const float l2 = top + log2f(sum), l = l2 * kLn2;
+    const int t = list[row];
+    lse[t] = l;
+    loss[t] = fmaf(z * l, l, (fmaf(-hit[row], k, top) + log2f(sum)) * kLn2);
+  }
+}
+
+// dh: the sum of the splits' FP32 rows, rounded; zeros for tokens that do not count.
+__global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, int splits, int rows_cap, const int* inv, int T,
+                                                    int D, __nv_bfloat16* dh) {
+  after_previous();
+  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    const int i = inv[t];
+    for (int c = threadIdx.x; c < D / 8; c += 256) {
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+      if (i >= 0) {
+        for (int s = 0; s < splits; ++s) {
+          const float4* q = reinterpret_cast<const float4*>(part + (static_cast<long long>(s) * rows_cap + i) * D) + 2 * c;
+          const float4 u = q[0], v = q[1];
+          a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
+          b.x += v.x, b.y += v.y, b.z += v.z, b.w += v.w;
+        }
+      }
+      reinterpret_cast<uint4*>(dh + static_cast<long long>(t) * D)[c] =
+          make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+bool config_ok(const moe_linear_ce_config* c) {
+  if (!c || c->tokens < 0 || c->d_model < 1 || c->vocab < 1) return false;
+  if (c->target_bytes != 4 && c->target_bytes != 8) return false;
+  if (!(c->logit_scale > 0.0f) || c->logit_scale > 1.0e30f) return false;
+  if (!(c->z_weight >= 0.0f) || c->z_weight > 1.0e30f) return false;
+  return c->h_stride == 0 || c->h_stride >= c->d_model;
+}
+bool supported(const moe_linear_ce_config* c) {
+  if (c->d_model % 8 != 0 || c->d_model > 65536 || c->vocab > (1 << 24) || c->tokens > (1 << 24)) return false;
+  const long long row_tiles = (c->tokens + kTile - 1) / kTile, col_tiles = (c->vocab + kTile - 1) / kTile;
+  return row_tiles * col_tiles < (1ll << 30);   // tiles are counted in 32 bits
+}
+
+// Parts of the vocabulary that the dh product sums apart, so that its tiles
+// fill the pairs: the fewest whose last round is fullest, a part being worth
+// three percent of a round (its sums are written and read once more).
+int dh_splits(int T, int D, int pairs) {
+  const long long tiles = static_cast<long long>((T + kTile - 1) / kTile) * ((D + kTile - 1) / kTile);
+  int best = 1;
+  double cost = 1e30;
+  for (int s = 1; s <= 16; ++s) {
+    const long long n = tiles * s;
+    const double c = static_cast<double>((n + pairs - 1) / pairs) * pairs / static_cast<double>(n) + 0.03 * s;
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct Layout {
+  int rows_cap, col_tiles, splits;
+  int64_t piece;          // vocabulary entries a piece, a multiple of 256
+  size_t count, list, target, inv, lse2, coef, hit, part, packed, g, dh, bytes;
+};
+size_t take(size_t* at, size_t n) {
+  const size_t r = *at;
+  *at += (n + 255) / 256 * 256;
+  return r;
+}
+Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int sms) {
+  Layout l{};
+  l.rows_cap = (c->tokens + kTile - 1) / kTile * kTile;
+  l.col_tiles = (c->vocab + kTile - 1) / kTile;
+  l.piece = std::min<int64_t>(piece, static_cast<int64_t>(l.col_tiles) * kTile);
+  l.splits = dh_splits(c->tokens, c->d_model, sms / 2);
+  const size_t rows = l.rows_cap, D = c->d_model;
+  size_t at = 0;
+  l.count = take(&at, 4);
+  l.list = take(&at, rows * 4);
+  l.target = take(&at, rows * 4);
+  l.packed = take(&at, rows * D * 2);
+  if (backward) {
+    l.inv = take(&at, rows * 4);
+    l.lse2 = take(&at, rows * 4);
+    l.coef = take(&at, rows * 8);
+    l.dh = take(&at, rows * D * 4 * l.splits);
+    l.g = take(&at, rows * 2 * l.piece);
+  } else {
+    l.hit = take(&at, rows * 4);
+    l.part = take(&at, rows * 8 * 2 * l.col_tiles);
+  }
+  l.bytes = at;
+  return l;
+}
+
+// 2D map of a row-major matrix, 128-byte boxes of `box_rows` rows.
+bool map_2d(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int box_rows, bool f32) {
+  const int esz = f32 ? 4 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * esz};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esz), static_cast<cuuint32_t>(box_rows)};
+  return make_tmap_nd(tm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+                      box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int KIND>
+cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
+                        long long tiles, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  cudaError_t e = once.once(
+      [&] { return cudaFuncSetAttribute(ce_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+  if (e != cudaSuccess) return e;
+  void* args[] = {const_cast<CUtensorMap*>(&a), const_cast<CUtensorMap*>(&b), const_cast<CUtensorMap*>(&c),
+                  const_cast<CeParams*>(&p)};
+  const int grid = 2 * static_cast<int>(std::max<long long>(1, std::min<long long>(pairs, tiles)));
+  return launch_dependent(reinterpret_cast<const void*>(ce_gemm_kernel<KIND>), dim3(grid), kThreads, kSmem, stream, args);
+}
+
+cudaError_t launch_rows(const RowParams& p, int sms, cudaStream_t stream) {
+  ce_rows_kernel<<<1, 1024, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  void* args[] = {const_cast<RowParams*>(&p)};
+  return launch_dependent(reinterpret_cast<const void*>(ce_pack_kernel), dim3(std::min(p.rows_cap, 8 * sms)), 256, 0,
+                          stream, args);
+}
+
+template <typename X>
+X* at(void* base, size_t off) {
+  return reinterpret_cast<X*>(static_cast<uint8_t*>(base) + off);
+}
+
+// What the calls share: rows packed, parameters of the products.
+void fill(const moe_linear_ce_config* c, const Layout& l, const void* h, const void* targets, void* ws, uint32_t* err,
+          RowParams* r, CeParams* p) {
+  r->T = c->tokens;
+  r->D = c->d_model;
+  r->V = c->vocab;
+  r->rows_cap = l.rows_cap;
+  r->targets = targets;
+  r->wide = c->target_bytes == 8;
+  r->ignore = c->ignore_index;
+  r->h = static_cast<const __nv_bfloat16*>(h);
+  r->ldh = c->h_stride ? c->h_stride : c->d_model;
+  r->count = at<int>(ws, l.count);
+  r->list = at<int>(ws, l.list);
+  r->target = at<int>(ws, l.target);
+  r->packed = at<__nv_bfloat16>(ws, l.packed);
+  r->scale = c->logit_scale;
+  r->z = c->z_weight;
+  p->count = r->count;
+  p->rows_cap = l.rows_cap;
+  p->D = c->d_model;
+  p->V = c->vocab;
+  p->splits = 1;
+  p->k = c->logit_scale * kLog2e;
+  p->target = r->target;
+  p->err = err;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_linear_ce_workspace_bytes(const moe_linear_ce_config* cfg, int backward, int32_t piece) {
+  if (!config_ok(cfg) || !supported(cfg) || piece < 1) return 0;
+  const int sms = device_sms();
+  if (sms < 2) return 0;
+  return lay_out(cfg, backward != 0, (static_cast<int64_t>(piece) + kTile - 1) / kTile * kTile, sms).bytes;
+}
+
+moe_status moe_linear_ce_forward(const moe_linear_ce_config* cfg, const void* h, const void* weight, const void* targets,
+                                 float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                                 uint32_t* device_error_word, cudaStream_t stream) {
+  if (!config_ok(cfg)) return MOE_ERR_INVALID_ARG;
+  if (!supported(cfg)) return MOE_ERR_UNSUPPORTED;
+  if (cfg->tokens == 0) return MOE_OK;
+  for (const void* q : {h, weight, targets, static_cast<const void*>(loss), static_cast<const void*>(lse)})
+    if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MOE_ERR_INVALID_ARG;
+  if (!device_error_word || (reinterpret_cast<uintptr_t>(device_error_word) & 3)) return MOE_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms < 2) return MOE_ERR_CUDA;
+  const Layout l = lay_out(cfg, false, kTile, sms);
+  if (workspace_bytes < l.bytes) return MOE_ERR_CAPACITY;
+  RowParams r{};
+  CeParams p{};
+  fill(cfg, l, h, targets, workspace, device_error_word, &r, &p);
+  r.loss = loss;
+  r.lse = lse;
+  p.part = at<float2>(workspace, l.part);
+  p.hit = at<float>(workspace, l.hit);
+  CUtensorMap a, b;
+  if (!map_2d(&a, r.packed, l.rows_cap, cfg->d_model, 128, false) ||
+      !map_2d(&b, weight, cfg->vocab, cfg->d_model, 128, false))
+    return MOE_ERR_CUDA;
+  if (launch_rows(r, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_gemm<kLse>(a, b, a, p, sms / 2, static_cast<long long>(l.rows_cap / kTile) * l.col_tiles, stream) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  int parts = 2 * l.col_tiles;
+  float k = p.k, z = cfg->z_weight;
+  const float2* part = p.part;
+  const float* hit = p.hit;
+  const int* list = r.list;
+  const int* count = r.count;
+  int cap = l.rows_cap;
+  void* args[] = {&part, &hit, &list, &count, &parts, &cap, &k, &z, &loss, &lse};
+  if (launch_dependent(reinterpret_cast<const void*>(ce_join_kernel), dim3((cfg->tokens + 31) / 32), 1024, 0, stream, args) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h, const void* weight, const void* targets,
+                                  const float* lse, const float* d_loss, void* dh, void* dweight, void* workspace,
+                                  size_t workspace_bytes, uint32_t* device_error_word, cudaStream_t stream) {
+  if (!config_ok(cfg)) return MOE_ERR_INVALID_ARG;
+  if (!supported(cfg)) return MOE_ERR_UNSUPPORTED;
+  const int T = cfg->tokens, D = cfg->d_model, V = cfg->vocab;
+  if (T == 0) {   // no rows: the weight's gradient is zero
+    if (!aligned16(dweight)) return MOE_ERR_INVALID_ARG;
+    return !dweight || cudaMemsetAsync(dweight, 0, 2ull * V * D, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  for (const void* q : {h, weight, targets, static_cast<const void*>(lse), static_cast<const void*>(d_loss)})
+    if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if ((!dh && !dweight) || !aligned16(dh) || !aligned16(dweight)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MOE_ERR_INVALID_ARG;
+  if (!device_error_word || (reinterpret_cast<uintptr_t>(device_error_word) & 3)) return MOE_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms < 2) return MOE_ERR_CUDA;
+  // the largest pieces that the workspace holds
+  Layout l = lay_out(cfg, true, kTile, sms);
+  if (workspace_bytes < l.bytes) return MOE_ERR_CAPACITY;
+  const size_t more = (workspace_bytes - l.bytes) / (static_cast<size_t>(l.rows_cap) * 2 * kTile);
+  const int64_t most = static_cast<int64_t>(std::min<size_t>(more + 1, l.col_tiles));   // tiles of 256 entries a piece
+  const int64_t pieces = (l.col_tiles + most - 1) / most;
+  l = lay_out(cfg, true, (l.col_tiles + pieces - 1) / pieces * kTile, sms);
+  RowParams r{};
+  CeParams p{};
+  fill(cfg, l, h, targets, workspace, device_error_word, &r, &p);
+  r.lse_in = lse;
+  r.dloss = d_loss;
+  r.inv = at<int>(workspace, l.inv);
+  r.lse2 = at<float>(workspace, l.lse2);
+  r.coef = at<float2>(workspace, l.coef);
+  p.lse2 = r.lse2;
+  p.coef = r.coef;
+  p.splits = l.splits;
+  __nv_bfloat16* g = at<__nv_bfloat16>(workspace, l.g);
+  float* part = at<float>(workspace, l.dh);
+  CUtensorMap hk, hm, wk, wm, gk, gm, gs, ds, os;
+  if (!map_2d(&hk, r.packed, l.rows_cap, D, 128, false) || !map_2d(&hm, r.packed, l.rows_cap, D, 64, false) ||
+      !map_2d(&wk, weight, V, D, 128, false) || !map_2d(&wm, weight, V, D, 64, false) ||
+      !map_2d(&gk, g, l.rows_cap, l.piece, 128, false) || !map_2d(&gm, g, l.rows_cap, l.piece, 64, false) ||
+      !map_2d(&gs, g, l.rows_cap, l.piece, 32, false) ||
+      !map_2d(&os, part, static_cast<int64_t>(l.rows_cap) * l.splits, D, 32, true) ||
+      (dweight && !map_2d(&ds, dweight, V, D, 32, false)))
+    return MOE_ERR_CUDA;
+  if (launch_rows(r, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  const long long row_tiles = l.rows_cap / kTile, d_tiles = (D + kTile - 1) / kTile;
+  for (int64_t v0 = 0; v0 < V; v0 += l.piece) {
+    p.v0 = static_cast<int>(v0);
+    p.vn = static_cast<int>(std::min<int64_t>(l.piece, V - v0));
+    p.first = v0 == 0;
+    const long long v_tiles = (p.vn + kTile - 1) / kTile;
+    if (launch_gemm<kGrad>(hk, wk, gs, p, sms / 2, row_tiles * v_tiles, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dh && launch_gemm<kDh>(gk, wm, os, p, sms / 2, row_tiles * d_tiles * l.splits, stream) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    if (dweight && launch_gemm<kDw>(gm, hm, ds, p, sms / 2, v_tiles * d_tiles, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (dh) {
+    int splits = l.splits, cap = l.rows_cap, t = T, d = D;
+    const float* in = part;
+    const int* inv = r.inv;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dh);
+    void* args[] = {&in, &splits, &cap, &inv, &t, &d, &out};
+    if (launch_dependent(reinterpret_cast<const void*>(ce_dh_kernel), dim3(std::min(T, 8 * sms)), 256, 0, stream, args) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"
