@@ -4,8 +4,13 @@
 // the [T, D] tensor, whatever its strides.
 //
 // A thread takes groups of eight elements, which share one block of the
-// generator, kBatch of them with all loads sent first.  What bounds it is the
-// stream, once long.
+// generator, one after the other, the next one's loads ahead of this one's mask.
+// What bounds it: 32 x 32 -> 64 bit products take 4 cycles a warp, and 19 of them a
+// group are 76 cycles where BF16's bytes take 70 (16384 x 7168: 77.6 us, 6.05 TB/s;
+// floor 69); in FP32 the stream alone (139 us, 6.76 TB/s).  On the way there, BF16: four groups a
+// thread at a time with 98 registers 133 us (22 % of the warps: products and
+// logic, which run in different pipes, hardly overlapped), the first round's product
+// with the site once a thread, dropped places cleared in the packed words.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -17,7 +22,10 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;
+// CTAs an SM at most, of which eight run at a time: a few groups a thread spread the keys'
+// cost, and many CTAs keep the SMs evenly busy (16384 x 7168 in BF16: 8 an SM
+// 79.9 us, 16 78.4, 64 77.6; in FP32 148, 147, 139).
+constexpr int kCtas = 64;
 
 struct DropoutParams {
   long long groups;          // of eight elements
@@ -31,23 +39,51 @@ struct DropoutParams {
   DropParams drop;
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-  v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                            pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+// Eight elements as they lie in memory.
+template <typename X>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+    v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+  // zeros where dropped, on the packed words: after the rounding, two elements an instruction
+  __device__ __forceinline__ void drop(const uint4& m) { u = make_uint4(u.x & m.x, u.y & m.y, u.z & m.z, u.w & m.w); }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void drop(const uint4& m) {
+    float v[8];
+    get(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!kept(m, j)) v[j] = 0.0f;
+    set(v);
+  }
+};
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
@@ -60,94 +96,97 @@ enum Layout {
   kAny      // element by element
 };
 
-template <typename X, int LAYOUT>
+// Group g element by element.
+template <typename X>
+__device__ __forceinline__ void scalar_group(const DropoutParams& p, const PhiloxKey<true>& key, long long g) {
+  uint4 m = make_uint4(~0u, ~0u, ~0u, ~0u);
+  if (p.drop.rng) m = keep_words(p.drop, philox(key, g));
+  long long t = g * 8 / p.D;
+  int d = static_cast<int>(g * 8 - t * p.D);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (g * 8 + j >= p.n) return;
+    float v = to_f(static_cast<const X*>(p.x)[t * p.ldx + d]);
+    v = kept(m, j) ? v * p.drop.scale : 0.0f;
+    if (p.residual) v += to_f(static_cast<const X*>(p.residual)[t * p.ldr + d]);
+    put(static_cast<X*>(p.out) + t * p.ldo + d, v);
+    if (++d == p.D) {
+      d = 0;
+      ++t;
+    }
+  }
+}
+
+template <typename X, int LAYOUT, bool RES>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutParams p) {
   const X* x = static_cast<const X*>(p.x);
   const X* res = static_cast<const X*>(p.residual);
   X* out = static_cast<X*>(p.out);
-  const bool drop = p.drop.rng != nullptr;
-  PhiloxKey key{};
-  if (drop) key = philox_key(p.drop);
-  const long long g0 = static_cast<long long>(blockIdx.x) * (kThreads * kBatch) + threadIdx.x;
+  const long long hop = static_cast<long long>(gridDim.x) * kThreads;
+  long long g = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  PhiloxKey<true> key{};
+  if (p.drop.rng) key = philox_key<true>(p.drop);
   if constexpr (LAYOUT == kAny) {
-    for (int b = 0; b < kBatch; ++b) {
-      const long long g = g0 + b * kThreads;
-      if (g >= p.groups) return;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (drop) w = philox(key, g);
-      long long t = g * 8 / p.D;
-      int d = static_cast<int>(g * 8 - t * p.D);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (g * 8 + j >= p.n) return;
-        float v = to_f(x[t * p.ldx + d]);
-        v = !drop || kept(w, j, p.drop.threshold) ? v * p.drop.scale : 0.0f;
-        if (res) v += to_f(res[t * p.ldr + d]);
-        put(out + t * p.ldo + d, v);
-        if (++d == p.D) {
-          d = 0;
-          ++t;
-        }
-      }
-    }
-    return;
+    for (; g < p.groups; g += hop) scalar_group<X>(p, key, g);
   } else {
-    long long at[kBatch][3];
-    bool on[kBatch];
-    float v[kBatch][8], r[kBatch][8];
+    // row and group in the row, moved on by adding: no division in the loop
+    long long t = 0, d = g, hop_t = 0, hop_d = hop;
+    if (LAYOUT == kRows) {
+      t = g / p.row_groups;
+      d = g - t * p.row_groups;
+      hop_t = hop / p.row_groups;
+      hop_d = hop - hop_t * p.row_groups;
+    }
+    const long long whole = p.n / 8;
+    Raw<X> v, r;
+    if (g < whole) {
+      v.load(x + t * p.ldx + d * 8);
+      if (RES) r.load(res + t * p.ldr + d * 8);
+    }
+    for (; g < whole; g += hop) {
+      X* o = out + t * p.ldo + d * 8;
+      t += hop_t;
+      d += hop_d;
+      if (LAYOUT == kRows && d >= p.row_groups) {
+        d -= p.row_groups;
+        ++t;
+      }
+      Raw<X> nv, nr;   // the next group is on its way while this one's mask is drawn
+      if (g + hop < whole) {
+        nv.load(x + t * p.ldx + d * 8);
+        if (RES) nr.load(res + t * p.ldr + d * 8);
+      }
+      uint4 m = make_uint4(~0u, ~0u, ~0u, ~0u);
+      if (p.drop.rng) m = keep_words(p.drop, philox(key, g));
+      float f[8];
+      v.get(f);
+      if constexpr (RES) {
+        float s[8];
+        r.get(s);
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const long long g = g0 + b * kThreads;
-      on[b] = (g + 1) * 8 <= p.n;
-      if constexpr (LAYOUT == kFlat) {
-        at[b][0] = at[b][1] = at[b][2] = g * 8;
+        for (int j = 0; j < 8; ++j) f[j] = kept(m, j) ? fmaf(f[j], p.drop.scale, s[j]) : s[j];
+        v.set(f);
       } else {
-        const long long t = g / p.row_groups;
-        const long long d = (g - t * p.row_groups) * 8;
-        at[b][0] = t * p.ldx + d;
-        at[b][1] = t * p.ldr + d;
-        at[b][2] = t * p.ldo + d;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= p.drop.scale;
+        v.set(f);
+        v.drop(m);
       }
-      if (on[b]) load8(x + at[b][0], v[b]);
+      v.store(o);
+      v = nv;
+      r = nr;
     }
-    if (res) {
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (on[b]) load8(res + at[b][1], r[b]);
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const long long g = g0 + b * kThreads;
-      if (g >= p.groups) continue;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (drop) w = philox(key, g);
-      if (on[b]) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[b][j] = !drop || kept(w, j, p.drop.threshold) ? v[b][j] * p.drop.scale : 0.0f;
-          if (res) v[b][j] += r[b][j];
-        }
-        store8(out + at[b][2], v[b]);
-      } else {   // the last elements of a flat tensor
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const long long e = g * 8 + j;
-          if (e < p.n) {
-            float u = !drop || kept(w, j, p.drop.threshold) ? to_f(x[e]) * p.drop.scale : 0.0f;
-            if (res) u += to_f(res[e]);
-            put(out + e, u);
-          }
-        }
-      }
-    }
+    if (LAYOUT == kFlat && g == whole && g < p.groups) scalar_group<X>(p, key, g);   // the last elements
   }
 }
 
 template <typename X>
 void launch(int layout, unsigned grid, const DropoutParams& p, cudaStream_t stream) {
-  if (layout == kFlat) dropout_kernel<X, kFlat><<<grid, kThreads, 0, stream>>>(p);
-  else if (layout == kRows) dropout_kernel<X, kRows><<<grid, kThreads, 0, stream>>>(p);
-  else dropout_kernel<X, kAny><<<grid, kThreads, 0, stream>>>(p);
+  if (layout == kAny) dropout_kernel<X, kAny, false><<<grid, kThreads, 0, stream>>>(p);
+  else if (layout == kFlat && p.residual) dropout_kernel<X, kFlat, true><<<grid, kThreads, 0, stream>>>(p);
+  else if (layout == kFlat) dropout_kernel<X, kFlat, false><<<grid, kThreads, 0, stream>>>(p);
+  else if (p.residual) dropout_kernel<X, kRows, true><<<grid, kThreads, 0, stream>>>(p);
+  else dropout_kernel<X, kRows, false><<<grid, kThreads, 0, stream>>>(p);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -186,8 +225,9 @@ moe_status moe_dropout(const moe_dropout_config* cfg, const void* x, const void*
   int layout = kAny;
   if (cfg->tokens == 1 || (p.ldx == p.D && p.ldr == p.D && p.ldo == p.D)) layout = kFlat;
   else if (p.D % 8 == 0 && p.ldx % 8 == 0 && p.ldr % 8 == 0 && p.ldo % 8 == 0) layout = kRows;
-  const long long per = kThreads * kBatch, grid = (p.groups + per - 1) / per;
-  if (grid > 0x7FFFFFFFll) return MOE_ERR_UNSUPPORTED;
+  const int sms = device_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const long long grid = std::min<long long>((p.groups + kThreads - 1) / kThreads, kCtas * sms);
   if (cfg->type == MOE_TYPE_FP32) launch<float>(layout, static_cast<unsigned>(grid), p, stream);
   else launch<__nv_bfloat16>(layout, static_cast<unsigned>(grid), p, stream);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -13,20 +13,33 @@
 // Reading y instead of x and o saves the backward a stream.
 //
 // Work layout: persistent CTAs, one per SM.  A group of W warps owns a row, P
-// pieces of 8 columns a thread; as many groups share a CTA as its threads and
-// shared memory hold, and take rows in turns over the CTAs.  Rows come in
-// through a ring in shared memory by cp.async; a thread copies just the pieces
-// it reads itself, so the copies need no barrier.
+// pieces of 8 columns a thread; as many groups share a CTA as its threads hold,
+// and take rows in turns over the CTAs.  The forward keeps a row in registers
+// from its one read to its results, and sends for the next row as soon as the
+// row's own values have been used.  The backward, whose registers hold the
+// column sums, has its rows in flight in a ring in shared memory (cp.async; a
+// thread copies the pieces it reads itself, so the copies need no barrier).
+// Dropout's mask of the next row is drawn while that row is under way.
+//
+// What bounds it (BF16 with a branch, one GB300): the stream.  Forward 2048 x 7168 21.3 us
+// (5.5 TB/s; floor 17.3), 8192 x 7168 75.5 us (6.2 TB/s); the backward with its second
+// kernel 39.5 us (floor 21.6) and 106 us (5.6 TB/s).  Short inputs add a fixed part (launch, first
+// row, last stores; the backward's column sums and second kernel, 17 us).  Dropout adds the generator's
+// products, 4 cycles a warp each, beside the norm's own arithmetic: forward 27.9 and 90.8 us, backward 48.8 us.
+// Tried and slower: forward rows through a ring too (27.5 us, 88.7 us), 24 warps
+// (80 registers: one row in flight a CTA, 24.7 us), one piece a thread (25.6 us); backward with rows
+// in registers (56 us, spills), 28 warps without a row's normalised values kept (53.7 us), a dependent launch
+// of the second kernel (40.5 us).
 //
 // Widths that 8 does not divide: row t starts t D mod 8 elements past a
 // 16-byte boundary.  Each group's rows are a multiple of 8 apart, so for it
 // that offset is one number: its pieces are the aligned ones, shifted by it
 // against the columns, with the columns' factors shifted as well and the row's
-// ends masked.  Every access stays a whole vector, the generator's groups of
-// eight coincide with the pieces, and a thread's columns are the same in every
-// row, so that column sums stay in registers.  A tensor whose rows start
-// elsewhere (a stride that differs from D modulo 8) is read and written
-// element by element in the same layout.
+// ends masked.  Every access but at the ends stays a whole vector, the
+// generator's groups of eight coincide with the pieces, and a thread's columns
+// are the same in every row, so that column sums stay in registers.  A tensor
+// whose rows start elsewhere (a stride that differs from D modulo 8) is read
+// and written element by element in the same layout.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -38,39 +51,29 @@ namespace moe {
 namespace {
 
 constexpr int kMaxCols = 8192;
-constexpr int kSharedMem = 216 * 1024;   // the columns' factors and the rows in flight
-constexpr int kMaxThreads = 896;         // of a CTA: 72 registers a thread
-constexpr int kMaxGroups = 15;           // named barriers 1 .. 15
-constexpr int kMaxWarps = 28;
+constexpr int kFwdThreads = 896;   // of a CTA: 72 registers a thread
+constexpr int kBwdThreads = 512;   // 128 registers: the column sums and a row's normalised values stay in them
+constexpr int kMaxGroups = 15;     // named barriers 1 .. 15
 
-struct Stream {
-  const uint8_t* base;   // NULL: not there
-  long long ld;          // elements between rows
-  const uint8_t* end;    // past the last row's last element
-  int off;               // place in a row's slot
-  int vec;               // its rows start where the layout's do, modulo 8 elements
-};
-// forward: x, branch; backward: y, dh, dy
-enum { kX = 0, kO = 1, kY = 0, kDh = 1, kDy = 2, kStreams = 3 };
-
-struct Out {
-  void* base;            // NULL: not wanted
-  long long ld;
-  int vec;
+struct Tensor {
+  void* base;      // NULL: not there
+  long long ld;    // elements between rows
+  int vec;         // its rows start where the layout's do, modulo 8 elements
+  const uint8_t* end;   // past its last element
 };
 
 struct LnParams {
   int T, D;
-  int warps, groups, stages, slot;
-  int table;             // bytes of the columns' factors
-  Stream in[kStreams];
+  int warps, groups;
+  int stages, slot;      // backward: rows in flight per group, bytes of one
+  Tensor x, o, dy, dh;   // forward: x, branch; backward: x is y
+  Tensor out0;           // y; dx
+  Tensor out1;           // h; dbranch
   const void* weight;    // or NULL
   const void* bias;      // forward, or NULL
   int params_f32;
   float alpha, beta, eps;
   DropParams drop;
-  Out out0;              // y; dx
-  Out out1;              // h; dbranch
   float* stats;          // [2][T]: mean, 1/sqrt(var + eps)
   float* partial;        // backward: [2][gridDim.x][D]: sums of dh n, dh
 };
@@ -106,8 +109,6 @@ __device__ __forceinline__ float sum2(Pair v) {
   return a + b;
 }
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ float param_at(const void* p, int f32, int i) {
@@ -120,39 +121,72 @@ __device__ __forceinline__ float inv_sqrt(float x) {
   return r < INFINITY && r > 0.0f ? r * fmaf(-0.5f * x * r, r, 1.5f) : r;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// the first `bytes` of 16, zeros after them
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, Pair (&q)[4]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  q[0] = pair_of(bf16_lo(u.x), bf16_hi(u.x));
-  q[1] = pair_of(bf16_lo(u.y), bf16_hi(u.y));
-  q[2] = pair_of(bf16_lo(u.z), bf16_hi(u.z));
-  q[3] = pair_of(bf16_lo(u.w), bf16_hi(u.w));
-}
-__device__ __forceinline__ void load8(const float* p, Pair (&q)[4]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  q[0] = pair_of(a.x, a.y);
-  q[1] = pair_of(a.z, a.w);
-  q[2] = pair_of(b.x, b.y);
-  q[3] = pair_of(b.z, b.w);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const Pair (&q)[4]) {
-  float v[8];
+// Eight elements as they lie in memory.
+template <typename X>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void set(const Pair (&q)[4]) {
+    float v[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) split(q[j], v[2 * j], v[2 * j + 1]);
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                            pack_bf16x2(v[6], v[7]));
+    for (int j = 0; j < 4; ++j) split(q[j], v[2 * j], v[2 * j + 1]);
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  // element by element, those of the bits `on`; zeros elsewhere
+  __device__ __forceinline__ void gather(const __nv_bfloat16* p, uint32_t on) {
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = on >> j & 1 ? reinterpret_cast<const unsigned short*>(p)[j] : 0;
+    u = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+  __device__ __forceinline__ void only(uint32_t on) {   // zeros elsewhere
+    uint32_t* w[4] = {&u.x, &u.y, &u.z, &u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *w[j] &= (on >> (2 * j) & 1 ? 0x0000FFFFu : 0u) | (on >> (2 * j) & 2 ? 0xFFFF0000u : 0u);
+  }
+  __device__ __forceinline__ void keep(const uint4& m) { u = make_uint4(u.x & m.x, u.y & m.y, u.z & m.z, u.w & m.w); }
+  __device__ __forceinline__ void get(Pair (&q)[4]) const {
+    q[0] = pair_of(bf16_lo(u.x), bf16_hi(u.x));
+    q[1] = pair_of(bf16_lo(u.y), bf16_hi(u.y));
+    q[2] = pair_of(bf16_lo(u.z), bf16_hi(u.z));
+    q[3] = pair_of(bf16_lo(u.w), bf16_hi(u.w));
+  }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void gather(const float* p, uint32_t on) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = on >> j & 1 ? p[j] : 0.0f;
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void only(uint32_t on) {
+    float* w[8] = {&a.x, &a.y, &a.z, &a.w, &b.x, &b.y, &b.z, &b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!(on >> j & 1)) *w[j] = 0.0f;
+  }
+  __device__ __forceinline__ void get(Pair (&q)[4]) const {
+    q[0] = pair_of(a.x, a.y);
+    q[1] = pair_of(a.z, a.w);
+    q[2] = pair_of(b.x, b.y);
+    q[3] = pair_of(b.z, b.w);
+  }
+};
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const Pair (&q)[4]) {
+  Raw<__nv_bfloat16> v;
+  v.set(q);
+  *reinterpret_cast<uint4*>(p) = v.u;
 }
 __device__ __forceinline__ void store8(float* p, const Pair (&q)[4]) {
   float v[8];
@@ -162,21 +196,18 @@ __device__ __forceinline__ void store8(float* p, const Pair (&q)[4]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// A group of warps and its rows in flight.  Pieces are numbered from the
-// aligned start of a row; element j of piece c is column 8 c + j - off.
-// RAGGED: D is no multiple of 8 (off may be other than 0, ends are masked).
-template <typename R, int P, bool RAGGED>
+// A group of warps.  Pieces are numbered from the aligned start of a row;
+// element j of piece c is column 8 c + j - off.  ODD: D is no multiple of 8 (off
+// may be other than 0, ends are masked), or a tensor's rows start elsewhere.
+template <int P, bool ODD>
 struct Group {
   const LnParams& p;
   int grp, wig, nt, t, bar;
   int off, pieces;        // of its rows
   float* red;
   int turn = 0;
-  uint8_t* slots;
-  long long next_row, step;
-  int left, fill, take;
 
-  __device__ __forceinline__ Group(const LnParams& p_, uint8_t* shared, float (*red_all)[128]) : p(p_) {
+  __device__ __forceinline__ Group(const LnParams& p_, float (*red_all)[128]) : p(p_) {
     const int warp = threadIdx.x >> 5;
     grp = warp / p.warps;
     wig = warp - grp * p.warps;
@@ -184,21 +215,25 @@ struct Group {
     t = threadIdx.x - grp * nt;
     bar = 1 + grp;
     red = red_all[grp];
-    slots = shared + p.table + static_cast<size_t>(grp) * p.stages * p.slot;
     // rows blockIdx.x + a multiple of 8: the launcher makes gridDim.x one where it matters
-    off = RAGGED ? static_cast<int>((static_cast<long long>(blockIdx.x) * p.D) & 7) : 0;
-    pieces = RAGGED ? (p.D + off + 7) >> 3 : p.D >> 3;
+    off = ODD ? static_cast<int>((static_cast<long long>(blockIdx.x) * p.D) & 7) : 0;
+    pieces = ODD ? (p.D + off + 7) >> 3 : p.D >> 3;
+    for (int i = threadIdx.x; i < kMaxGroups * 128; i += blockDim.x) (&red_all[0][0])[i] = 0.0f;
   }
 
   __device__ __forceinline__ int piece(int i) const { return t + i * nt; }
-  __device__ __forceinline__ bool any(int i) const { return piece(i) < pieces; }
   __device__ __forceinline__ bool valid(int c, int j) const {
     return static_cast<unsigned>(8 * c + j - off) < static_cast<unsigned>(p.D);
   }
-  __device__ __forceinline__ bool whole(int c) const { return !RAGGED || (8 * c >= off && 8 * c + 8 <= p.D + off); }
+  __device__ __forceinline__ bool whole(int c) const { return !ODD || (8 * c >= off && 8 * c + 8 <= p.D + off); }
+  // Its columns of the row, a bit each.
+  __device__ __forceinline__ uint32_t columns(int c) const {
+    const int lo = max(0, off - 8 * c), hi = max(0, min(8, p.D + off - 8 * c));
+    return (0xFFu << lo) & (0xFFu >> (8 - hi));
+  }
   // zeros where the piece passes the row's ends
   __device__ __forceinline__ void mask(int c, Pair (&q)[4]) const {
-    if (RAGGED && !whole(c)) {
+    if (ODD && !whole(c)) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float a, b;
@@ -208,18 +243,17 @@ struct Group {
     }
   }
 
-  __device__ __forceinline__ void sync() const {
-    if (p.warps == 1) __syncwarp();
-    else named_bar_sync(bar, nt);
-  }
-
-  // Sums over the group in a fixed order: an xor tree in each warp, then the
-  // warps in order.  `red` holds two turns of 2 x 32 floats (zeros past the
+  // Sums over the group in a fixed order: an xor tree in each warp, then a tree
+  // over the warps.  `red` holds two turns of 2 x 32 floats (zeros past the
   // warps), so one barrier a sum is enough.
   __device__ __forceinline__ float warp_sums(const float* r) const {
     const float4* q = reinterpret_cast<const float4*>(r);
     float s = (q[0].x + q[0].y) + (q[0].z + q[0].w);
-    for (int k = 1; 4 * k < p.warps; ++k) s += (q[k].x + q[k].y) + (q[k].z + q[k].w);
+    if (p.warps > 4) s += (q[1].x + q[1].y) + (q[1].z + q[1].w);
+    if (p.warps > 8) s += ((q[2].x + q[2].y) + (q[2].z + q[2].w)) + ((q[3].x + q[3].y) + (q[3].z + q[3].w));
+    if (p.warps > 16)
+      s += (((q[4].x + q[4].y) + (q[4].z + q[4].w)) + ((q[5].x + q[5].y) + (q[5].z + q[5].w))) +
+           (((q[6].x + q[6].y) + (q[6].z + q[6].w)) + ((q[7].x + q[7].y) + (q[7].z + q[7].w)));
     return s;
   }
   __device__ __forceinline__ float sum(float v) {
@@ -232,93 +266,56 @@ struct Group {
     named_bar_sync(bar, nt);
     return warp_sums(r);
   }
+  // Two at once: the lower half of a warp carries a, the upper half b.
   __device__ __forceinline__ void sum_two(float& a, float& b) {
+    const bool upper = threadIdx.x & 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (p.warps == 1) {
+      a = __shfl_sync(0xFFFFFFFFu, v, 0);
+      b = __shfl_sync(0xFFFFFFFFu, v, 16);
+      return;
     }
-    if (p.warps == 1) return;
     float* r = red + turn;
     turn ^= 64;
-    if ((threadIdx.x & 31) == 0) {
-      r[wig] = a;
-      r[32 + wig] = b;
-    }
+    if ((threadIdx.x & 15) == 0) r[2 * (threadIdx.x & 16) + wig] = v;
     named_bar_sync(bar, nt);
     a = warp_sums(r);
     b = warp_sums(r + 32);
   }
 
-  // Send for stream k of the next row.
+  // Whether whole vectors may be read along the row: those at its ends hold
+  // elements of the rows beside it, but none past the tensor's end.
   template <typename X>
-  __device__ __forceinline__ void copy(int k) const {
-    const Stream& s = p.in[k];
-    if (s.base == nullptr) return;
-    X* slot = reinterpret_cast<X*>(slots + fill * p.slot + s.off);
-    const X* row = reinterpret_cast<const X*>(s.base) + next_row * s.ld - off;
-    if (s.vec) {
+  __device__ __forceinline__ bool vectors(const Tensor& s, long long row) const {
+    return !ODD || (s.vec && reinterpret_cast<const uint8_t*>(static_cast<const X*>(s.base) + row * s.ld - off + 8 * pieces) <= s.end);
+  }
+  // The thread's pieces of a row; anything past its ends.
+  template <typename X>
+  __device__ __forceinline__ void load(const Tensor& s, long long row, Raw<X> (&q)[P]) const {
+    const X* at = static_cast<const X*>(s.base) + row * s.ld + 8 * t - off;
+    if (vectors<X>(s, row)) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int c = piece(i);
-        if (c >= pieces) continue;
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(row + 8 * c);
-        const uint32_t dst = smem_u32(slot + 8 * c);
-#pragma unroll
-        for (int b = 0; b < 8 * static_cast<int>(sizeof(X)); b += 16) {
-          if constexpr (RAGGED) {   // no byte past the tensor's last element
-            const long long rest = s.end - (src + b);
-            cp_async16(dst + b, rest > 0 ? src + b : s.base, rest >= 16 ? 16 : rest > 0 ? static_cast<int>(rest) : 0);
-          } else {
-            cp_async16(dst + b, src + b);
-          }
-        }
-      }
+      for (int i = 0; i < P; ++i)
+        if (piece(i) < pieces) q[i].load(at + 8 * i * nt);
     } else {
 #pragma unroll 1
       for (int i = 0; i < P; ++i) {
-        const int c = piece(i);
-        if (c >= pieces) continue;
+        if (piece(i) >= pieces) continue;
+        Raw<X> v;
+        v.gather(at + 8 * i * nt, columns(piece(i)));
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (valid(c, j)) slot[8 * c + j] = row[8 * c + j];
+        for (int k = 0; k < P; ++k)
+          if (k == i) q[k] = v;
       }
     }
   }
-  __device__ __forceinline__ void send() {
-    if (left > 0) {
-      copy<R>(0);
-      copy<__nv_bfloat16>(1);
-      copy<R>(2);
-      next_row += step;
-      --left;
-      fill = fill + 1 == p.stages ? 0 : fill + 1;
-    }
-    cp_commit();
-  }
-  __device__ __forceinline__ void start(long long first, long long step_, int n) {
-    next_row = first;
-    step = step_;
-    left = n;
-    fill = 0;
-    take = -1;
-    for (int i = 0; i < p.stages; ++i) send();
-  }
-  // Make the next row ready: its slot.
-  __device__ __forceinline__ const uint8_t* next() {
-    take = take + 1 == p.stages ? 0 : take + 1;
-    if (p.stages == 1) cp_wait<0>();
-    else if (p.stages == 2) cp_wait<1>();
-    else if (p.stages == 3) cp_wait<2>();
-    else cp_wait<3>();
-    return slots + take * p.slot;
-  }
-
   // Piece c of a row of an output.
   template <typename X>
-  __device__ __forceinline__ void store(const Out& o, long long row, int c, const Pair (&q)[4]) const {
+  __device__ __forceinline__ void store(const Tensor& o, long long row, int c, const Pair (&q)[4]) const {
     X* at = static_cast<X*>(o.base) + row * o.ld + 8 * c - off;
-    if (o.vec && whole(c)) {
+    if (!ODD || (o.vec && whole(c))) {
       store8(at, q);
     } else {
       float v[8];
@@ -328,6 +325,27 @@ struct Group {
       for (int j = 0; j < 8; ++j)
         if (valid(c, j)) put(at + j, v[j]);
     }
+  }
+  // ... of one in BF16, zeros where `m` has them.
+  __device__ __forceinline__ void store(const Tensor& o, long long row, int c, const Pair (&q)[4], const uint4& m) const {
+    __nv_bfloat16* at = static_cast<__nv_bfloat16*>(o.base) + row * o.ld + 8 * c - off;
+    Raw<__nv_bfloat16> v;
+    v.set(q);
+    v.keep(m);
+    if (!ODD || (o.vec && whole(c))) {
+      *reinterpret_cast<uint4*>(at) = v.u;
+    } else {
+      const uint32_t w[4] = {v.u.x, v.u.y, v.u.z, v.u.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (valid(c, j)) reinterpret_cast<unsigned short*>(at)[j] = static_cast<unsigned short>(w[j >> 1] >> (16 * (j & 1)));
+    }
+  }
+  // Which of the row's elements dropout keeps: keep_words of each piece.
+  __device__ __forceinline__ void draw(const PhiloxKey<false>& key, long long row, uint4 (&m)[P]) const {
+    const unsigned long long group0 = static_cast<unsigned long long>(row * p.D) >> 3;
+#pragma unroll
+    for (int i = 0; i < P; ++i) m[i] = keep_words(p.drop, philox(key, group0 + piece(i)));
   }
 };
 
@@ -375,72 +393,68 @@ __device__ __forceinline__ void make_table(const LnParams& p, uint8_t* shared, i
   __syncthreads();
 }
 
-// q *= f where kept, 0 elsewhere.
-__device__ __forceinline__ void drop_scale(const PhiloxKey& key, const DropParams& d, unsigned long long group, float f,
-                                           Pair (&q)[4]) {
-  const uint4 w = philox(key, group);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float a, b;
-    split(q[j], a, b);
-    q[j] = pair_of(kept(w, 2 * j, d.threshold) ? a * f : 0.0f, kept(w, 2 * j + 1, d.threshold) ? b * f : 0.0f);
-  }
-}
-
-template <typename R, int P, bool RAGGED, bool DROP>
-__global__ void __launch_bounds__(kMaxThreads, 1) layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
+// ALL: a branch is there and y is written (the common call): a test around a
+// row's loads or stores keeps the compiler from moving anything past it, which
+// costs 17 % (8192 x 7168 without dropout: 72.9 and 84.1 us).
+template <typename R, int P, bool ODD, bool DROP, bool ALL>
+__global__ void __launch_bounds__(kFwdThreads, 1) layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) float red_all[kMaxGroups][128];
-  Group<R, P, RAGGED> g(p, shared, red_all);
-  const int planes = (p.D + 7 + (RAGGED ? 7 : 0)) >> 3;
-  const int first = g.grp * gridDim.x + blockIdx.x, step = gridDim.x * p.groups;
-  const int n = first < p.T ? (p.T - 1 - first) / step + 1 : 0;
-  for (int i = threadIdx.x; i < kMaxGroups * 128; i += blockDim.x) (&red_all[0][0])[i] = 0.0f;
-  g.start(first, step, n);
-  PhiloxKey key{};
-  if (DROP) key = philox_key(p.drop);
+  Group<P, ODD> g(p, red_all);
+  const int planes = (p.D + 7 + (ODD ? 7 : 0)) >> 3;
+  const long long step = static_cast<long long>(gridDim.x) * p.groups;
+  long long row = g.grp * gridDim.x + blockIdx.x;
+  const bool has_o = ALL || p.o.base != nullptr;
+  Raw<R> x[P];
+  Raw<__nv_bfloat16> o[P];
+  uint4 keep[P];
+  if (row < p.T) {
+    g.load(p.x, row, x);
+    if (has_o) g.load(p.o, row, o);
+  }
+  PhiloxKey<false> key{};
+  if (DROP) {
+    key = philox_key<false>(p.drop);
+    g.draw(key, row, keep);
+  }
   make_table<2>(p, shared, g.off, g.pieces, planes);
-  const bool has_o = p.in[kO].base != nullptr;
   const float inv_d = 1.0f / static_cast<float>(p.D), beta = p.beta * p.drop.scale;
-  long long row = first;
-  for (int it = 0; it < n; ++it, row += step) {
-    const uint8_t* slot = g.next();
-    const unsigned long long group0 = DROP ? static_cast<unsigned long long>(row * p.D) >> 3 : 0;
+  for (; row < p.T; row += step) {
     Pair y[P][4], s = both(0.0f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int c = g.piece(i);
-      if (c >= g.pieces) continue;
-      load8(reinterpret_cast<const R*>(slot + p.in[kX].off) + 8 * c, y[i]);
+      if (g.piece(i) >= g.pieces) continue;
+      x[i].get(y[i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[i][j] = mul2(y[i][j], both(p.alpha));
       if (has_o) {
-        Pair o[4];
-        load8(reinterpret_cast<const __nv_bfloat16*>(slot + p.in[kO].off) + 8 * c, o);
-        if constexpr (DROP) {
-          drop_scale(key, p.drop, group0 + c, beta, o);
+        Pair b[4];
+        if (DROP) o[i].keep(keep[i]);
+        o[i].get(b);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[i][j] = add2(y[i][j], o[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[i][j] = fma2(o[j], both(beta), y[i][j]);
-        }
+        for (int j = 0; j < 4; ++j) y[i][j] = fma2(b[j], both(beta), y[i][j]);
       }
-      g.mask(c, y[i]);
+      g.mask(g.piece(i), y[i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) s = add2(s, y[i][j]);
-      if (p.out0.base) g.template store<R>(p.out0, row, c, y[i]);
     }
-    g.send();
+    if (row + step < p.T) {
+      g.load(p.x, row + step, x);
+      if (has_o) g.load(p.o, row + step, o);
+    }
+    if (ALL || p.out0.base) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (g.piece(i) < g.pieces) g.template store<R>(p.out0, row, g.piece(i), y[i]);
+    }
     const float mean = g.sum(sum2(s)) * inv_d;
     s = both(0.0f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int c = g.piece(i);
-      if (c >= g.pieces) continue;
+      if (g.piece(i) >= g.pieces) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[i][j] = add2(y[i][j], both(-mean));
-      g.mask(c, y[i]);
+      g.mask(g.piece(i), y[i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) s = fma2(y[i][j], y[i][j], s);
     }
@@ -460,109 +474,179 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layer_norm_fwd_kernel(const __
       for (int j = 0; j < 4; ++j) w[j] = fma2(mul2(y[i][j], both(r)), w[j], b[j]);
       g.template store<__nv_bfloat16>(p.out1, row, c, w);
     }
+    if (DROP) g.draw(key, row + step, keep);   // while the next row is on its way
   }
-  cp_wait<0>();
 }
 
-template <typename R, int P, bool RAGGED, bool DROP>
-__global__ void __launch_bounds__(kMaxThreads, 1) layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A group's rows in flight: y, dh and dy in a ring of slots in shared memory.  A
+// thread copies just the pieces it will read itself, so nothing but its own
+// copies has to be waited for.
+template <typename R, int P, bool ODD, bool ALL>
+struct Ring {
+  const LnParams& p;
+  const Group<P, ODD>& g;
+  uint8_t* slots;
+  int planes, fill, take;
+  long long next;         // row to send for
+  long long step;
+
+  __device__ __forceinline__ Ring(const LnParams& p_, const Group<P, ODD>& g_, uint8_t* base, int planes_, long long first,
+                                  long long step_)
+      : p(p_), g(g_), slots(base + static_cast<size_t>(g_.grp) * p_.stages * p_.slot), planes(planes_), fill(0), take(-1),
+        next(first), step(step_) {
+    for (int i = 0; i < p.stages; ++i) send();
+  }
+  template <typename X>
+  __device__ __forceinline__ void copy(const Tensor& s, uint8_t* to) const {
+    const X* at = static_cast<const X*>(s.base) + next * s.ld + 8 * g.t - g.off;
+    X* dst = reinterpret_cast<X*>(to) + 8 * g.t;
+    const bool vectors = g.template vectors<X>(s, next);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c = g.piece(i);
+      if (c >= g.pieces) continue;
+      const X* src = at + 8 * i * g.nt;
+      if (vectors) {
+        const uint32_t d = smem_u32(dst + 8 * i * g.nt);
+        cp_async16(d, src);
+        if (sizeof(X) == 4) cp_async16(d + 16, src + 4);
+      } else {
+        Raw<X> q;
+        q.gather(src, g.columns(c));
+        *reinterpret_cast<Raw<X>*>(dst + 8 * i * g.nt) = q;
+      }
+    }
+  }
+  __device__ __forceinline__ void send() {
+    if (next < p.T) {
+      uint8_t* to = slots + fill * p.slot;
+      copy<R>(p.x, to);
+      copy<__nv_bfloat16>(p.dh, to + planes * 8 * sizeof(R));
+      if (ALL || p.dy.base) copy<R>(p.dy, to + planes * 8 * (sizeof(R) + 2));
+      next += step;
+      fill = fill + 1 == p.stages ? 0 : fill + 1;
+    }
+    cp_commit();
+  }
+  // Make the next row ready: its slot.
+  __device__ __forceinline__ const uint8_t* wait() {
+    take = take + 1 == p.stages ? 0 : take + 1;
+    if (p.stages == 1) cp_wait<0>();
+    else if (p.stages == 2) cp_wait<1>();
+    else if (p.stages == 3) cp_wait<2>();
+    else cp_wait<3>();
+    return slots + take * p.slot;
+  }
+};
+
+// ALL: dy is there, dx and dbranch are wanted (the common call).
+template <typename R, int P, bool ODD, bool DROP, bool ALL>
+__global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) float red_all[kMaxGroups][128];
-  Group<R, P, RAGGED> g(p, shared, red_all);
-  const int planes = (p.D + 7 + (RAGGED ? 7 : 0)) >> 3;
-  const int first = g.grp * gridDim.x + blockIdx.x, step = gridDim.x * p.groups;
-  const int n = first < p.T ? (p.T - 1 - first) / step + 1 : 0;
-  for (int i = threadIdx.x; i < kMaxGroups * 128; i += blockDim.x) (&red_all[0][0])[i] = 0.0f;
-  g.start(first, step, n);
-  PhiloxKey key{};
-  if (DROP) key = philox_key(p.drop);
+  Group<P, ODD> g(p, red_all);
+  const int planes = (p.D + 7 + (ODD ? 7 : 0)) >> 3;
+  const long long step = static_cast<long long>(gridDim.x) * p.groups;
+  long long row = g.grp * gridDim.x + blockIdx.x;
+  Ring<R, P, ODD, ALL> ring(p, g, shared + planes * 32, planes, row, step);
+  float mean = 0.0f, r = 0.0f;
+  if (row < p.T) {
+    mean = p.stats[row];
+    r = p.stats[p.T + row];
+  }
+  PhiloxKey<false> key{};
+  uint4 keep[P];
+  if (DROP) {
+    key = philox_key<false>(p.drop);
+    g.draw(key, row, keep);
+  }
   make_table<1>(p, shared, g.off, g.pieces, planes);
-  const bool has_dy = p.in[kDy].base != nullptr;
   const float inv_d = 1.0f / static_cast<float>(p.D), beta = p.beta * p.drop.scale;
   Pair sw[P][4], sb[P][4];   // sums over the group's rows of dh n and dh
 #pragma unroll
   for (int i = 0; i < P; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) sw[i][j] = sb[i][j] = both(0.0f);
-  long long row = first;
-  float mean = 0.0f, r = 0.0f;
-  if (n > 0) {
-    mean = p.stats[row];
-    r = p.stats[p.T + row];
-  }
-  for (int it = 0; it < n; ++it, row += step) {
-    const uint8_t* slot = g.next();
-    const R* ys = reinterpret_cast<const R*>(slot + p.in[kY].off);
-    const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(slot + p.in[kDh].off);
-    float mean1 = 0.0f, r1 = 0.0f;   // the next row's
-    if (it + 1 < n) {
-      mean1 = p.stats[row + step];
-      r1 = p.stats[p.T + row + step];
-    }
+  for (; row < p.T; row += step) {
+    const uint8_t* slot = ring.wait();
     const Pair r2 = both(r), mr = both(-mean * r);
-    Pair sa = both(0.0f), san = both(0.0f);
+    if (row + step < p.T) {   // the next row's
+      mean = p.stats[row + step];
+      r = p.stats[p.T + row + step];
+    }
+    Pair n[P][4], a[P][4], sa = both(0.0f), san = both(0.0f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int c = g.piece(i);
       if (c >= g.pieces) continue;
-      Pair n2[4], dh[4], w[4];
-      load8(ys + 8 * c, n2);
-      load8(hs + 8 * c, dh);
-      g.mask(c, n2);
-      g.mask(c, dh);
+      Raw<R> y;
+      Raw<__nv_bfloat16> dh;
+      y.load(reinterpret_cast<const R*>(slot) + 8 * c);
+      dh.load(reinterpret_cast<const __nv_bfloat16*>(slot + planes * 8 * sizeof(R)) + 8 * c);
+      if (ODD && !g.whole(c)) {
+        y.only(g.columns(c));
+        dh.only(g.columns(c));
+      }
+      Pair w[4];
+      y.get(n[i]);
+      dh.get(a[i]);
       table_load(shared, planes, 0, c, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        n2[j] = fma2(n2[j], r2, mr);
-        sb[i][j] = add2(sb[i][j], dh[j]);
-        sw[i][j] = fma2(dh[j], n2[j], sw[i][j]);
-        dh[j] = mul2(dh[j], w[j]);
-        sa = add2(sa, dh[j]);
-        san = fma2(dh[j], n2[j], san);
+        n[i][j] = fma2(n[i][j], r2, mr);
+        sb[i][j] = add2(sb[i][j], a[i][j]);
+        sw[i][j] = fma2(a[i][j], n[i][j], sw[i][j]);
+        a[i][j] = mul2(a[i][j], w[j]);
+        sa = add2(sa, a[i][j]);
+        san = fma2(a[i][j], n[i][j], san);
       }
     }
     float ma = sum2(sa), man = sum2(san);
     g.sum_two(ma, man);
-    const Pair rma = both(-r * ma * inv_d), rman = both(-r * man * inv_d);
-    const unsigned long long group0 = DROP ? static_cast<unsigned long long>(row * p.D) >> 3 : 0;
+    float rr, unused;
+    split(r2, rr, unused);
+    const Pair rma = both(-rr * ma * inv_d), rman = both(-rr * man * inv_d);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int c = g.piece(i);
       if (c >= g.pieces) continue;
-      Pair n2[4], dh[4], w[4], s[4];
-      load8(ys + 8 * c, n2);
-      load8(hs + 8 * c, dh);
-      table_load(shared, planes, 0, c, w);
-      if (has_dy) {
-        load8(reinterpret_cast<const R*>(slot + p.in[kDy].off) + 8 * c, s);
+      Pair s[4];
+      if (ALL || p.dy.base) {
+        Raw<R> dy;
+        dy.load(reinterpret_cast<const R*>(slot + planes * 8 * (sizeof(R) + 2)) + 8 * c);
+        dy.get(s);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[j] = both(0.0f);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        n2[j] = fma2(n2[j], r2, mr);
-        s[j] = add2(s[j], fma2(n2[j], rman, fma2(mul2(dh[j], w[j]), r2, rma)));
-        n2[j] = mul2(s[j], both(p.alpha));
+        s[j] = fma2(n[i][j], rman, fma2(a[i][j], r2, add2(s[j], rma)));
+        n[i][j] = mul2(s[j], both(p.alpha));
       }
-      if (p.out0.base) g.template store<R>(p.out0, row, c, n2);
-      if (p.out1.base) {
-        if constexpr (DROP) {
-          drop_scale(key, p.drop, group0 + c, beta, s);
-        } else {
+      if (ALL || p.out0.base) g.template store<R>(p.out0, row, c, n[i]);
+      if (ALL || p.out1.base) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[j] = mul2(s[j], both(beta));
-        }
-        g.template store<__nv_bfloat16>(p.out1, row, c, s);
+        for (int j = 0; j < 4; ++j) s[j] = mul2(s[j], both(beta));
+        if (DROP) g.store(p.out1, row, c, s, keep[i]);
+        else g.template store<__nv_bfloat16>(p.out1, row, c, s);
       }
     }
-    g.send();
-    mean = mean1;
-    r = r1;
+    ring.send();
+    if (DROP) g.draw(key, row + step, keep);   // while the next row is on its way
   }
   cp_wait<0>();
   __syncthreads();   // the rows' memory is free: it takes the groups' sums
-  float4* acc = reinterpret_cast<float4*>(shared + p.table);   // [2 halves][planes], when groups > 1
+  float4* acc = reinterpret_cast<float4*>(shared) + 2 * planes;   // [2 halves][planes], when groups > 1
 #pragma unroll
   for (int arr = 0; arr < 2; ++arr) {
     float* out = p.partial + (static_cast<long long>(arr) * gridDim.x + blockIdx.x) * p.D;
@@ -588,7 +672,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layer_norm_bwd_kernel(const __
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (!RAGGED || g.valid(c, j)) out[8 * c + j - g.off] = v[j];
+              if (!ODD || g.valid(c, j)) out[8 * c + j - g.off] = v[j];
           }
         }
       }
@@ -649,82 +733,80 @@ LnParams common_params(const moe_layer_norm_config* c) {
 }
 
 // Rows whose stride is D's modulo 8 start where the layout's pieces do.
-int phased(long long ld, const LnParams& p) { return (ld - p.D) % 8 == 0 || p.T == 1; }
-
-void add_stream(LnParams* p, int k, const void* base, int64_t ld, int esz) {
-  if (base == nullptr) return;
-  Stream& s = p->in[k];
-  s.base = static_cast<const uint8_t*>(base);
-  s.ld = ld ? ld : p->D;
-  s.end = s.base + ((p->T - 1) * s.ld + p->D) * esz;
-  s.vec = phased(s.ld, *p);
-  s.off = p->slot;
-  p->slot += (p->D + 14) / 8 * 8 * esz;
-}
-Out make_out(const LnParams& p, void* base, int64_t ld) {
+Tensor tensor(const LnParams& p, const void* base, int64_t ld, int esz) {
   const long long l = ld ? ld : p.D;
-  return {base, l, phased(l, p)};
+  return {const_cast<void*>(base), l, (l - p.D) % 8 == 0 || p.T == 1,
+          static_cast<const uint8_t*>(base) + ((p.T - 1) * l + p.D) * esz};
 }
+
+constexpr int kSmem = 216 * 1024;   // the columns' factors and the backward's rows in flight
 
 struct Shape {
   int pieces, ctas, threads;
+  bool odd;
   size_t smem;
 };
 
-// Pieces a thread, warps a row, groups a CTA and rows in flight.
-bool place(LnParams* p, bool fwd, int sms, Shape* s) {
+// Pieces a thread, warps a row, groups a CTA.
+Shape place(LnParams* p, bool fwd, int esz, int sms) {
+  Shape s;
   const bool ragged = p->D % 8 != 0;
-  const int all = (p->D + 7 + (ragged ? 7 : 0)) / 8;   // pieces of a row
-  // the largest number of pieces a thread that wastes no more than a sixth of the lanes
-  const int most = fwd ? 4 : 2;
-  s->pieces = 1;
-  for (int q = 2; q <= most; q *= 2)
-    if ((all + 32 * q - 1) / (32 * q) * (32 * q) * 6 <= all * 7) s->pieces = q;
-  if ((all + 32 * s->pieces - 1) / (32 * s->pieces) > kMaxWarps) s->pieces *= 2;
-  p->warps = (all + 32 * s->pieces - 1) / (32 * s->pieces);
-  p->table = (fwd ? 2 : 1) * all * 32;
-  const int room = kSharedMem - p->table;
-  int groups = std::max(1, std::min({kMaxWarps / p->warps, kMaxGroups, room / (2 * p->slot)}));
-  groups = std::min(groups, (p->T - 1) / sms + 1);
-  p->groups = groups;
-  p->stages = std::max(1, std::min(4, room / (groups * p->slot)));
-  if (p->stages * p->slot > room) return false;
-  s->threads = p->warps * groups * 32;
+  s.odd = ragged;
+  for (const Tensor* t : {&p->x, &p->o, &p->dy, &p->dh, &p->out0, &p->out1}) s.odd = s.odd || (t->base && !t->vec);
+  const int all = (p->D + 7 + (s.odd ? 7 : 0)) / 8;   // pieces of a row, at most
+  // One piece a thread where a warp holds the row, and where an FP32 residual's two would not fit the forward's registers
+  // beside the other group's (16384 x 2048 without dropout 62.7 and 73.8 us; with it 73.3 and 68.6); four for the odd
+  // widths next to the limit, which two do not hold.
+  s.pieces = all <= 32 || (fwd && esz == 4 && !p->drop.rng && all <= kFwdThreads) ? 1 : all <= 1024 ? 2 : 4;
+  p->warps = (all + 32 * s.pieces - 1) / (32 * s.pieces);
+  int most = std::min((fwd ? kFwdThreads : kBwdThreads) / 32 / p->warps, kMaxGroups);
+  const int room = kSmem - all * 32;
+  if (!fwd) {
+    p->slot = all * 8 * (2 * esz + 2);
+    most = std::max(1, std::min(most, room / (2 * p->slot)));   // two rows in flight a group at least, where they fit
+  }
+  p->groups = std::min(most, (p->T - 1) / sms + 1);
+  s.threads = p->warps * p->groups * 32;
   // a group's rows have to be a multiple of 8 apart
-  const int ctas = std::min(sms, p->T);
-  s->ctas = !ragged || p->T <= sms ? ctas : std::max(8, sms / 8 * 8);
-  const size_t rows = std::max<size_t>(static_cast<size_t>(groups) * p->stages * p->slot, groups > 1 ? all * 32ull : 0);
-  s->smem = p->table + rows;
-  return true;
+  s.ctas = !ragged || p->T <= sms ? std::min(sms, p->T) : std::max(8, sms / 8 * 8);
+  // the columns' factors; backward: the rows in flight, whose place the groups' sums take
+  s.smem = 2 * all * 32;
+  if (!fwd) {
+    p->stages = std::max(1, std::min(4, room / (p->groups * p->slot)));
+    s.smem = all * 32 + std::max(all * 32, p->groups * p->stages * p->slot);
+  }
+  return s;
 }
 
 template <typename K>
 cudaError_t launch(K kernel, PerDeviceOnce& once, const Shape& s, const LnParams& p, cudaStream_t stream) {
   const cudaError_t e =
-      once.once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMem); });
+      once.once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
   if (e != cudaSuccess) return e;
   kernel<<<s.ctas, s.threads, s.smem, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <typename R, int P, bool RAGGED, bool DROP>
+template <typename R, int P, bool ODD, bool DROP>
 cudaError_t launch_as(bool fwd, const Shape& s, const LnParams& p, cudaStream_t stream) {
-  static PerDeviceOnce f, b;
-  if (fwd) return launch(layer_norm_fwd_kernel<R, P, RAGGED, DROP>, f, s, p, stream);
-  if constexpr (P <= 2) return launch(layer_norm_bwd_kernel<R, P, RAGGED, DROP>, b, s, p, stream);
-  else return cudaErrorInvalidConfiguration;
+  static PerDeviceOnce f, b, f_all, b_all;
+  if (fwd)
+    return p.o.base && p.out0.base ? launch(layer_norm_fwd_kernel<R, P, ODD, DROP, true>, f_all, s, p, stream)
+                                   : launch(layer_norm_fwd_kernel<R, P, ODD, DROP, false>, f, s, p, stream);
+  return p.dy.base && p.out0.base && p.out1.base ? launch(layer_norm_bwd_kernel<R, P, ODD, DROP, true>, b_all, s, p, stream)
+                                                 : launch(layer_norm_bwd_kernel<R, P, ODD, DROP, false>, b, s, p, stream);
 }
 template <typename R, int P>
 cudaError_t launch_p(bool fwd, const Shape& s, const LnParams& p, cudaStream_t stream) {
-  const bool ragged = p.D % 8 != 0, drop = p.drop.rng != nullptr;
-  if (ragged) return drop ? launch_as<R, P, true, true>(fwd, s, p, stream) : launch_as<R, P, true, false>(fwd, s, p, stream);
+  const bool drop = p.drop.rng != nullptr;
+  if (s.odd) return drop ? launch_as<R, P, true, true>(fwd, s, p, stream) : launch_as<R, P, true, false>(fwd, s, p, stream);
   return drop ? launch_as<R, P, false, true>(fwd, s, p, stream) : launch_as<R, P, false, false>(fwd, s, p, stream);
 }
 template <typename R>
 cudaError_t launch_r(bool fwd, const Shape& s, const LnParams& p, cudaStream_t stream) {
   if (s.pieces == 1) return launch_p<R, 1>(fwd, s, p, stream);
   if (s.pieces == 2) return launch_p<R, 2>(fwd, s, p, stream);
-  return launch_p<R, 4>(fwd, s, p, stream);
+  return p.drop.rng ? launch_as<R, 4, true, true>(fwd, s, p, stream) : launch_as<R, 4, true, false>(fwd, s, p, stream);
 }
 cudaError_t launch_norm(bool fwd, bool f32, const Shape& s, const LnParams& p, cudaStream_t stream) {
   return f32 ? launch_r<float>(fwd, s, p, stream) : launch_r<__nv_bfloat16>(fwd, s, p, stream);
@@ -752,17 +834,17 @@ moe_status moe_layer_norm_forward(const moe_layer_norm_config* cfg, const void* 
                         static_cast<const void*>(h), static_cast<const void*>(stats)})
     if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
   const bool f32 = cfg->residual_type == MOE_TYPE_FP32;
+  const int esz = f32 ? 4 : 2;
   p.weight = weight;
   p.bias = bias;
   p.stats = stats;
-  add_stream(&p, kX, x, cfg->x_stride, f32 ? 4 : 2);
-  add_stream(&p, kO, branch, cfg->branch_stride, 2);
-  p.out0 = make_out(p, y, cfg->y_stride);
-  p.out1 = make_out(p, h, cfg->h_stride);
+  p.x = tensor(p, x, cfg->x_stride, esz);
+  p.o = tensor(p, branch, cfg->branch_stride, 2);
+  p.out0 = tensor(p, y, cfg->y_stride, esz);
+  p.out1 = tensor(p, h, cfg->h_stride, 2);
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  Shape s;
-  if (!place(&p, true, sms, &s)) return MOE_ERR_UNSUPPORTED;
+  const Shape s = place(&p, true, esz, sms);
   return launch_norm(true, f32, s, p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -800,16 +882,16 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, const void*
   if (!workspace || workspace_bytes < need) return MOE_ERR_CAPACITY;
   const int sms = device_sms();
   const bool f32 = cfg->residual_type == MOE_TYPE_FP32;
+  const int esz = f32 ? 4 : 2;
   p.weight = weight;
   p.stats = const_cast<float*>(stats);
   p.partial = static_cast<float*>(workspace);
-  add_stream(&p, kY, y, cfg->x_stride, f32 ? 4 : 2);
-  add_stream(&p, kDh, dh, cfg->h_stride, 2);
-  add_stream(&p, kDy, dy, cfg->y_stride, f32 ? 4 : 2);
-  p.out0 = make_out(p, dx, 0);
-  p.out1 = make_out(p, dbranch, 0);
-  Shape s;
-  if (!place(&p, false, sms, &s)) return MOE_ERR_UNSUPPORTED;
+  p.x = tensor(p, y, cfg->x_stride, esz);
+  p.dh = tensor(p, dh, cfg->h_stride, 2);
+  p.dy = tensor(p, dy, cfg->y_stride, esz);
+  p.out0 = tensor(p, dx, 0, esz);
+  p.out1 = tensor(p, dbranch, 0, 2);
+  const Shape s = place(&p, false, esz, sms);
   if (launch_norm(false, f32, s, p, stream) != cudaSuccess) return MOE_ERR_CUDA;
   if (dweight || dbias) {
     layer_norm_sums_kernel<<<dim3((D + 31) / 32, 2), 256, 0, stream>>>(p.partial, s.ctas, D, dweight, dbias);
