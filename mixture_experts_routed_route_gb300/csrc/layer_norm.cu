@@ -291,6 +291,14 @@ struct Group {
   __device__ __forceinline__ bool vectors(const Tensor& s, long long row) const {
     return !ODD || (s.vec && reinterpret_cast<const uint8_t*>(static_cast<const X*>(s.base) + row * s.ld - off + 8 * pieces) <= s.end);
   }
+  // Piece c, at src, of a row where they may not.
+  template <typename X>
+  __device__ __forceinline__ Raw<X> single(const Tensor& s, const X* src, int c) const {
+    Raw<X> v;
+    if (s.vec && reinterpret_cast<const uint8_t*>(src + 8) <= s.end) v.load(src);
+    else v.gather(src, columns(c));
+    return v;
+  }
   // The thread's pieces of a row; anything past its ends.
   template <typename X>
   __device__ __forceinline__ void load(const Tensor& s, long long row, Raw<X> (&q)[P]) const {
@@ -303,8 +311,7 @@ struct Group {
 #pragma unroll 1
       for (int i = 0; i < P; ++i) {
         if (piece(i) >= pieces) continue;
-        Raw<X> v;
-        v.gather(at + 8 * i * nt, columns(piece(i)));
+        const Raw<X> v = single<X>(s, at + 8 * i * nt, piece(i));
 #pragma unroll
         for (int k = 0; k < P; ++k)
           if (k == i) q[k] = v;
@@ -520,9 +527,7 @@ struct Ring {
         cp_async16(d, src);
         if (sizeof(X) == 4) cp_async16(d + 16, src + 4);
       } else {
-        Raw<X> q;
-        q.gather(src, g.columns(c));
-        *reinterpret_cast<Raw<X>*>(dst + 8 * i * g.nt) = q;
+        *reinterpret_cast<Raw<X>*>(dst + 8 * i * g.nt) = g.template single<X>(s, src, c);
       }
     }
   }

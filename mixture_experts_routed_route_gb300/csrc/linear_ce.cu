@@ -49,6 +49,17 @@ constexpr int kStages = 6;
 constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * 4096 + 256;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr int kGroup = 8;          // row tiles that share the columns' operand before the next ones
+#ifndef SEG
+#define SEG 16
+#endif
+// Stages that the forward's accumulators sum before a new sum begins, in
+// registers: 1024 elements.
+constexpr int kSegment = SEG;
+// Few tokens: at most 64, 32 a group of four epilogue warps.
+constexpr int kFew = 64;
+constexpr int kFewSteps = 4;       // contraction steps of 64 a stage, which is also a segment
+constexpr int kFewSmem = 230 * 1000;
+static_assert(kFewSmem <= 232448, "shared memory per CTA");
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 constexpr float kLowest = -1.0e30f;
 
@@ -149,6 +160,70 @@ __device__ __forceinline__ CeTile ce_tile(const CeWork<KIND>& w, int tile) {
 // One 16-byte piece of a warp's 32 rows x 128 bytes, in the 128-byte swizzle.
 __device__ __forceinline__ void stage16(uint8_t* ws, int lane, int piece, uint4 v) {
   *reinterpret_cast<uint4*>(ws + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long pair_of(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Element i of 32 registers.
+__device__ __forceinline__ float pick(const float (&x)[32], int i) {
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = (i & 16) ? x[16 + j] : x[j];
+#pragma unroll
+  for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+    for (int j = 0; j < w; ++j) v[j] = (i & w) ? v[w + j] : v[j];
+  return v[0];
+}
+
+// 32 logits of a row, columns c .. c + 31 of n, join its maximum and sum of exponentials.
+__device__ __forceinline__ void join_chunk(float (&x)[32], int c, int n, int row, int target, const CeParams& p, float& top,
+                                           float& sum) {
+  if (c + 32 > n) {   // past the vocabulary
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c + j >= n) x[j] = -INFINITY;
+  }
+  if (static_cast<unsigned>(target - c) < 32u) p.hit[row] = pick(x, target - c);
+  float m = x[0];
+#pragma unroll
+  for (int j = 1; j < 31; j += 2) m = max3(m, x[j], x[j + 1]);
+  m = fmaxf(top, fmaxf(m, x[31]) * p.k);
+  sum *= exp2_fast(top - m);
+  top = m;
+  unsigned long long s = pair_of(0.0f, 0.0f);
+  const unsigned long long kk = pair_of(p.k, p.k), mm = pair_of(-m, -m);
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    float a, b;
+    split(fma2(pair_of(x[j], x[j + 1]), kk, mm), a, b);
+    s = add2(s, pair_of(exp2_fast(a), exp2_fast(b)));
+  }
+  float a, b;
+  split(s, a, b);
+  sum += a + b;
 }
 
 template <int KIND>
@@ -254,11 +329,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int tile = cid; ok && tile < w.total; tile += ncl, ++tc) {
         const CeTile t = ce_tile<KIND>(w, tile);
         const uint32_t idesc = idesc0 | ((static_cast<uint32_t>(t.n) >> 3) << 17);
-        const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+        uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem + acc * 256;
+        uint32_t d_tmem = tmem + acc * 256;
+        int first = 0;
         for (int ks = 0; ks < t.ks; ++ks, ++it) {
+          if (KIND == kLse && ks - first == kSegment) {   // the next segment, in the other accumulator
+            if (lane == 0) tc_commit_pair_mc(&tfull[acc], 3);
+            __syncwarp();
+            first = ks;
+            ++tc;
+            acc = tc & 1, aph = (tc >> 1) & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            d_tmem = tmem + acc * 256;
+          }
           const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
           if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&full[slot], ph, abort_flag, p.err))) {
             ok = false;
@@ -271,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < kBk / 16; ++j) {
               const uint64_t ad = kAMn ? sdesc_mn_bf16(sa + j * 2048) : sdesc_k_sw128(sa + j * 32);
               const uint64_t bd = kBMn ? sdesc_mn_bf16(sb + j * 2048) : sdesc_k_sw128(sb + j * 32);
-              mma_bf16_pair(d_tmem, ad, bd, idesc, (ks | j) ? 1u : 0u);
+              mma_bf16_pair(d_tmem, ad, bd, idesc, ((ks - first) | j) ? 1u : 0u);
             }
             tc_commit_pair_mc(&empty[slot], 3);
           }
@@ -293,14 +382,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* ws = turn + (warp - 2) * 4096;
     const uint32_t tempty0 = cluster_addr(tempty, 0);
     uint32_t tc = 0;
-    for (int tile = cid; tile < w.total; tile += ncl, ++tc) {
+    for (int tile = cid; tile < w.total; tile += ncl) {
       const CeTile t = ce_tile<KIND>(w, tile);
-      const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
       const int row = t.row0 + 128 * rank + 32 * q + lane;     // this thread's
       const int row_w = row - lane;
       const int cols = t.n / 2, c0 = t.col0 + h * cols;        // this warp's columns
       int target = -1;
-      float top = kLowest, sum = 0.0f, hit = 0.0f;
       float lse2 = 0.0f;
       float2 coef = make_float2(0.0f, 0.0f);
       if constexpr (KIND == kLse || KIND == kGrad) {
@@ -310,102 +397,143 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           coef = p.coef[row];
         }
       }
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
-      tc_fence_after();
-      const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
+      if constexpr (KIND == kLse) {
+        float top = kLowest, sum = 0.0f;
+        bool ok = true;
+        if (t.ks <= kSegment) {
+          const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+          ++tc;
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
+          tc_fence_after();
+          const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int ci = 0; ci < cols / 32; ++ci) {
-        uint32_t v[32];
-        tmem_ld32(tbase + 32 * ci, v);
-        tmem_ld_wait();
-        if (ci == cols / 32 - 1) {   // every column has been read: the accumulator is free
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
-        }
-        const int c = c0 + 32 * ci;
-        if constexpr (KIND == kLse) {
-          if (c + 32 > w.n) {   // past the vocabulary
+          for (int ci = 0; ci < cols / 32; ++ci) {
+            uint32_t v[32];
+            tmem_ld32(tbase + 32 * ci, v);
+            tmem_ld_wait();
+            if (ci == cols / 32 - 1) {   // every column has been read: the accumulator is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
+            }
+            float x[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j >= w.n) v[j] = __float_as_uint(-INFINITY);
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+            join_chunk(x, c0 + 32 * ci, w.n, row, target, p, top, sum);
           }
-          if (static_cast<unsigned>(target - c) < 32u) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (target - c == j) hit = __uint_as_float(v[j]);
-            p.hit[row] = hit;
-          }
-          float m = __uint_as_float(v[0]);
-#pragma unroll
-          for (int j = 1; j < 32; ++j) m = fmaxf(m, __uint_as_float(v[j]));
-          m = fmaxf(top, m * p.k);
-          sum *= exp2_fast(top - m);
-          top = m;
-          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast(fmaf(__uint_as_float(v[j]), p.k, -m));
-          sum += (s[0] + s[1]) + (s[2] + s[3]);
         } else {
-          constexpr int kHalves = KIND == kDh ? 1 : 2;   // chunks of 32 columns in 128 bytes
-          float x[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
-          if (KIND != kGrad && t.ks == 0) {   // an empty contraction
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = 0.0f;
-          }
-          if constexpr (KIND == kGrad) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = coef.x * exp2_fast(fmaf(x[j], p.k, -lse2));
-            if (static_cast<unsigned>(target - c) < 32u) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (target - c == j) x[j] -= coef.y;
+          // this thread's 128 columns: sums of the segments
+          float x[4][32];
+          for (int ks = 0; ks < t.ks; ks += kSegment, ++tc) {
+            const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) {
+              ok = false;
+              break;
             }
-            if (c + 32 > w.n) {   // past the piece, whose end is the vocabulary's
+            tc_fence_after();
+            const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
+            const bool last = ks + kSegment >= t.ks;
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c + j >= w.n) x[j] = 0.0f;
-            }
-          }
-          if (ci % kHalves == 0) {   // the stores that read the buffer before are done
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-          }
-          if constexpr (KIND == kDh) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              stage16(ws, lane, j, make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
-                                              __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              stage16(ws, lane, 4 * (ci % kHalves) + j,
-                      make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
-                                 pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7])));
-          }
-          if (ci % kHalves == kHalves - 1) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              const int cs = c - 32 * (kHalves - 1);
-              if constexpr (KIND == kGrad) {
-                tma_store_2d(&tmC, ws, cs, row_w);
-              } else if constexpr (KIND == kDh) {
-                if (cs < p.D) {
-                  if (p.first) tma_store_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
-                  else tma_reduce_add_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
-                }
-              } else {
-                if (cs < p.D && p.v0 + row_w < p.V) tma_store_2d(&tmC, ws, cs, p.v0 + row_w);
+            for (int ci = 0; ci < 4; ++ci) {
+              if (ci >= 2 && cols == 64) continue;
+              uint32_t v[32];
+              tmem_ld32(tbase + 32 * ci, v);
+              tmem_ld_wait();
+              if (ci == (cols == 64 ? 1 : 3)) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
               }
-              bulk_commit();
+              if (ks == 0) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[ci][j] = __uint_as_float(v[j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[ci][j] += __uint_as_float(v[j]);
+              }
+              if (last) join_chunk(x[ci], c0 + 32 * ci, w.n, row, target, p, top, sum);
+            }
+          }
+        }
+        if (!ok) break;
+        p.part[static_cast<long long>(2 * (t.col0 / kTile) + h) * p.rows_cap + row] = make_float2(top, sum);
+      } else {
+        const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+        ++tc;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
+        tc_fence_after();
+        const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+        for (int ci = 0; ci < cols / 32; ++ci) {
+          uint32_t v[32];
+          tmem_ld32(tbase + 32 * ci, v);
+          tmem_ld_wait();
+          if (ci == cols / 32 - 1) {   // every column has been read: the accumulator is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
+          }
+          const int c = c0 + 32 * ci;
+          {
+            constexpr int kHalves = KIND == kDh ? 1 : 2;   // chunks of 32 columns in 128 bytes
+            float x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+            if (KIND != kGrad && t.ks == 0) {   // an empty contraction
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+            }
+            if constexpr (KIND == kGrad) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = coef.x * exp2_fast(fmaf(x[j], p.k, -lse2));
+              if (static_cast<unsigned>(target - c) < 32u) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (target - c == j) x[j] -= coef.y;
+              }
+              if (c + 32 > w.n) {   // past the piece, whose end is the vocabulary's
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (c + j >= w.n) x[j] = 0.0f;
+              }
+            }
+            if (ci % kHalves == 0) {   // the stores that read the buffer before are done
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+            }
+            if constexpr (KIND == kDh) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                stage16(ws, lane, j, make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                                                __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                stage16(ws, lane, 4 * (ci % kHalves) + j,
+                        make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
+                                   pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7])));
+            }
+            if (ci % kHalves == kHalves - 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int cs = c - 32 * (kHalves - 1);
+                if constexpr (KIND == kGrad) {
+                  tma_store_2d(&tmC, ws, cs, row_w);
+                } else if constexpr (KIND == kDh) {
+                  if (cs < p.D) {
+                    if (p.first) tma_store_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
+                    else tma_reduce_add_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
+                  }
+                } else {
+                  if (cs < p.D && p.v0 + row_w < p.V) tma_store_2d(&tmC, ws, cs, p.v0 + row_w);
+                }
+                bulk_commit();
+              }
             }
           }
         }
       }
-      if constexpr (KIND == kLse) p.part[static_cast<long long>(2 * (t.col0 / kTile) + h) * p.rows_cap + row] = make_float2(top, sum);
     }
     if (KIND != kLse && lane == 0) bulk_wait<0>();
     __syncwarp();
@@ -415,6 +543,202 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   cluster_sync();
   if (warp == 1) tmem_dealloc_cg<2>(tmem, 512);
+}
+
+// Forward of at most N tokens: the vocabulary's rows are the products' rows, so
+// that the tensor cores take N columns instead of 256 and what is left is the
+// weight's one way from HBM.  A stage takes 512 bytes of a row at a time: with
+// 128, the rows' neighbouring lines are asked for too far apart for HBM's pages (1 x 2048 x
+// 131072 98.5 us, with 256 86.4, with 512 86.3).  Each CTA has a run of 32-row units, worked through
+// in tiles of 128 rows (the last one shorter, and no row loaded twice); a
+// thread keeps, for its place in the tiles, each token's running maximum and
+// sum of exponentials, which lanes exchange once at the end.
+template <int N>
+__global__ void __launch_bounds__(64 + 4 * N, 1)
+    ce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, const CeParams p) {
+  constexpr int kStep = N * kBk * 2, kBytes = kFewSteps * (kOperand + kStep);
+  constexpr int kFewStages = (kFewSmem - 1024 - 512) / kBytes;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewStages * kBytes);
+  uint64_t* empty = full + kFewStages;
+  uint64_t* tfull = empty + kFewStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ int targets[N];
+  __shared__ float2 red[4][N];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // this CTA's units of 32 rows
+  const long long all = (p.V + 31) / 32;
+  const int u0 = static_cast<int>(all * blockIdx.x / gridDim.x);
+  const int units = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x) - u0;
+  const int tiles = (units + 3) / 4, steps = (p.D + kFewSteps * kBk - 1) / (kFewSteps * kBk);
+  // the weight's rows of stage ks of a tile into slot `slot`
+  auto load_w = [&](int tile, int ks, uint32_t slot) {
+    const int n = min(4, units - 4 * tile);
+    uint8_t* sa = smem + slot * kBytes;
+    mbar_arrive_expect_tx(&full[slot], kFewSteps * (n * (32 * kBk * 2) + kStep));
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int j = 0; j < kFewSteps; ++j)
+        tma_load_2d(sa + j * kOperand + i * (32 * kBk * 2), &tmW, &full[slot], (ks * kFewSteps + j) * kBk,
+                    (u0 + 4 * tile + i) * 32);
+  };
+  const int ahead = min(tiles * steps, kFewStages);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kFewStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], N / 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    // no kernel that may still run writes the weight: its first stages go out before the packed rows are waited for
+    for (int i = 0; i < ahead; ++i) load_w(i / steps, i % steps, i);
+    tma_prefetch(&tmH);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 2 * N);
+    tmem_relinquish();
+  }
+  after_previous();
+  const int count = min(*p.count, N);
+  if (threadIdx.x < N) targets[threadIdx.x] = p.target[threadIdx.x];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = 0; ok && tile < tiles; ++tile) {
+      for (int ks = 0; ks < steps; ++ks, ++it) {
+        const uint32_t slot = it % kFewStages, ph = (it / kFewStages) & 1;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[slot], ph ^ 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          if (it >= static_cast<uint32_t>(ahead)) load_w(tile, ks, slot);
+#pragma unroll
+          for (int j = 0; j < kFewSteps; ++j)
+            tma_load_2d(smem + slot * kBytes + kFewSteps * kOperand + j * kStep, &tmH, &full[slot], (ks * kFewSteps + j) * kBk, 0);
+        }
+        __syncwarp();
+      }
+    }
+    // no load may still be landing when the CTA exits
+    if (lane == 0) {
+      const uint32_t pend = it < static_cast<uint32_t>(kFewStages) ? it : static_cast<uint32_t>(kFewStages);
+      for (uint32_t j = 0; j < pend; ++j) {
+        const uint32_t i2 = it - 1 - j;
+        drain_wait(&full[i2 % kFewStages], (i2 / kFewStages) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_bf16(N, 128);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = 0; ok && tile < tiles; ++tile) {
+      for (int ks = 0; ks < steps; ++ks, ++it) {
+        const uint32_t acc = it & 1, aph = (it >> 1) & 1, slot = it % kFewStages, ph = (it / kFewStages) & 1;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], aph ^ 1, abort_flag, p.err) &&
+                                         mbar_wait(&full[slot], ph, abort_flag, p.err));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t sa = smem_u32(smem + slot * kBytes), sb = sa + kFewSteps * kOperand;
+#pragma unroll
+          for (int j = 0; j < kFewSteps * kBk / 16; ++j)
+            mma_bf16(tmem + acc * N, sdesc_k_sw128(sa + (j >> 2) * kOperand + (j & 3) * 32),
+                     sdesc_k_sw128(sb + (j >> 2) * kStep + (j & 3) * 32), idesc, j ? 1u : 0u);
+          tc_commit(&empty[slot]);
+          tc_commit(&tfull[acc]);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0 && it > 0) {
+      tc_commit(drain);
+      drain_wait(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, j0 = 32 * ((warp - 2) >> 2);   // lane quadrant, tokens
+    float top[32], sum[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      top[j] = kLowest;
+      sum[j] = 0.0f;
+    }
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = 0; ok && tile < tiles; ++tile) {
+      const int unit = 4 * tile + q, row = (u0 + unit) * 32 + lane;
+      float x[32];
+      for (int ks = 0; ks < steps; ++ks, ++it) {
+        const uint32_t acc = it & 1, aph = (it >> 1) & 1;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], aph, abort_flag, p.err));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[32];
+        tmem_ld32(tmem + acc * N + j0 + (static_cast<uint32_t>(q * 32) << 16), v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = ks == 0 ? __uint_as_float(v[j]) : x[j] + __uint_as_float(v[j]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[acc]);
+      }
+      if (!ok || unit >= units || row >= p.V) continue;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (j0 + j >= count) break;
+        if (targets[j0 + j] == row) p.hit[j0 + j] = x[j];
+        const float m = fmaxf(top[j], x[j] * p.k);
+        sum[j] = fmaf(sum[j], exp2_fast(top[j] - m), exp2_fast(fmaf(x[j], p.k, -m)));
+        top[j] = m;
+      }
+    }
+    // over the warp's rows, and the warps'
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j0 + j >= count) break;
+      float m = top[j];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      float t = sum[j] * exp2_fast(top[j] - m);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      if (lane == 0) red[q][j0 + j] = make_float2(m, t);
+    }
+    named_bar_sync(1, 4 * N);
+    const int j = threadIdx.x - 64;
+    if (j < count) {
+      float m = red[0][j].x, t = red[0][j].y;
+#pragma unroll
+      for (int i = 1; i < 4; ++i) {
+        const float2 r = red[i][j];
+        const float n = fmaxf(m, r.x);
+        t = t * exp2_fast(m - n) + r.y * exp2_fast(r.x - n);
+        m = n;
+      }
+      p.part[static_cast<long long>(blockIdx.x) * p.rows_cap + j] = make_float2(m, t);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 2 * N);
 }
 
 // ----------------------------------------------------- rows that count
@@ -443,30 +767,31 @@ struct RowParams {
   float2* coef;          // [rows_cap]
 };
 
-// The packed rows' tokens in order, one CTA: 1024 tokens a turn.  Tokens that
-// do not count get their results here: loss 0 (NaN for a target outside the
-// vocabulary), lse 0.
-__global__ void __launch_bounds__(1024) ce_rows_kernel(const __grid_constant__ RowParams p) {
-  __shared__ int warp_count[2][32];
+// A turn of 1024 tokens from t0, of which `base` rows that count come before:
+// the packed row of this thread's token (-1: it does not count) and the number
+// of rows after the turn.  counts: the warps', a turn's own.  write: put
+// down what the products need of the row; tokens that do not count get their results: loss 0
+// (NaN for a target outside the vocabulary), lse 0.
+__device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, int* counts, bool write) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int base = 0;
-  for (int t0 = 0, turn = 0; t0 < p.T; t0 += 1024, turn ^= 1) {
-    const int t = t0 + threadIdx.x;
-    long long target = p.ignore;
-    if (t < p.T) target = p.wide ? static_cast<const long long*>(p.targets)[t] : static_cast<const int*>(p.targets)[t];
-    const bool on = target != p.ignore && target >= 0 && target < p.V;
-    const unsigned vote = __ballot_sync(0xFFFFFFFFu, on);
-    if (lane == 0) warp_count[turn][warp] = __popc(vote);
-    __syncthreads();
-    const int mine = warp_count[turn][lane];
-    int before = 0, all = 0;
+  const int t = t0 + threadIdx.x;
+  long long target = p.ignore;
+  if (t < p.T) target = p.wide ? static_cast<const long long*>(p.targets)[t] : static_cast<const int*>(p.targets)[t];
+  const bool on = target != p.ignore && target >= 0 && target < p.V;
+  const unsigned vote = __ballot_sync(0xFFFFFFFFu, on);
+  if (lane == 0) counts[warp] = __popc(vote);
+  __syncthreads();
+  const int mine = counts[lane];
+  int before = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int c = __shfl_sync(0xFFFFFFFFu, mine, i);
-      if (i < warp) before += c;
-      all += c;
-    }
-    const int at = base + before + __popc(vote & ((1u << lane) - 1));
+  for (int i = 0; i < 32; ++i) {
+    const int c = __shfl_sync(0xFFFFFFFFu, mine, i);
+    if (i < warp) before += c;
+    all += c;
+  }
+  const int at = base + before + __popc(vote & ((1u << lane) - 1));
+  base += all;
+  if (write) {
     if (on) {
       p.list[at] = t;
       p.target[at] = static_cast<int>(target);
@@ -480,11 +805,15 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const __grid_constant__ R
       p.lse[t] = 0.0f;
     }
     if (t < p.T && p.inv) p.inv[t] = on ? at : -1;
-    base += all;
   }
-  if (threadIdx.x == 0) *p.count = base;
-  const int end = (base + kTile - 1) / kTile * kTile;
-  for (int i = base + threadIdx.x; i < end; i += 1024) {
+  return on ? at : -1;
+}
+
+// After the last turn: the number of rows, and what stands for none up to a multiple of 256.
+__device__ __forceinline__ void row_end(const RowParams& p, int count) {
+  if (threadIdx.x == 0) *p.count = count;
+  const int end = (count + kTile - 1) / kTile * kTile;
+  for (int i = count + threadIdx.x; i < end; i += 1024) {
     p.list[i] = -1;
     p.target[i] = -1;
     if (p.coef) {
@@ -494,30 +823,51 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const __grid_constant__ R
   }
 }
 
-// Packed copy of h, one row a block, zeros from the last row to a multiple of 256.
+// Row i of the packed copy of h, token t's (-1: zeros).
+__device__ __forceinline__ void pack_row(const RowParams& p, int i, int t) {
+  uint4* out = reinterpret_cast<uint4*>(p.packed + static_cast<long long>(i) * p.D);
+  const __nv_bfloat16* in = p.h + static_cast<long long>(max(t, 0)) * p.ldh;
+  for (int c = threadIdx.x; c < p.D / 8; c += blockDim.x) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (t >= 0) {
+      if (p.ldh % 8 == 0) {
+        v = reinterpret_cast<const uint4*>(in)[c];
+      } else {
+        const unsigned short* s = reinterpret_cast<const unsigned short*>(in) + 8 * c;
+        v.x = s[0] | static_cast<uint32_t>(s[1]) << 16;
+        v.y = s[2] | static_cast<uint32_t>(s[3]) << 16;
+        v.z = s[4] | static_cast<uint32_t>(s[5]) << 16;
+        v.w = s[6] | static_cast<uint32_t>(s[7]) << 16;
+      }
+    }
+    out[c] = v;
+  }
+}
+
+// Up to 1024 tokens: every block finds the rows that count, the first writes them down, and all pack them.
+__global__ void __launch_bounds__(1024) ce_rows_once_kernel(const __grid_constant__ RowParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int counts[32], list[1024];
+  int count = 0;
+  const int at = row_turn(p, 0, count, counts, blockIdx.x == 0);
+  if (at >= 0) list[at] = threadIdx.x;
+  if (blockIdx.x == 0) row_end(p, count);
+  __syncthreads();
+  const int end = (count + kTile - 1) / kTile * kTile;
+  for (int i = blockIdx.x; i < end; i += gridDim.x) pack_row(p, i, i < count ? list[i] : -1);
+}
+
+// More tokens: one block finds the rows, 1024 tokens a turn, and others pack them.
+__global__ void __launch_bounds__(1024) ce_rows_kernel(const __grid_constant__ RowParams p) {
+  __shared__ int counts[2][32];
+  int base = 0;
+  for (int t0 = 0, turn = 0; t0 < p.T; t0 += 1024, turn ^= 1) row_turn(p, t0, base, counts[turn], true);
+  row_end(p, base);
+}
 __global__ void __launch_bounds__(256) ce_pack_kernel(const __grid_constant__ RowParams p) {
   after_previous();
   const int count = *p.count, end = (count + kTile - 1) / kTile * kTile;
-  for (int i = blockIdx.x; i < end; i += gridDim.x) {
-    const int t = p.list[i];
-    uint4* out = reinterpret_cast<uint4*>(p.packed + static_cast<long long>(i) * p.D);
-    const __nv_bfloat16* in = p.h + static_cast<long long>(t) * p.ldh;
-    for (int c = threadIdx.x; c < p.D / 8; c += 256) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (t >= 0) {
-        if (p.ldh % 8 == 0) {
-          v = reinterpret_cast<const uint4*>(in)[c];
-        } else {
-          const unsigned short* s = reinterpret_cast<const unsigned short*>(in) + 8 * c;
-          v.x = s[0] | static_cast<uint32_t>(s[1]) << 16;
-          v.y = s[2] | static_cast<uint32_t>(s[3]) << 16;
-          v.z = s[4] | static_cast<uint32_t>(s[5]) << 16;
-          v.w = s[6] | static_cast<uint32_t>(s[7]) << 16;
-        }
-      }
-      out[c] = v;
-    }
-  }
+  for (int i = blockIdx.x; i < end; i += gridDim.x) pack_row(p, i, p.list[i]);
 }
 
 // loss and lse of the packed rows from the tiles' maxima and sums: 32 rows a
@@ -532,50 +882,64 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* part, const
   if (static_cast<int>(blockIdx.x) * 32 >= n) return;
   float top = kLowest, sum = 0.0f;
   if (row < n) {
-#pragma unroll 4
-    for (int i = y; i < parts; i += 32) {
-      const float2 q = part[static_cast<long long>(i) * rows_cap + row];
-      const float m = fmaxf(top, q.x);
-      sum = sum * exp2_fast(top - m) + q.y * exp2_fast(q.x - m);
+    for (int i0 = y; i0 < parts; i0 += 32 * 8) {
+      float2 q[8];   // asked for together
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        q[j] = i0 + 32 * j < parts ? part[static_cast<long long>(i0 + 32 * j) * rows_cap + row] : make_float2(kLowest, 0.0f);
+      float m = top;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, q[j].x);
+      sum *= exp2_fast(top - m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(q[j].y, exp2_fast(q[j].x - m), sum);
       top = m;
     }
   }
   s[y][x] = make_float2(top, sum);
   __syncthreads();
-  if (y == 0 && row < n) {
-    for (int i = 1; i < 32; ++i) {
-      const float2 q = s[i][x];
-      const float m = fmaxf(top, q.x);
-      sum = sum * exp2_fast(top - m) + q.y * exp2_fast(q.x - m);
-      top = m;
-    }
+  // warp y joins row y's 32 sums
+  const int r = blockIdx.x * 32 + y;
+  if (r >= n) return;
+  const float2 v = s[x][y];
+  top = v.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  sum = v.y * exp2_fast(v.x - top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (x == 0) {
     // in base 2 until the end: the loss is rounded relative to itself
-    const float l2 = top + log2f(sum), l = l2 * kLn2;
-    const int t = list[row];
+    const float ls = log2f(sum), l = (top + ls) * kLn2;
+    const int t = list[r];
     lse[t] = l;
-    loss[t] = fmaf(z * l, l, (fmaf(-hit[row], k, top) + log2f(sum)) * kLn2);
+    loss[t] = fmaf(z * l, l, (fmaf(-hit[r], k, top) + ls) * kLn2);
   }
 }
 
-// dh: the sum of the splits' FP32 rows, rounded; zeros for tokens that do not count.
+// dh: the sum of the splits' FP32 rows, rounded; zeros for tokens that do not
+// count.  A thread takes four columns and asks for four splits at a time.
 __global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, int splits, int rows_cap, const int* inv, int T,
                                                     int D, __nv_bfloat16* dh) {
   after_previous();
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+  const int per = D / 4;
+  const long long all = static_cast<long long>(T) * per, plane = static_cast<long long>(rows_cap) * D;
+  for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < all; k += static_cast<long long>(gridDim.x) * 256) {
+    const int t = static_cast<int>(k / per), c = static_cast<int>(k - static_cast<long long>(t) * per) * 4;
     const int i = inv[t];
-    for (int c = threadIdx.x; c < D / 8; c += 256) {
-      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-      if (i >= 0) {
-        for (int s = 0; s < splits; ++s) {
-          const float4* q = reinterpret_cast<const float4*>(part + (static_cast<long long>(s) * rows_cap + i) * D) + 2 * c;
-          const float4 u = q[0], v = q[1];
-          a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
-          b.x += v.x, b.y += v.y, b.z += v.z, b.w += v.w;
-        }
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i >= 0) {
+      const float* q = part + static_cast<long long>(i) * D + c;
+      for (int s = 0; s < splits; s += 4) {
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] = s + j < splits ? *reinterpret_cast<const float4*>(q + (s + j) * plane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a.x += v[j].x, a.y += v[j].y, a.z += v[j].z, a.w += v[j].w;
       }
-      reinterpret_cast<uint4*>(dh + static_cast<long long>(t) * D)[c] =
-          make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
     }
+    *reinterpret_cast<uint2*>(dh + static_cast<long long>(t) * D + c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   }
 }
 
@@ -614,6 +978,10 @@ int dh_splits(int T, int D, int pairs) {
   return best;
 }
 
+// Tokens that the vocabulary-wise forward takes: the weight's bytes bound both,
+// and it moves no others (1 x 2048 x 131072: 87 and 103 us).
+bool few(int T) { return T <= kFew; }
+
 struct Layout {
   int rows_cap, col_tiles, splits;
   int64_t piece;          // vocabulary entries a piece, a multiple of 256
@@ -644,7 +1012,7 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
     l.g = take(&at, rows * 2 * l.piece);
   } else {
     l.hit = take(&at, rows * 4);
-    l.part = take(&at, rows * 8 * 2 * l.col_tiles);
+    l.part = take(&at, rows * 8 * std::max(2 * l.col_tiles, few(c->tokens) ? sms : 0));
   }
   l.bytes = at;
   return l;
@@ -673,7 +1041,23 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtens
   return launch_dependent(reinterpret_cast<const void*>(ce_gemm_kernel<KIND>), dim3(grid), kThreads, kSmem, stream, args);
 }
 
+template <int N>
+cudaError_t launch_few(const void* weight, const void* packed, const CeParams& p, int sms, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  cudaError_t e =
+      once.once([&] { return cudaFuncSetAttribute(ce_few_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem); });
+  if (e != cudaSuccess) return e;
+  CUtensorMap w, h;
+  if (!map_2d(&w, weight, p.V, p.D, 32, false) || !map_2d(&h, packed, p.rows_cap, p.D, N, false)) return cudaErrorInvalidValue;
+  void* args[] = {&w, &h, const_cast<CeParams*>(&p)};
+  return launch_dependent(reinterpret_cast<const void*>(ce_few_kernel<N>), dim3(sms), 64 + 4 * N, kFewSmem, stream, args);
+}
+
 cudaError_t launch_rows(const RowParams& p, int sms, cudaStream_t stream) {
+  if (p.T <= 1024) {
+    ce_rows_once_kernel<<<std::min(p.rows_cap, sms), 1024, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
   ce_rows_kernel<<<1, 1024, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -751,14 +1135,21 @@ moe_status moe_linear_ce_forward(const moe_linear_ce_config* cfg, const void* h,
   r.lse = lse;
   p.part = at<float2>(workspace, l.part);
   p.hit = at<float>(workspace, l.hit);
-  CUtensorMap a, b;
-  if (!map_2d(&a, r.packed, l.rows_cap, cfg->d_model, 128, false) ||
-      !map_2d(&b, weight, cfg->vocab, cfg->d_model, 128, false))
-    return MOE_ERR_CUDA;
   if (launch_rows(r, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
-  if (launch_gemm<kLse>(a, b, a, p, sms / 2, static_cast<long long>(l.rows_cap / kTile) * l.col_tiles, stream) != cudaSuccess)
-    return MOE_ERR_CUDA;
   int parts = 2 * l.col_tiles;
+  if (few(cfg->tokens)) {
+    parts = sms;
+    if ((cfg->tokens <= 32 ? launch_few<32>(weight, r.packed, p, sms, stream)
+                           : launch_few<64>(weight, r.packed, p, sms, stream)) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  } else {
+    CUtensorMap a, b;
+    if (!map_2d(&a, r.packed, l.rows_cap, cfg->d_model, 128, false) ||
+        !map_2d(&b, weight, cfg->vocab, cfg->d_model, 128, false) ||
+        launch_gemm<kLse>(a, b, a, p, sms / 2, static_cast<long long>(l.rows_cap / kTile) * l.col_tiles, stream) !=
+            cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
   float k = p.k, z = cfg->z_weight;
   const float2* part = p.part;
   const float* hit = p.hit;
@@ -835,8 +1226,8 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
     const int* inv = r.inv;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dh);
     void* args[] = {&in, &splits, &cap, &inv, &t, &d, &out};
-    if (launch_dependent(reinterpret_cast<const void*>(ce_dh_kernel), dim3(std::min(T, 8 * sms)), 256, 0, stream, args) !=
-        cudaSuccess)
+    if (launch_dependent(reinterpret_cast<const void*>(ce_dh_kernel), dim3(static_cast<unsigned>(std::min<long long>((static_cast<long long>(T) * (D / 4) + 255) / 256, 16 * sms))), 256, 0,
+                         stream, args) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
   return MOE_OK;
