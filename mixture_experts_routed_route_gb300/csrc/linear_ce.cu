@@ -26,9 +26,20 @@
 // Exponentials are in base 2 with one fused product, exp2(l k - m), k = scale
 // log2 e: the rounding is relative to the small difference.
 //
+// What bounds it (one GB300): large products the tensor cores under the power cap: forward
+// 2048 x 7168 x 131072 2.29 to 2.37 ms (1.65 PFLOP/s), 4096 x 2048 x 131072 1.38 to 1.45 ms; backward 4096 x 2048 x
+// 131072 3.8 to 4.2 ms, 2.1 to 2.3 PFLOP/s with the logits formed again (8 T V D; what it cannot do without
+// is 6 T V D), 1531 x 1408 x 50021 with 30 % ignored 360 us.  One token: the weight's
+// bytes, 87 us (6.2 TB/s; floor 79), backward 312 us (three times them; floor 237).  Small problems: the
+// chain of launches, about 6 us each beside their work (512 x 256 x 32768: forward 20 us, backward 49 us).
+// Larger pieces of the vocabulary are faster (launches, dh's sums): 4096 x 2048 x 131072 in pieces of
+// 16384 entries 4.18 ms, 32768 3.94, 65536 3.79; pieces that stay in L2 are not.
+// Tried without gain: sixteen epilogue warps in the backward's products, L2-sized pieces,
+// rotated starts of the contraction.
+//
 // Warp roles: warp 0 TMA producer, warp 1 TMEM allocation and (rank 0) MMA
-// issue for the pair, warps 2 .. 9 epilogue (lane quadrant w % 4, half of the
-// tile's columns each).  A thread has its own row of the accumulator, so the
+// issue for the pair, the other 8 or 16 epilogue (lane quadrant w % 4, a part of
+// the tile's columns each).  A thread has its own row of the accumulator, so the
 // softmax needs no exchange between threads.
 #include <algorithm>
 
@@ -39,22 +50,29 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kEpiWarps = 8;
 constexpr int kTile = 256;         // rows and columns of a pair's tile
 constexpr int kBk = 64;            // contraction elements a stage: 128 bytes
 constexpr int kOperand = 128 * kBk * 2;
 constexpr int kStage = 2 * kOperand;
-constexpr int kStages = 6;
-constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * 4096 + 256;
-static_assert(kSmem <= 232448, "shared memory per CTA");
+enum CeKind { kLse, kGrad, kDh, kDw };
+
+// E epilogue warps, 4 KB each to turn their values around (the forward: the
+// warps' maxima and sums of a row).
+template <int KIND, int E>
+struct CeCfg {
+  static constexpr int kThreads = 64 + 32 * E;
+  static constexpr int kStages = 6;
+  static constexpr int kTurn = KIND == kLse ? 16384 : E * 4096;
+  static constexpr int kSmem = 1024 + kStages * kStage + kTurn + 256;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
 constexpr int kGroup = 8;          // row tiles that share the columns' operand before the next ones
-#ifndef SEG
-#define SEG 16
-#endif
 // Stages that the forward's accumulators sum before a new sum begins, in
-// registers: 1024 elements.
-constexpr int kSegment = SEG;
+// registers: 1024 elements.  The tensor cores cut off, not round, at each of
+// their additions, so a logit of 7168 elements is low by 7.5e-6 of itself in one sum, by
+// 1.0e-6 in seven (8 stages a sum: 0.5e-6, but reading the accumulators twice as often costs
+// 4 % of the product; one sum: 3 % faster).
+constexpr int kSegment = 16;
 // Few tokens: at most 64, 32 a group of four epilogue warps.
 constexpr int kFew = 64;
 constexpr int kFewSteps = 4;       // contraction steps of 64 a stage, which is also a segment
@@ -62,8 +80,6 @@ constexpr int kFewSmem = 230 * 1000;
 static_assert(kFewSmem <= 232448, "shared memory per CTA");
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 constexpr float kLowest = -1.0e30f;
-
-enum CeKind { kLse, kGrad, kDh, kDw };
 
 struct CeParams {
   const int* count;      // rows that count
@@ -74,7 +90,7 @@ struct CeParams {
   int first;             // dh: store (else add)
   float k;               // scale log2 e
   const int* target;     // [rows_cap], -1 past the rows
-  float2* part;          // lse: [2 column tiles][rows_cap]: maximum of l k, sum of exp2(l k - maximum)
+  float2* part;          // lse: [column tiles, or CTAs][rows_cap]: maximum of l k, sum of exp2(l k - maximum)
   float* hit;            // lse: l_target (before the scale)
   const float* lse2;     // grad: lse log2 e
   const float2* coef;    // grad: scale dl (1 + 2 z lse), scale dl
@@ -139,7 +155,7 @@ struct CeTile {
   int row0, col0, n, split, ks0, ks;
 };
 // Groups of kGroup row tiles; within one, column after column.
-template <int KIND>
+template <int KIND, int E>
 __device__ __forceinline__ CeTile ce_tile(const CeWork<KIND>& w, int tile) {
   CeTile t;
   const int per = w.mt * w.nt;
@@ -151,7 +167,7 @@ __device__ __forceinline__ CeTile ce_tile(const CeWork<KIND>& w, int tile) {
   const int c = i / rows;
   t.row0 = (g * kGroup + i - c * rows) * kTile;
   t.col0 = c * kTile;
-  t.n = w.n - t.col0 <= 128 ? 128 : 256;
+  t.n = E == 8 && w.n - t.col0 <= 128 ? 128 : 256;
   t.ks0 = t.split * w.split_steps;
   t.ks = max(0, min(w.split_steps, (w.k + kBk - 1) / kBk - t.ks0));
   return t;
@@ -226,15 +242,16 @@ __device__ __forceinline__ void join_chunk(float (&x)[32], int c, int n, int row
   sum += a + b;
 }
 
-template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int KIND, int E>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmC, const CeParams p) {
   constexpr bool kAMn = KIND == kDw, kBMn = KIND == kDh || KIND == kDw;
+  constexpr int kStages = CeCfg<KIND, E>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* turn = smem + kStages * kStage;    // [8 warps][32 rows x 128 bytes]
-  uint64_t* full = reinterpret_cast<uint64_t*>(turn + kEpiWarps * 4096);   // rank 0: both CTAs' operands landed
+  uint8_t* turn = smem + kStages * kStage;    // [E warps][32 rows x 128 bytes]
+  uint64_t* full = reinterpret_cast<uint64_t*>(turn + CeCfg<KIND, E>::kTurn);   // rank 0: both CTAs' operands landed
   uint64_t* empty = full + kStages;    // the stage's MMAs are done
   uint64_t* tfull = empty + kStages;   // [2] an accumulator is complete
   uint64_t* tempty = tfull + 2;        // [2] rank 0: both CTAs drained it
@@ -252,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpiWarps);
+      mbar_init(&tempty[a], 2 * E);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -278,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int tile = cid; ok && tile < w.total; tile += ncl) {
-      const CeTile t = ce_tile<KIND>(w, tile);
+      const CeTile t = ce_tile<KIND, E>(w, tile);
       const int arow = t.row0 + 128 * rank;                                  // this CTA's rows of A
       const int brow = t.col0 + t.n / 2 * rank + (KIND == kGrad ? p.v0 : 0);   // its half of the N rows
       for (int ks = 0; ks < t.ks; ++ks, ++it) {
@@ -327,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t it = 0, tc = 0;
       bool ok = true;
       for (int tile = cid; ok && tile < w.total; tile += ncl, ++tc) {
-        const CeTile t = ce_tile<KIND>(w, tile);
+        const CeTile t = ce_tile<KIND, E>(w, tile);
         const uint32_t idesc = idesc0 | ((static_cast<uint32_t>(t.n) >> 3) << 17);
         uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) break;
@@ -380,34 +397,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------- epilogue
     const int q = warp & 3, h = (warp - 2) >> 2;
     uint8_t* ws = turn + (warp - 2) * 4096;
+    float2(*red)[E / 4][128] = reinterpret_cast<float2(*)[E / 4][128]>(turn);   // forward: [2 turns]
     const uint32_t tempty0 = cluster_addr(tempty, 0);
     uint32_t tc = 0;
-    for (int tile = cid; tile < w.total; tile += ncl) {
-      const CeTile t = ce_tile<KIND>(w, tile);
-      const int row = t.row0 + 128 * rank + 32 * q + lane;     // this thread's
-      const int row_w = row - lane;
-      const int cols = t.n / 2, c0 = t.col0 + h * cols;        // this warp's columns
-      int target = -1;
-      float lse2 = 0.0f;
-      float2 coef = make_float2(0.0f, 0.0f);
+    int side = 0;
+    bool dead = false;   // forward: a wait ran out of time; the tiles' barriers are still met
+    struct {
+      int target;
+      float lse2;
+      float2 coef;
+    } next{};
+    auto row_values = [&](int tile) {
       if constexpr (KIND == kLse || KIND == kGrad) {
-        target = p.target[row] - (KIND == kGrad ? p.v0 : 0);
+        const int row = ce_tile<KIND, E>(w, tile).row0 + 128 * rank + 32 * q + lane;
+        next.target = p.target[row];
         if constexpr (KIND == kGrad) {
-          lse2 = p.lse2[row];
-          coef = p.coef[row];
+          next.lse2 = p.lse2[row];
+          next.coef = p.coef[row];
         }
       }
+    };
+    if (cid < w.total) row_values(cid);
+    for (int tile = cid; tile < w.total; tile += ncl) {
+      const CeTile t = ce_tile<KIND, E>(w, tile);
+      const int row = t.row0 + 128 * rank + 32 * q + lane;     // this thread's
+      const int row_w = row - lane;
+      const int cols = t.n / (E / 4), c0 = t.col0 + h * cols;  // this warp's columns
+      // what the rows need, asked for a tile ahead
+      const int target = next.target - (KIND == kGrad ? p.v0 : 0);
+      const float lse2 = next.lse2;
+      const float2 coef = next.coef;
+      if (tile + ncl < w.total) row_values(tile + ncl);
       if constexpr (KIND == kLse) {
         float top = kLowest, sum = 0.0f;
-        bool ok = true;
-        if (t.ks <= kSegment) {
+        if (dead) {
+          // nothing is waited for, but the barrier below is met
+        } else if (E == 16 || t.ks <= kSegment) {   // one segment
           const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
           ++tc;
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
+          dead = !__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err));
           tc_fence_after();
           const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-          for (int ci = 0; ci < cols / 32; ++ci) {
+          for (int ci = 0; ci < (dead ? 0 : cols / 32); ++ci) {
             uint32_t v[32];
             tmem_ld32(tbase + 32 * ci, v);
             tmem_ld_wait();
@@ -421,15 +453,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
             join_chunk(x, c0 + 32 * ci, w.n, row, target, p, top, sum);
           }
-        } else {
+        } else if constexpr (E == 8) {
           // this thread's 128 columns: sums of the segments
           float x[4][32];
           for (int ks = 0; ks < t.ks; ks += kSegment, ++tc) {
             const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) {
-              ok = false;
-              break;
-            }
+            dead = !__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err));
+            if (dead) break;
             tc_fence_after();
             const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
             const bool last = ks + kSegment >= t.ks;
@@ -455,8 +485,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!ok) break;
-        p.part[static_cast<long long>(2 * (t.col0 / kTile) + h) * p.rows_cap + row] = make_float2(top, sum);
+        // the warps that share the rows
+        red[side][h][32 * q + lane] = make_float2(top, sum);
+        named_bar_sync(1 + q, 8 * E);
+        if (h == 0) {
+#pragma unroll
+          for (int i = 1; i < E / 4; ++i) {
+            const float2 r = red[side][i][32 * q + lane];
+            const float m = fmaxf(top, r.x);
+            sum = sum * exp2_fast(top - m) + r.y * exp2_fast(r.x - m);
+            top = m;
+          }
+          p.part[static_cast<long long>(t.col0 / kTile) * p.rows_cap + row] = make_float2(top, sum);
+        }
+        side ^= 1;
       } else {
         const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
         ++tc;
@@ -474,62 +516,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
           }
           const int c = c0 + 32 * ci;
-          {
-            constexpr int kHalves = KIND == kDh ? 1 : 2;   // chunks of 32 columns in 128 bytes
-            float x[32];
+          constexpr int kHalves = KIND == kDh ? 1 : 2;   // chunks of 32 columns in 128 bytes
+          float x[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
-            if (KIND != kGrad && t.ks == 0) {   // an empty contraction
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+          if (KIND != kGrad && t.ks == 0) {   // an empty contraction
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+            for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+          }
+          if constexpr (KIND == kGrad) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = coef.x * exp2_fast(fmaf(x[j], p.k, -lse2));
+            if (static_cast<unsigned>(target - c) < 32u) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (target - c == j) x[j] -= coef.y;
             }
-            if constexpr (KIND == kGrad) {
+            if (c + 32 > w.n) {   // past the piece, whose end is the vocabulary's
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = coef.x * exp2_fast(fmaf(x[j], p.k, -lse2));
-              if (static_cast<unsigned>(target - c) < 32u) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (target - c == j) x[j] -= coef.y;
-              }
-              if (c + 32 > w.n) {   // past the piece, whose end is the vocabulary's
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (c + j >= w.n) x[j] = 0.0f;
-              }
+              for (int j = 0; j < 32; ++j)
+                if (c + j >= w.n) x[j] = 0.0f;
             }
-            if (ci % kHalves == 0) {   // the stores that read the buffer before are done
-              if (lane == 0) bulk_wait_read<0>();
-              __syncwarp();
-            }
-            if constexpr (KIND == kDh) {
+          }
+          if (ci % kHalves == 0) {   // the stores that read the buffer before are done
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+          }
+          if constexpr (KIND == kDh) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                stage16(ws, lane, j, make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
-                                                __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])));
-            } else {
+            for (int j = 0; j < 8; ++j)
+              stage16(ws, lane, j, make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                                              __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])));
+          } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                stage16(ws, lane, 4 * (ci % kHalves) + j,
-                        make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
-                                   pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7])));
-            }
-            if (ci % kHalves == kHalves - 1) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                const int cs = c - 32 * (kHalves - 1);
-                if constexpr (KIND == kGrad) {
-                  tma_store_2d(&tmC, ws, cs, row_w);
-                } else if constexpr (KIND == kDh) {
-                  if (cs < p.D) {
-                    if (p.first) tma_store_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
-                    else tma_reduce_add_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
-                  }
-                } else {
-                  if (cs < p.D && p.v0 + row_w < p.V) tma_store_2d(&tmC, ws, cs, p.v0 + row_w);
+            for (int j = 0; j < 4; ++j)
+              stage16(ws, lane, 4 * (ci % kHalves) + j,
+                      make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
+                                 pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7])));
+          }
+          if (ci % kHalves == kHalves - 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int cs = c - 32 * (kHalves - 1);
+              if constexpr (KIND == kGrad) {
+                tma_store_2d(&tmC, ws, cs, row_w);
+              } else if constexpr (KIND == kDh) {
+                if (cs < p.D) {
+                  if (p.first) tma_store_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
+                  else tma_reduce_add_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
                 }
-                bulk_commit();
+              } else {
+                if (cs < p.D && p.v0 + row_w < p.V) tma_store_2d(&tmC, ws, cs, p.v0 + row_w);
               }
+              bulk_commit();
             }
           }
         }
@@ -961,17 +1001,19 @@ bool supported(const moe_linear_ce_config* c) {
 }
 
 // Parts of the vocabulary that the dh product sums apart, so that its tiles
-// fill the pairs: the fewest whose last round is fullest, a part being worth
-// three percent of a round (its sums are written and read once more).
-int dh_splits(int T, int D, int pairs) {
+// fill the pairs: what takes the least time by a stage's 0.27 us, a tile's 1.5 us around its
+// stages, and the parts' sums at 4 TB/s (written once a piece and read in the end).
+int dh_splits(int T, int D, int64_t piece, int pairs) {
   const long long tiles = static_cast<long long>((T + kTile - 1) / kTile) * ((D + kTile - 1) / kTile);
+  const long long steps = (piece + kBk - 1) / kBk;
   int best = 1;
-  double cost = 1e30;
-  for (int s = 1; s <= 16; ++s) {
-    const long long n = tiles * s;
-    const double c = static_cast<double>((n + pairs - 1) / pairs) * pairs / static_cast<double>(n) + 0.03 * s;
-    if (c < cost) {
-      cost = c;
+  double least = 1e30;
+  for (int s = 1; s <= 64 && s <= steps; ++s) {
+    const double rounds = static_cast<double>((tiles * s + pairs - 1) / pairs);
+    const double us = rounds * (0.27 * static_cast<double>((steps + s - 1) / s) + 1.5) +
+                      static_cast<double>(s) * T * D * 8.0 / 4.0e6;
+    if (us < least) {
+      least = us;
       best = s;
     }
   }
@@ -979,7 +1021,7 @@ int dh_splits(int T, int D, int pairs) {
 }
 
 // Tokens that the vocabulary-wise forward takes: the weight's bytes bound both,
-// and it moves no others (1 x 2048 x 131072: 87 and 103 us).
+// and it moves no others (1 x 2048 x 131072 87 and 103 us, 64 tokens 95 and 107).
 bool few(int T) { return T <= kFew; }
 
 struct Layout {
@@ -997,7 +1039,8 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
   l.rows_cap = (c->tokens + kTile - 1) / kTile * kTile;
   l.col_tiles = (c->vocab + kTile - 1) / kTile;
   l.piece = std::min<int64_t>(piece, static_cast<int64_t>(l.col_tiles) * kTile);
-  l.splits = dh_splits(c->tokens, c->d_model, sms / 2);
+  // whatever the piece, so that the workspace grows with it alone: by pieces of about 512 MB
+  l.splits = dh_splits(c->tokens, c->d_model, std::min<int64_t>(c->vocab, std::max(kTile, (256 << 20) / std::max(l.rows_cap, 1))), sms / 2);
   const size_t rows = l.rows_cap, D = c->d_model;
   size_t at = 0;
   l.count = take(&at, 4);
@@ -1012,7 +1055,7 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
     l.g = take(&at, rows * 2 * l.piece);
   } else {
     l.hit = take(&at, rows * 4);
-    l.part = take(&at, rows * 8 * std::max(2 * l.col_tiles, few(c->tokens) ? sms : 0));
+    l.part = take(&at, rows * 8 * std::max(l.col_tiles, few(c->tokens) ? sms : 0));
   }
   l.bytes = at;
   return l;
@@ -1028,17 +1071,30 @@ bool map_2d(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int b
                       box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int KIND>
-cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
-                        long long tiles, cudaStream_t stream) {
+template <int KIND, int E>
+cudaError_t launch_gemm_as(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
+                           long long tiles, cudaStream_t stream) {
+  using C = CeCfg<KIND, E>;
   static PerDeviceOnce once;
-  cudaError_t e = once.once(
-      [&] { return cudaFuncSetAttribute(ce_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+  cudaError_t e = once.once([&] {
+    return cudaFuncSetAttribute(ce_gemm_kernel<KIND, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<CUtensorMap*>(&a), const_cast<CUtensorMap*>(&b), const_cast<CUtensorMap*>(&c),
                   const_cast<CeParams*>(&p)};
   const int grid = 2 * static_cast<int>(std::max<long long>(1, std::min<long long>(pairs, tiles)));
-  return launch_dependent(reinterpret_cast<const void*>(ce_gemm_kernel<KIND>), dim3(grid), kThreads, kSmem, stream, args);
+  return launch_dependent(reinterpret_cast<const void*>(ce_gemm_kernel<KIND, E>), dim3(grid), C::kThreads, C::kSmem, stream,
+                          args);
+}
+// Sixteen epilogue warps where the forward's product is too short to hide eight
+// warps' exponentials and takes one segment (512 x 256 x 32768 22.8 and 20.2 us, 4096 x 512 x
+// 65536 224 and 210, 4096 x 1024 x 65536 373 and 366).  The backward's first product gained nothing.
+template <int KIND>
+cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
+                        long long tiles, cudaStream_t stream) {
+  if constexpr (KIND == kLse)
+    if (p.D <= kSegment * kBk) return launch_gemm_as<KIND, 16>(a, b, c, p, pairs, tiles, stream);
+  return launch_gemm_as<KIND, 8>(a, b, c, p, pairs, tiles, stream);
 }
 
 template <int N>
@@ -1136,7 +1192,7 @@ moe_status moe_linear_ce_forward(const moe_linear_ce_config* cfg, const void* h,
   p.part = at<float2>(workspace, l.part);
   p.hit = at<float>(workspace, l.hit);
   if (launch_rows(r, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
-  int parts = 2 * l.col_tiles;
+  int parts = l.col_tiles;
   if (few(cfg->tokens)) {
     parts = sms;
     if ((cfg->tokens <= 32 ? launch_few<32>(weight, r.packed, p, sms, stream)

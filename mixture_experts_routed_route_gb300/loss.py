@@ -17,7 +17,7 @@ from .block import put_back, unaligned
 from .optim import _error_word
 
 # bytes that a backward call's own workspace may take for a piece's gradient of the logits, unless 256 entries need more
-PIECE_BYTES = 256 << 20
+PIECE_BYTES = 512 << 20
 
 _TARGET = {_INT32: 4, _INT64: 8}
 
@@ -52,7 +52,7 @@ def _workspace_bytes(cfg, backward, piece):
 def workspace(T, D, V, *, backward=True, piece=None, device="cuda"):
     """A workspace for calls on up to T tokens: of the forward or the backward,
     which works in pieces of `piece` vocabulary entries (default: as many as
-    256 MiB hold; a larger workspace means larger pieces)."""
+    512 MiB hold; a larger workspace means larger pieces)."""
     cfg = abi.moe_linear_ce_config(T, D, V, 8, 1.0, 0.0, -100, 0)
     device = torch.device(device)
     with torch.cuda.device(device):
