@@ -798,8 +798,9 @@ MOE_API moe_status moe_muon_update(const moe_muon_config* cfg, const moe_muon_ra
  *                     graph draws a new mask where the program advances the
  *                     step between replays; may be NULL with p = 0
  *   site              tells calls of one step apart (a layer's number)
- * T may be 0.  Pointers 16-byte aligned.  Errors: MOE_ERR_INVALID_ARG,
- * MOE_ERR_UNSUPPORTED (more than 2^31 blocks of 8192 elements).
+ * T may be 0.  Pointers 16-byte aligned.  Errors: MOE_ERR_INVALID_ARG (null
+ * cfg, T < 0, D < 1, unknown type, p outside [0, 1], p of 2^-17 or more without
+ * rng, a stride in (0, D), null or misaligned pointers).
  */
 typedef struct {
   int32_t tokens;          /* T */

@@ -423,6 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
       const int row = t.row0 + 128 * rank + 32 * q + lane;     // this thread's
       const int row_w = row - lane;
       const int cols = t.n / (E / 4), c0 = t.col0 + h * cols;  // this warp's columns
+      // Whether anything reads this warp's rows: those that count; of g, which the dW product reads 64 rows at a time, those
+      // up to a multiple of 64; of dW, the vocabulary's.
+      const bool live = KIND == kDw ? p.v0 + row_w < p.V : row_w < (KIND == kGrad ? (w.m + 63) / 64 * 64 : w.m);
       // what the rows need, asked for a tile ahead
       const int target = next.target - (KIND == kGrad ? p.v0 : 0);
       const float lse2 = next.lse2;
@@ -505,6 +508,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
         if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
         tc_fence_after();
         const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
+        if (!live) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
+          continue;
+        }
 #pragma unroll 1
         for (int ci = 0; ci < cols / 32; ++ci) {
           uint32_t v[32];
@@ -567,7 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
                   else tma_reduce_add_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
                 }
               } else {
-                if (cs < p.D && p.v0 + row_w < p.V) tma_store_2d(&tmC, ws, cs, p.v0 + row_w);
+                if (cs < p.D) tma_store_2d(&tmC, ws, cs, p.v0 + row_w);
               }
               bulk_commit();
             }
@@ -1040,7 +1049,8 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
   l.col_tiles = (c->vocab + kTile - 1) / kTile;
   l.piece = std::min<int64_t>(piece, static_cast<int64_t>(l.col_tiles) * kTile);
   // whatever the piece, so that the workspace grows with it alone: by pieces of about 512 MB
-  l.splits = dh_splits(c->tokens, c->d_model, std::min<int64_t>(c->vocab, std::max(kTile, (256 << 20) / std::max(l.rows_cap, 1))), sms / 2);
+  l.splits = dh_splits(c->tokens, c->d_model,
+                       std::min<int64_t>(c->vocab, std::max(kTile, (256 << 20) / std::max(l.rows_cap, 1))), sms / 2);
   const size_t rows = l.rows_cap, D = c->d_model;
   size_t at = 0;
   l.count = take(&at, 4);
