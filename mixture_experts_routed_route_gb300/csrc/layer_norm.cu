@@ -75,7 +75,7 @@ struct LnParams {
   float alpha, beta, eps;
   DropParams drop;
   float* stats;          // [2][T]: mean, 1/sqrt(var + eps)
-  float* partial;        // backward: [2][gridDim.x][D]: sums of dh n, dh
+  float* partial;        // backward: [2][gridDim.x][pieces of 8]: sums of dh n, dh
 };
 
 using Pair = unsigned long long;   // two FP32, one instruction (packed f32x2)
@@ -651,18 +651,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
   }
   cp_wait<0>();
   __syncthreads();   // the rows' memory is free: it takes the groups' sums
-  float4* acc = reinterpret_cast<float4*>(shared) + 2 * planes;   // [2 halves][planes], when groups > 1
+  float4* acc = reinterpret_cast<float4*>(shared) + 2 * planes;   // [2 arrays][2 halves][planes], when groups > 1
+  for (int k = 0; k < p.groups; ++k) {
+    if (k == g.grp) {
 #pragma unroll
-  for (int arr = 0; arr < 2; ++arr) {
-    float* out = p.partial + (static_cast<long long>(arr) * gridDim.x + blockIdx.x) * p.D;
-    for (int k = 0; k < p.groups; ++k) {
-      if (k == g.grp) {
+      for (int arr = 0; arr < 2; ++arr) {
+        // in the layout's pieces, shifted like the rows
+        float4* out = reinterpret_cast<float4*>(p.partial) + (static_cast<long long>(arr) * gridDim.x + blockIdx.x) * 2 * planes;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const int c = g.piece(i);
           if (c >= g.pieces) continue;
           Pair b[4];
-          if (k > 0) table_load(reinterpret_cast<uint8_t*>(acc), planes, 0, c, b);
+          if (k > 0) table_load(reinterpret_cast<uint8_t*>(acc), planes, arr, c, b);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const Pair v = arr == 0 ? sw[i][j] : sb[i][j];
@@ -671,25 +672,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
           float v[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) split(b[j], v[2 * j], v[2 * j + 1]);
-          if (k + 1 < p.groups) {
-            acc[c] = make_float4(v[0], v[1], v[2], v[3]);
-            acc[planes + c] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (!ODD || g.valid(c, j)) out[8 * c + j - g.off] = v[j];
-          }
+          const bool last = k + 1 == p.groups;
+          float4* lo = last ? out + 2 * c : table_at(reinterpret_cast<uint8_t*>(acc), planes, arr, 0, c);
+          float4* hi = last ? lo + 1 : lo + planes;
+          *lo = make_float4(v[0], v[1], v[2], v[3]);
+          *hi = make_float4(v[4], v[5], v[6], v[7]);
         }
       }
-      if (p.groups > 1) __syncthreads();
     }
+    if (k + 1 < p.groups) __syncthreads();
   }
 }
 
 // The CTAs' column sums joined in a fixed order (eight interleaved sums a
 // column, then those in order): blockIdx.y = 0 dweight, 1 dbias.
-__global__ void __launch_bounds__(256) layer_norm_sums_kernel(const float* partial, int rows, int D, float* dweight,
-                                                              float* dbias) {
+__global__ void __launch_bounds__(256) layer_norm_sums_kernel(const float* partial, int rows, int D, int pitch,
+                                                              float* dweight, float* dbias) {
   __shared__ float part[8][33];
   float* out = blockIdx.y ? dbias : dweight;
   if (out == nullptr) return;
@@ -697,9 +695,10 @@ __global__ void __launch_bounds__(256) layer_norm_sums_kernel(const float* parti
   const int c = blockIdx.x * 32 + cx;
   float s = 0.0f;
   if (c < D) {
-    const float* q = partial + static_cast<long long>(blockIdx.y) * rows * D + c;
+    const float* q = partial + static_cast<long long>(blockIdx.y) * rows * pitch + c;
+    // CTA r's columns are shifted like its rows
 #pragma unroll 8
-    for (int r = ry; r < rows; r += 8) s += q[static_cast<long long>(r) * D];
+    for (int r = ry; r < rows; r += 8) s += q[static_cast<long long>(r) * pitch + (r * (D & 7) & 7)];
   }
   part[ry][cx] = s;
   __syncthreads();
@@ -748,6 +747,7 @@ constexpr int kSmem = 216 * 1024;   // the columns' factors and the backward's r
 
 struct Shape {
   int pieces, ctas, threads;
+  int row_pieces;      // pieces of a row, at most
   bool odd;
   size_t smem;
 };
@@ -758,7 +758,7 @@ Shape place(LnParams* p, bool fwd, int esz, int sms) {
   const bool ragged = p->D % 8 != 0;
   s.odd = ragged;
   for (const Tensor* t : {&p->x, &p->o, &p->dy, &p->dh, &p->out0, &p->out1}) s.odd = s.odd || (t->base && !t->vec);
-  const int all = (p->D + 7 + (s.odd ? 7 : 0)) / 8;   // pieces of a row, at most
+  const int all = s.row_pieces = (p->D + 7 + (s.odd ? 7 : 0)) / 8;
   // One piece a thread where a warp holds the row, and where an FP32 residual's two would not fit the forward's registers
   // beside the other group's (16384 x 2048 without dropout 62.7 and 73.8 us; with it 73.3 and 68.6); four for the odd
   // widths next to the limit, which two do not hold.
@@ -778,7 +778,7 @@ Shape place(LnParams* p, bool fwd, int esz, int sms) {
   s.smem = 2 * all * 32;
   if (!fwd) {
     p->stages = std::max(1, std::min(4, room / (p->groups * p->slot)));
-    s.smem = all * 32 + std::max(all * 32, p->groups * p->stages * p->slot);
+    s.smem = all * 32 + std::max(p->groups > 1 ? all * 64 : 0, p->groups * p->stages * p->slot);
   }
   return s;
 }
@@ -858,7 +858,7 @@ size_t moe_layer_norm_workspace_bytes(const moe_layer_norm_config* cfg) {
   const int sms = device_sms();
   if (sms <= 0) return 0;
   // two arrays of column sums a CTA
-  return 2 * static_cast<size_t>(std::min(cfg->tokens, std::max(8, sms))) * cfg->d_model * sizeof(float) + 256;
+  return 2 * static_cast<size_t>(std::min(cfg->tokens, std::max(8, sms))) * static_cast<size_t>((cfg->d_model + 14) / 8 * 8) * sizeof(float) + 256;
 }
 
 moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, const void* y, const void* weight, const float* stats,
@@ -899,7 +899,8 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, const void*
   const Shape s = place(&p, false, esz, sms);
   if (launch_norm(false, f32, s, p, stream) != cudaSuccess) return MOE_ERR_CUDA;
   if (dweight || dbias) {
-    layer_norm_sums_kernel<<<dim3((D + 31) / 32, 2), 256, 0, stream>>>(p.partial, s.ctas, D, dweight, dbias);
+    layer_norm_sums_kernel<<<dim3((D + 31) / 32, 2), 256, 0, stream>>>(p.partial, s.ctas, D, 8 * s.row_pieces, dweight,
+                                                                      dbias);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
