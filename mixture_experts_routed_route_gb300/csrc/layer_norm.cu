@@ -51,7 +51,10 @@ namespace moe {
 namespace {
 
 constexpr int kMaxCols = 8192;
-constexpr int kFwdThreads = 896;   // of a CTA: 72 registers a thread
+// Threads of a CTA: 896 have 72 registers each, 512 have 128.  Odd widths with
+// dropout run out of the 72 (16384 x 1411 with 896 threads 64 us, with 512 57; FP32 75 and 63;
+// without dropout 38 and 42).
+constexpr int fwd_threads(bool odd, bool drop) { return odd && drop ? 512 : 896; }
 constexpr int kBwdThreads = 512;   // 128 registers: the column sums and a row's normalised values stay in them
 constexpr int kMaxGroups = 15;     // named barriers 1 .. 15
 
@@ -109,8 +112,6 @@ __device__ __forceinline__ float sum2(Pair v) {
   return a + b;
 }
 
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ float param_at(const void* p, int f32, int i) {
   return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
@@ -147,6 +148,27 @@ struct Raw<__nv_bfloat16> {
     for (int j = 0; j < 4; ++j)
       *w[j] &= (on >> (2 * j) & 1 ? 0x0000FFFFu : 0u) | (on >> (2 * j) & 2 ? 0xFFFF0000u : 0u);
   }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  // Elements lo .. hi - 1 of a piece at a row's end.  vec: the piece is aligned; what is missing then is at
+  // one of its ends, and one, two and four elements at a time are enough.
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int lo, int hi, bool vec) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    unsigned short* s = reinterpret_cast<unsigned short*>(p);
+    if (vec && hi == 8) {
+      const int i = (lo + 1) & 6;   // the first whole pair (8 & 6 = 0: none)
+      if (lo & 1) s[lo] = static_cast<unsigned short>((lo < 4 ? (lo == 1 ? w[0] : w[1]) : lo == 5 ? w[2] : w[3]) >> 16);
+      if (i & 2) *reinterpret_cast<uint32_t*>(s + i) = i == 2 ? w[1] : w[3];
+      if (lo <= 4) *reinterpret_cast<uint2*>(s + 4) = make_uint2(w[2], w[3]);
+    } else if (vec && lo == 0) {
+      if (hi & 4) *reinterpret_cast<uint2*>(s) = make_uint2(w[0], w[1]);
+      if (hi & 2) *reinterpret_cast<uint32_t*>(s + (hi & 4)) = hi & 4 ? w[2] : w[0];
+      if (hi & 1) s[hi - 1] = static_cast<unsigned short>(hi < 4 ? (hi == 1 ? w[0] : w[1]) : hi == 5 ? w[2] : w[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= lo && j < hi) s[j] = static_cast<unsigned short>(w[j >> 1] >> (16 * (j & 1)));
+    }
+  }
   __device__ __forceinline__ void keep(const uint4& m) { u = make_uint4(u.x & m.x, u.y & m.y, u.z & m.z, u.w & m.w); }
   __device__ __forceinline__ void get(Pair (&q)[4]) const {
     q[0] = pair_of(bf16_lo(u.x), bf16_hi(u.x));
@@ -158,6 +180,33 @@ struct Raw<__nv_bfloat16> {
 template <>
 struct Raw<float> {
   float4 a, b;
+  __device__ __forceinline__ void set(const Pair (&q)[4]) {
+    split(q[0], a.x, a.y);
+    split(q[1], a.z, a.w);
+    split(q[2], b.x, b.y);
+    split(q[3], b.z, b.w);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void store(float* p, int lo, int hi, bool vec) const {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (vec && hi == 8) {
+      const int i = (lo + 1) & 6;
+      if (lo & 1) p[lo] = lo < 4 ? (lo == 1 ? v[1] : v[3]) : lo == 5 ? v[5] : v[7];
+      if (i & 2) *reinterpret_cast<float2*>(p + i) = i == 2 ? make_float2(v[2], v[3]) : make_float2(v[6], v[7]);
+      if (lo <= 4) *reinterpret_cast<float4*>(p + 4) = b;
+    } else if (vec && lo == 0) {
+      if (hi & 4) *reinterpret_cast<float4*>(p) = a;
+      if (hi & 2) *reinterpret_cast<float2*>(p + (hi & 4)) = hi & 4 ? make_float2(v[4], v[5]) : make_float2(v[0], v[1]);
+      if (hi & 1) p[hi - 1] = hi < 4 ? (hi == 1 ? v[0] : v[2]) : hi == 5 ? v[4] : v[6];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= lo && j < hi) p[j] = v[j];
+    }
+  }
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
@@ -183,18 +232,8 @@ struct Raw<float> {
   }
 };
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const Pair (&q)[4]) {
-  Raw<__nv_bfloat16> v;
-  v.set(q);
-  *reinterpret_cast<uint4*>(p) = v.u;
-}
-__device__ __forceinline__ void store8(float* p, const Pair (&q)[4]) {
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) split(q[j], v[2 * j], v[2 * j + 1]);
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+// What is read where a row's vectors may not be.
+__device__ uint4 g_zeros[2];
 
 // A group of warps.  Pieces are numbered from the aligned start of a row;
 // element j of piece c is column 8 c + j - off.  ODD: D is no multiple of 8 (off
@@ -299,39 +338,41 @@ struct Group {
     else v.gather(src, columns(c));
     return v;
   }
-  // The thread's pieces of a row; anything past its ends.
+  // Out of line for the rows that need it, which are few.
+  template <typename X>
+  static __device__ __noinline__ Raw<X> single_call(const uint8_t* end, const X* src, uint32_t on, bool vec) {
+    Raw<X> v;
+    if (vec && reinterpret_cast<const uint8_t*>(src + 8) <= end) v.load(src);
+    else v.gather(src, on);
+    return v;
+  }
+  // The thread's pieces of a row; anything past its ends.  Where vectors may not
+  // be read, anything at all, for `mend` to put right when the row is used: a
+  // branch around the loads would keep the compiler from moving other work past them.
   template <typename X>
   __device__ __forceinline__ void load(const Tensor& s, long long row, Raw<X> (&q)[P]) const {
     const X* at = static_cast<const X*>(s.base) + row * s.ld + 8 * t - off;
-    if (vectors<X>(s, row)) {
+    const bool ok = vectors<X>(s, row);
 #pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (piece(i) < pieces) q[i].load(at + 8 * i * nt);
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < P; ++i) {
-        if (piece(i) >= pieces) continue;
-        const Raw<X> v = single<X>(s, at + 8 * i * nt, piece(i));
+    for (int i = 0; i < P; ++i)
+      if (piece(i) < pieces) q[i].load(ok ? at + 8 * i * nt : reinterpret_cast<const X*>(g_zeros));
+  }
+  template <typename X>
+  __device__ __forceinline__ void mend(const Tensor& s, long long row, Raw<X> (&q)[P]) const {
+    if (!ODD || vectors<X>(s, row)) return;
+    const X* at = static_cast<const X*>(s.base) + row * s.ld + 8 * t - off;
 #pragma unroll
-        for (int k = 0; k < P; ++k)
-          if (k == i) q[k] = v;
-      }
-    }
+    for (int i = 0; i < P; ++i)
+      if (piece(i) < pieces) q[i] = single_call<X>(s.end, at + 8 * i * nt, columns(piece(i)), s.vec);
   }
   // Piece c of a row of an output.
   template <typename X>
   __device__ __forceinline__ void store(const Tensor& o, long long row, int c, const Pair (&q)[4]) const {
     X* at = static_cast<X*>(o.base) + row * o.ld + 8 * c - off;
-    if (!ODD || (o.vec && whole(c))) {
-      store8(at, q);
-    } else {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) split(q[j], v[2 * j], v[2 * j + 1]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (valid(c, j)) put(at + j, v[j]);
-    }
+    Raw<X> v;
+    v.set(q);
+    if (!ODD || (o.vec && whole(c))) v.store(at);
+    else v.store(at, max(0, off - 8 * c), min(8, p.D + off - 8 * c), o.vec);
   }
   // ... of one in BF16, zeros where `m` has them.
   __device__ __forceinline__ void store(const Tensor& o, long long row, int c, const Pair (&q)[4], const uint4& m) const {
@@ -339,14 +380,8 @@ struct Group {
     Raw<__nv_bfloat16> v;
     v.set(q);
     v.keep(m);
-    if (!ODD || (o.vec && whole(c))) {
-      *reinterpret_cast<uint4*>(at) = v.u;
-    } else {
-      const uint32_t w[4] = {v.u.x, v.u.y, v.u.z, v.u.w};
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (valid(c, j)) reinterpret_cast<unsigned short*>(at)[j] = static_cast<unsigned short>(w[j >> 1] >> (16 * (j & 1)));
-    }
+    if (!ODD || (o.vec && whole(c))) v.store(at);
+    else v.store(at, max(0, off - 8 * c), min(8, p.D + off - 8 * c), o.vec);
   }
   // Which of the row's elements dropout keeps: keep_words of each piece.
   __device__ __forceinline__ void draw(const PhiloxKey<false>& key, long long row, uint4 (&m)[P]) const {
@@ -404,7 +439,7 @@ __device__ __forceinline__ void make_table(const LnParams& p, uint8_t* shared, i
 // row's loads or stores keeps the compiler from moving anything past it, which
 // costs 17 % (8192 x 7168 without dropout: 72.9 and 84.1 us).
 template <typename R, int P, bool ODD, bool DROP, bool ALL>
-__global__ void __launch_bounds__(kFwdThreads, 1) layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
+__global__ void __launch_bounds__(fwd_threads(ODD, DROP), 1) layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) float red_all[kMaxGroups][128];
   Group<P, ODD> g(p, red_all);
@@ -427,6 +462,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) layer_norm_fwd_kernel(const __
   make_table<2>(p, shared, g.off, g.pieces, planes);
   const float inv_d = 1.0f / static_cast<float>(p.D), beta = p.beta * p.drop.scale;
   for (; row < p.T; row += step) {
+    g.mend(p.x, row, x);
+    if (has_o) g.mend(p.o, row, o);
     Pair y[P][4], s = both(0.0f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -762,15 +799,17 @@ Shape place(LnParams* p, bool fwd, int esz, int sms) {
   // One piece a thread where a warp holds the row, and where an FP32 residual's two would not fit the forward's registers
   // beside the other group's (16384 x 2048 without dropout 62.7 and 73.8 us; with it 73.3 and 68.6); four for the odd
   // widths next to the limit, which two do not hold.
-  s.pieces = all <= 32 || (fwd && esz == 4 && !p->drop.rng && all <= kFwdThreads) ? 1 : all <= 1024 ? 2 : 4;
+  s.pieces = all <= 32 || (fwd && esz == 4 && !p->drop.rng && all <= fwd_threads(s.odd, false)) ? 1 : all <= 1024 ? 2 : 4;
   p->warps = (all + 32 * s.pieces - 1) / (32 * s.pieces);
-  int most = std::min((fwd ? kFwdThreads : kBwdThreads) / 32 / p->warps, kMaxGroups);
+  int most = std::min((fwd ? fwd_threads(s.odd, p->drop.rng != nullptr) : kBwdThreads) / 32 / p->warps, kMaxGroups);
   const int room = kSmem - all * 32;
   if (!fwd) {
     p->slot = all * 8 * (2 * esz + 2);
     most = std::max(1, std::min(most, room / (2 * p->slot)));   // two rows in flight a group at least, where they fit
   }
-  p->groups = std::min(most, (p->T - 1) / sms + 1);
+  // no more groups than save a round of rows
+  const int rounds = (p->T - 1) / (sms * most) + 1;
+  p->groups = (p->T - 1) / (sms * rounds) + 1;
   s.threads = p->warps * p->groups * 32;
   // a group's rows have to be a multiple of 8 apart
   s.ctas = !ragged || p->T <= sms ? std::min(sms, p->T) : std::max(8, sms / 8 * 8);
