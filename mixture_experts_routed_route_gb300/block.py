@@ -417,15 +417,32 @@ def _layer_norm_config(name, x, weight, bias, residual_scale, branch_scale, drop
     if T >= _MOST or D >= _MOST:
         raise ValueError(f"{name}: sizes have to be below 2^31")
     par = _FP32
-    for which, w in (("weight", weight), ("bias", bias)):
-        if w is not None:
-            if w.dtype not in _TYPE:
-                raise ValueError("weight and bias are bfloat16 or float32")
-            _dense(which, w, w.dtype if which == "weight" or weight is None else weight.dtype, (D,), dev)
-            par = w.dtype
-    _check_rng(dropout, rng, site, dev)
+    if weight is not None or bias is not None:
+        par = (bias if weight is None else weight).dtype
+        if par not in _TYPE:
+            raise ValueError("weight and bias are bfloat16 or float32")
+        if weight is not None:
+            _dense("weight", weight, par, (D,), dev)
+        if bias is not None:
+            _dense("bias", bias, par, (D,), dev)
+    if dropout or rng is not None or site:
+        _check_rng(dropout, rng, site, dev)
     return _LayerNormConfig(T, D, _TYPE[kind], _TYPE[par], residual_scale, branch_scale, eps, site, dropout,
-                            _rows(name, x, kind, shape, dev), 0, 0, 0)
+                            _rows(name, x, kind, shape, dev))
+
+
+_norm_bytes = {}
+
+
+def _layer_norm_workspace(cfg, dev):
+    """moe_layer_norm_workspace_bytes, remembered by what it depends on."""
+    key = cfg.tokens, cfg.d_model, dev.index
+    nb = _norm_bytes.get(key)
+    if nb is None:
+        if len(_norm_bytes) >= 1024:
+            _norm_bytes.clear()
+        nb = _norm_bytes[key] = _LIB.moe_layer_norm_workspace_bytes(_byref(cfg))
+    return _empty(nb, dtype=torch.uint8, device=dev)
 
 
 def layer_norm(x, branch=None, *, weight=None, bias=None, residual_scale=1.0, branch_scale=1.0, dropout=0.0, rng=None,
@@ -503,12 +520,10 @@ def layer_norm_backward(y, stats, dh, dy=None, *, weight=None, bias=None, branch
         dbranch = _new(y, _BF16) if branch else None
         dweight = None if weight is None else _empty(D, dtype=_FP32, device=dev)
         dbias = None if bias is None else _empty(D, dtype=_FP32, device=dev)
-        ref = _byref(cfg)
-        nb = _LIB.moe_layer_norm_workspace_bytes(ref)
-        ws = _empty(nb, dtype=torch.uint8, device=dev)
-        status = _LIB.moe_layer_norm_backward(ref, y.data_ptr(), _at(weight), stats.data_ptr(), _at(rng), _at(dy),
+        ws = _layer_norm_workspace(cfg, dev)
+        status = _LIB.moe_layer_norm_backward(_byref(cfg), y.data_ptr(), _at(weight), stats.data_ptr(), _at(rng), _at(dy),
                                               dh.data_ptr(), dx.data_ptr(), _at(dbranch), _at(dweight), _at(dbias),
-                                              ws.data_ptr(), nb, s)
+                                              ws.data_ptr(), ws.numel(), s)
         if status:
             if status == _INVALID and unaligned(y, stats, dh, dy, weight, rng):
                 return layer_norm_backward(aligned(y), aligned(stats), aligned(dh), aligned(dy), weight=aligned(weight),
