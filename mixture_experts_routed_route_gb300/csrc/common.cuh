@@ -563,4 +563,8 @@ __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The wait alone: for the first kernel of a call, which may be placed while
+// whatever runs before it in the stream comes to its end.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace moe

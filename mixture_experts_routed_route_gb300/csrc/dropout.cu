@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
   X* out = static_cast<X*>(p.out);
   const long long hop = static_cast<long long>(gridDim.x) * kThreads;
   long long g = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  wait_previous();
   PhiloxKey<true> key{};
   if (p.drop.rng) key = philox_key<true>(p.drop);
   if constexpr (LAYOUT == kAny) {
@@ -181,12 +182,13 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
 }
 
 template <typename X>
-void launch(int layout, unsigned grid, const DropoutParams& p, cudaStream_t stream) {
-  if (layout == kAny) dropout_kernel<X, kAny, false><<<grid, kThreads, 0, stream>>>(p);
-  else if (layout == kFlat && p.residual) dropout_kernel<X, kFlat, true><<<grid, kThreads, 0, stream>>>(p);
-  else if (layout == kFlat) dropout_kernel<X, kFlat, false><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.residual) dropout_kernel<X, kRows, true><<<grid, kThreads, 0, stream>>>(p);
-  else dropout_kernel<X, kRows, false><<<grid, kThreads, 0, stream>>>(p);
+const void* kernel_of(int layout, bool residual) {
+  if (layout == kAny) return reinterpret_cast<const void*>(dropout_kernel<X, kAny, false>);
+  if (layout == kFlat)
+    return residual ? reinterpret_cast<const void*>(dropout_kernel<X, kFlat, true>)
+                    : reinterpret_cast<const void*>(dropout_kernel<X, kFlat, false>);
+  return residual ? reinterpret_cast<const void*>(dropout_kernel<X, kRows, true>)
+                  : reinterpret_cast<const void*>(dropout_kernel<X, kRows, false>);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -228,9 +230,11 @@ moe_status moe_dropout(const moe_dropout_config* cfg, const void* x, const void*
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
   const long long grid = std::min<long long>((p.groups + kThreads - 1) / kThreads, kCtas * sms);
-  if (cfg->type == MOE_TYPE_FP32) launch<float>(layout, static_cast<unsigned>(grid), p, stream);
-  else launch<__nv_bfloat16>(layout, static_cast<unsigned>(grid), p, stream);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  void* args[] = {&p};
+  const void* kernel =
+      cfg->type == MOE_TYPE_FP32 ? kernel_of<float>(layout, residual != nullptr) : kernel_of<__nv_bfloat16>(layout, residual != nullptr);
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, stream, args) == cudaSuccess ? MOE_OK
+                                                                                                              : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -28,8 +28,7 @@
 // products, 4 cycles a warp each, beside the norm's own arithmetic: forward 27.9 and 90.8 us, backward 48.8 us.
 // Tried and slower: forward rows through a ring too (27.5 us, 88.7 us), 24 warps
 // (80 registers: one row in flight a CTA, 24.7 us), one piece a thread (25.6 us); backward with rows
-// in registers (56 us, spills), 28 warps without a row's normalised values kept (53.7 us), a dependent launch
-// of the second kernel (40.5 us).
+// in registers (56 us, spills), 28 warps without a row's normalised values kept (53.7 us).
 //
 // Widths that 8 does not divide: row t starts t D mod 8 elements past a
 // 16-byte boundary.  Each group's rows are a multiple of 8 apart, so for it
@@ -443,6 +442,7 @@ __global__ void __launch_bounds__(fwd_threads(ODD, DROP), 1) layer_norm_fwd_kern
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) float red_all[kMaxGroups][128];
   Group<P, ODD> g(p, red_all);
+  wait_previous();
   const int planes = (p.D + 7 + (ODD ? 7 : 0)) >> 3;
   const long long step = static_cast<long long>(gridDim.x) * p.groups;
   long long row = g.grp * gridDim.x + blockIdx.x;
@@ -596,6 +596,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) float red_all[kMaxGroups][128];
   Group<P, ODD> g(p, red_all);
+  wait_previous();
   const int planes = (p.D + 7 + (ODD ? 7 : 0)) >> 3;
   const long long step = static_cast<long long>(gridDim.x) * p.groups;
   long long row = g.grp * gridDim.x + blockIdx.x;
@@ -726,6 +727,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
 __global__ void __launch_bounds__(256) layer_norm_sums_kernel(const float* partial, int rows, int D, int pitch,
                                                               float* dweight, float* dbias) {
   __shared__ float part[8][33];
+  wait_previous();
   float* out = blockIdx.y ? dbias : dweight;
   if (out == nullptr) return;
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
@@ -827,8 +829,8 @@ cudaError_t launch(K kernel, PerDeviceOnce& once, const Shape& s, const LnParams
   const cudaError_t e =
       once.once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
   if (e != cudaSuccess) return e;
-  kernel<<<s.ctas, s.threads, s.smem, stream>>>(p);
-  return cudaGetLastError();
+  void* args[] = {const_cast<LnParams*>(&p)};
+  return launch_dependent(reinterpret_cast<const void*>(kernel), dim3(s.ctas), s.threads, s.smem, stream, args);
 }
 
 template <typename R, int P, bool ODD, bool DROP>
@@ -938,9 +940,12 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, const void*
   const Shape s = place(&p, false, esz, sms);
   if (launch_norm(false, f32, s, p, stream) != cudaSuccess) return MOE_ERR_CUDA;
   if (dweight || dbias) {
-    layer_norm_sums_kernel<<<dim3((D + 31) / 32, 2), 256, 0, stream>>>(p.partial, s.ctas, D, 8 * s.row_pieces, dweight,
-                                                                      dbias);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    const float* partial = p.partial;
+    int rows = s.ctas, d = D, pitch = 8 * s.row_pieces;
+    void* args[] = {&partial, &rows, &d, &pitch, &dweight, &dbias};
+    if (launch_dependent(reinterpret_cast<const void*>(layer_norm_sums_kernel), dim3((D + 31) / 32, 2), 256, 0, stream,
+                         args) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }

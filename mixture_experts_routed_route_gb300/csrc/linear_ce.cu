@@ -895,8 +895,10 @@ __device__ __forceinline__ void pack_row(const RowParams& p, int i, int t) {
 
 // Up to 1024 tokens: every block finds the rows that count, the first writes them down, and all pack them.
 __global__ void __launch_bounds__(1024) ce_rows_once_kernel(const __grid_constant__ RowParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int counts[32], list[1024];
+  // in this order: the forward of few tokens reads the weight before its own wait, and everything before this call has ended then
+  wait_previous();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int count = 0;
   const int at = row_turn(p, 0, count, counts, blockIdx.x == 0);
   if (at >= 0) list[at] = threadIdx.x;
@@ -909,6 +911,7 @@ __global__ void __launch_bounds__(1024) ce_rows_once_kernel(const __grid_constan
 // More tokens: one block finds the rows, 1024 tokens a turn, and others pack them.
 __global__ void __launch_bounds__(1024) ce_rows_kernel(const __grid_constant__ RowParams p) {
   __shared__ int counts[2][32];
+  wait_previous();
   int base = 0;
   for (int t0 = 0, turn = 0; t0 < p.T; t0 += 1024, turn ^= 1) row_turn(p, t0, base, counts[turn], true);
   row_end(p, base);
@@ -1120,14 +1123,12 @@ cudaError_t launch_few(const void* weight, const void* packed, const CeParams& p
 }
 
 cudaError_t launch_rows(const RowParams& p, int sms, cudaStream_t stream) {
-  if (p.T <= 1024) {
-    ce_rows_once_kernel<<<std::min(p.rows_cap, sms), 1024, 0, stream>>>(p);
-    return cudaGetLastError();
-  }
-  ce_rows_kernel<<<1, 1024, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   void* args[] = {const_cast<RowParams*>(&p)};
+  if (p.T <= 1024)
+    return launch_dependent(reinterpret_cast<const void*>(ce_rows_once_kernel), dim3(std::min(p.rows_cap, sms)), 1024, 0,
+                            stream, args);
+  const cudaError_t e = launch_dependent(reinterpret_cast<const void*>(ce_rows_kernel), dim3(1), 1024, 0, stream, args);
+  if (e != cudaSuccess) return e;
   return launch_dependent(reinterpret_cast<const void*>(ce_pack_kernel), dim3(std::min(p.rows_cap, 8 * sms)), 256, 0,
                           stream, args);
 }
