@@ -29,9 +29,9 @@
 // What bounds it (one GB300): large products the tensor cores under the power cap: forward
 // 2048 x 7168 x 131072 2.29 to 2.37 ms (1.65 PFLOP/s), 4096 x 2048 x 131072 1.38 to 1.45 ms; backward 4096 x 2048 x
 // 131072 3.8 to 4.2 ms, 2.1 to 2.3 PFLOP/s with the logits formed again (8 T V D; what it cannot do without
-// is 6 T V D), 1531 x 1408 x 50021 with 30 % ignored 360 us.  One token: the weight's
-// bytes, 87 us (6.2 TB/s; floor 79), backward 312 us (three times them; floor 237).  Small problems: the
-// chain of launches, about 6 us each beside their work (512 x 256 x 32768: forward 20 us, backward 49 us).
+// is 6 T V D), 1531 x 1408 x 50021 with 30 % ignored 343 us.  One token: the weight's
+// bytes, 88 us (6.1 TB/s; floor 79), backward 298 us (three times them; floor 237).  Small problems: the
+// chain of launches, about 6 us each beside their work (512 x 256 x 32768: forward 19 us, backward 49 us).
 // Larger pieces of the vocabulary are faster (launches, dh's sums): 4096 x 2048 x 131072 in pieces of
 // 16384 entries 4.18 ms, 32768 3.94, 65536 3.79; pieces that stay in L2 are not.
 // Tried without gain: sixteen epilogue warps in the backward's products, L2-sized pieces,
@@ -81,12 +81,19 @@ static_assert(kFewSmem <= 232448, "shared memory per CTA");
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 constexpr float kLowest = -1.0e30f;
 
+// What the parts that the dh product sums apart are chosen from.
+struct DhPlan {
+  int D;
+  int steps;             // stages of the contraction, a piece of the vocabulary
+  int pairs;             // CTA pairs
+  int rows;              // rows of partial sums that the workspace holds, of all parts
+};
+
 struct CeParams {
-  const int* count;      // rows that count
+  const int* count;      // rows that count, parts of dh
   int rows_cap;          // their capacity, a multiple of 256
   int D, V;
   int v0, vn;            // piece of the vocabulary: first, number (backward)
-  int splits;            // dh: parts of the contraction
   int first;             // dh: store (else add)
   float k;               // scale log2 e
   const int* target;     // [rows_cap], -1 past the rows
@@ -132,6 +139,40 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// Parts of the vocabulary that the dh product sums apart, so that its tiles fill
+// the pairs: what takes the least time by a stage's 0.27 us, a tile's 1.5 us
+// around its stages, and the parts' sums at 4 TB/s (written once a piece, read in
+// the end).  Chosen once a call for the rows that count, so on the device; every
+// lane of a warp gets the number (1531 x 1408 x 50021 with 30 % ignored: the product, planned for all
+// tokens, took 137 us).
+__device__ __forceinline__ int dh_parts(const DhPlan& d, int count) {
+  const int rows = (count + kTile - 1) / kTile * kTile, tiles = rows / kTile * ((d.D + kTile - 1) / kTile);
+  const float sums = static_cast<float>(count) * static_cast<float>(d.D) * 2.0e-6f;
+  float least = 3.0e38f;
+  int best = 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = 1 + (threadIdx.x & 31) + 32 * i;
+    const float us = static_cast<float>((tiles * s + d.pairs - 1) / d.pairs) *
+                         (0.27f * static_cast<float>((d.steps + s - 1) / s) + 1.5f) +
+                     static_cast<float>(s) * sums;
+    if (us < least && (s == 1 || (s <= d.steps && static_cast<long long>(s) * rows <= d.rows))) {
+      least = us;
+      best = s;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xFFFFFFFFu, least, o);
+    const int b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+    if (u < least || (u == least && b < best)) {
+      least = u;
+      best = b;
+    }
+  }
+  return best;
+}
+
 // The products' sizes and the order of their tiles.
 template <int KIND>
 struct CeWork {
@@ -146,7 +187,7 @@ struct CeWork {
     k = KIND == kDh ? p.vn : KIND == kDw ? rows : p.D;
     mt = (m + kTile - 1) / kTile;
     nt = (n + kTile - 1) / kTile;
-    splits = KIND == kDh ? p.splits : 1;
+    splits = KIND == kDh ? p.count[1] : 1;
     total = mt * nt * splits;
     split_steps = ((k + kBk - 1) / kBk + splits - 1) / splits;
   }
@@ -572,8 +613,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
                 tma_store_2d(&tmC, ws, cs, row_w);
               } else if constexpr (KIND == kDh) {
                 if (cs < p.D) {
-                  if (p.first) tma_store_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
-                  else tma_reduce_add_2d(&tmC, ws, cs, t.split * p.rows_cap + row_w);
+                  if (p.first) tma_store_2d(&tmC, ws, cs, t.split * w.mt * kTile + row_w);
+                  else tma_reduce_add_2d(&tmC, ws, cs, t.split * w.mt * kTile + row_w);
                 }
               } else {
                 if (cs < p.D) tma_store_2d(&tmC, ws, cs, p.v0 + row_w);
@@ -800,7 +841,8 @@ struct RowParams {
   long long ignore;
   const __nv_bfloat16* h;
   long long ldh;
-  int* count;
+  int* count;            // rows that count, parts of dh
+  DhPlan dh;             // backward
   int* list;             // [rows_cap] token of each packed row, -1 past them
   int* target;           // [rows_cap], -1 past them
   int* inv;              // [T] packed row of each token, -1 (backward)
@@ -860,7 +902,13 @@ __device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, i
 
 // After the last turn: the number of rows, and what stands for none up to a multiple of 256.
 __device__ __forceinline__ void row_end(const RowParams& p, int count) {
-  if (threadIdx.x == 0) *p.count = count;
+  if (threadIdx.x < 32) {
+    const int parts = p.inv ? dh_parts(p.dh, count) : 1;
+    if (threadIdx.x == 0) {
+      p.count[0] = count;
+      p.count[1] = parts;
+    }
+  }
   const int end = (count + kTile - 1) / kTile * kTile;
   for (int i = count + threadIdx.x; i < end; i += 1024) {
     p.list[i] = -1;
@@ -971,11 +1019,11 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* part, const
 
 // dh: the sum of the splits' FP32 rows, rounded; zeros for tokens that do not
 // count.  A thread takes four columns and asks for four splits at a time.
-__global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, int splits, int rows_cap, const int* inv, int T,
-                                                    int D, __nv_bfloat16* dh) {
+__global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, const int* count, const int* inv, int T, int D,
+                                                    __nv_bfloat16* dh) {
   after_previous();
-  const int per = D / 4;
-  const long long all = static_cast<long long>(T) * per, plane = static_cast<long long>(rows_cap) * D;
+  const int n = count[0], splits = count[1], per = D / 4;
+  const long long all = static_cast<long long>(T) * per, plane = static_cast<long long>((n + kTile - 1) / kTile * kTile) * D;
   for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < all; k += static_cast<long long>(gridDim.x) * 256) {
     const int t = static_cast<int>(k / per), c = static_cast<int>(k - static_cast<long long>(t) * per) * 4;
     const int i = inv[t];
@@ -1012,32 +1060,13 @@ bool supported(const moe_linear_ce_config* c) {
   return row_tiles * col_tiles < (1ll << 30);   // tiles are counted in 32 bits
 }
 
-// Parts of the vocabulary that the dh product sums apart, so that its tiles
-// fill the pairs: what takes the least time by a stage's 0.27 us, a tile's 1.5 us around its
-// stages, and the parts' sums at 4 TB/s (written once a piece and read in the end).
-int dh_splits(int T, int D, int64_t piece, int pairs) {
-  const long long tiles = static_cast<long long>((T + kTile - 1) / kTile) * ((D + kTile - 1) / kTile);
-  const long long steps = (piece + kBk - 1) / kBk;
-  int best = 1;
-  double least = 1e30;
-  for (int s = 1; s <= 64 && s <= steps; ++s) {
-    const double rounds = static_cast<double>((tiles * s + pairs - 1) / pairs);
-    const double us = rounds * (0.27 * static_cast<double>((steps + s - 1) / s) + 1.5) +
-                      static_cast<double>(s) * T * D * 8.0 / 4.0e6;
-    if (us < least) {
-      least = us;
-      best = s;
-    }
-  }
-  return best;
-}
-
 // Tokens that the vocabulary-wise forward takes: the weight's bytes bound both,
 // and it moves no others (1 x 2048 x 131072 87 and 103 us, 64 tokens 95 and 107).
 bool few(int T) { return T <= kFew; }
 
 struct Layout {
-  int rows_cap, col_tiles, splits;
+  int rows_cap, col_tiles;
+  int64_t dh_rows;        // of partial sums
   int64_t piece;          // vocabulary entries a piece, a multiple of 256
   size_t count, list, target, inv, lse2, coef, hit, part, packed, g, dh, bytes;
 };
@@ -1051,12 +1080,11 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
   l.rows_cap = (c->tokens + kTile - 1) / kTile * kTile;
   l.col_tiles = (c->vocab + kTile - 1) / kTile;
   l.piece = std::min<int64_t>(piece, static_cast<int64_t>(l.col_tiles) * kTile);
-  // whatever the piece, so that the workspace grows with it alone: by pieces of about 512 MB
-  l.splits = dh_splits(c->tokens, c->d_model,
-                       std::min<int64_t>(c->vocab, std::max(kTile, (256 << 20) / std::max(l.rows_cap, 1))), sms / 2);
+  // 128 MB of partial sums, or one part of all rows
+  l.dh_rows = std::max<int64_t>(l.rows_cap, std::min<int64_t>(64ll * l.rows_cap, (32 << 20) / c->d_model / kTile * kTile));
   const size_t rows = l.rows_cap, D = c->d_model;
   size_t at = 0;
-  l.count = take(&at, 4);
+  l.count = take(&at, 8);
   l.list = take(&at, rows * 4);
   l.target = take(&at, rows * 4);
   l.packed = take(&at, rows * D * 2);
@@ -1064,7 +1092,7 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
     l.inv = take(&at, rows * 4);
     l.lse2 = take(&at, rows * 4);
     l.coef = take(&at, rows * 8);
-    l.dh = take(&at, rows * D * 4 * l.splits);
+    l.dh = take(&at, static_cast<size_t>(l.dh_rows) * D * 4);
     l.g = take(&at, rows * 2 * l.piece);
   } else {
     l.hit = take(&at, rows * 4);
@@ -1160,7 +1188,6 @@ void fill(const moe_linear_ce_config* c, const Layout& l, const void* h, const v
   p->rows_cap = l.rows_cap;
   p->D = c->d_model;
   p->V = c->vocab;
-  p->splits = 1;
   p->k = c->logit_scale * kLog2e;
   p->target = r->target;
   p->err = err;
@@ -1264,7 +1291,7 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
   r.coef = at<float2>(workspace, l.coef);
   p.lse2 = r.lse2;
   p.coef = r.coef;
-  p.splits = l.splits;
+  r.dh = {D, static_cast<int>(l.piece / kBk), sms / 2, static_cast<int>(l.dh_rows)};
   __nv_bfloat16* g = at<__nv_bfloat16>(workspace, l.g);
   float* part = at<float>(workspace, l.dh);
   CUtensorMap hk, hm, wk, wm, gk, gm, gs, ds, os;
@@ -1272,7 +1299,7 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
       !map_2d(&wk, weight, V, D, 128, false) || !map_2d(&wm, weight, V, D, 64, false) ||
       !map_2d(&gk, g, l.rows_cap, l.piece, 128, false) || !map_2d(&gm, g, l.rows_cap, l.piece, 64, false) ||
       !map_2d(&gs, g, l.rows_cap, l.piece, 32, false) ||
-      !map_2d(&os, part, static_cast<int64_t>(l.rows_cap) * l.splits, D, 32, true) ||
+      !map_2d(&os, part, l.dh_rows, D, 32, true) ||
       (dweight && !map_2d(&ds, dweight, V, D, 32, false)))
     return MOE_ERR_CUDA;
   if (launch_rows(r, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
@@ -1283,16 +1310,17 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
     p.first = v0 == 0;
     const long long v_tiles = (p.vn + kTile - 1) / kTile;
     if (launch_gemm<kGrad>(hk, wk, gs, p, sms / 2, row_tiles * v_tiles, stream) != cudaSuccess) return MOE_ERR_CUDA;
-    if (dh && launch_gemm<kDh>(gk, wm, os, p, sms / 2, row_tiles * d_tiles * l.splits, stream) != cudaSuccess)
+    if (dh && launch_gemm<kDh>(gk, wm, os, p, sms / 2, sms / 2, stream) != cudaSuccess)
       return MOE_ERR_CUDA;
     if (dweight && launch_gemm<kDw>(gm, hm, ds, p, sms / 2, v_tiles * d_tiles, stream) != cudaSuccess) return MOE_ERR_CUDA;
   }
   if (dh) {
-    int splits = l.splits, cap = l.rows_cap, t = T, d = D;
+    int t = T, d = D;
     const float* in = part;
     const int* inv = r.inv;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dh);
-    void* args[] = {&in, &splits, &cap, &inv, &t, &d, &out};
+    const int* count = r.count;
+    void* args[] = {&in, &count, &inv, &t, &d, &out};
     if (launch_dependent(reinterpret_cast<const void*>(ce_dh_kernel), dim3(static_cast<unsigned>(std::min<long long>((static_cast<long long>(T) * (D / 4) + 255) / 256, 16 * sms))), 256, 0,
                          stream, args) != cudaSuccess)
       return MOE_ERR_CUDA;
