@@ -5,12 +5,13 @@
 //
 // A thread takes groups of eight elements, which share one block of the
 // generator, one after the other, the next one's loads ahead of this one's mask.
-// What bounds it: 32 x 32 -> 64 bit products take 4 cycles a warp, and 19 of them a
-// group are 76 cycles where BF16's bytes take 70 (16384 x 7168: 77.6 us, 6.05 TB/s;
-// floor 69); in FP32 the stream alone (139 us, 6.76 TB/s).  On the way there, BF16: four groups a
-// thread at a time with 98 registers 133 us (22 % of the warps: products and
-// logic, which run in different pipes, hardly overlapped), the first round's product
-// with the site once a thread, dropped places cleared in the packed words.
+// What bounds it: 32 x 32 -> 64 bit products take 4 cycles a warp, and 19 of them
+// a group are 76 cycles where BF16's bytes take 70 (16384 x 7168: 77 us, 6.1 TB/s;
+// floor 69); in FP32 the stream alone (135 us, 6.9 TB/s).  On the way there, BF16:
+// four groups a thread at a time with 98 registers took 133 us (22 % of the warps:
+// products and logic, which run in different pipes, hardly overlapped); the first
+// round's product with the site is formed once a thread, and dropped places are
+// cleared in the packed words.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -22,9 +23,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-// CTAs an SM at most, of which eight run at a time: a few groups a thread spread the keys'
-// cost, and many CTAs keep the SMs evenly busy (16384 x 7168 in BF16: 8 an SM
-// 79.9 us, 16 78.4, 64 77.6; in FP32 148, 147, 139).
+// CTAs an SM at most, of which six or so run at a time: a few groups a thread
+// spread the keys' cost, and many CTAs keep the SMs evenly busy (16384 x 7168 in
+// BF16: 8 an SM 79.9 us, 16 78.4, 64 77.6; in FP32 148, 147, 139).
 constexpr int kCtas = 64;
 
 struct DropoutParams {
@@ -231,8 +232,8 @@ moe_status moe_dropout(const moe_dropout_config* cfg, const void* x, const void*
   if (sms <= 0) return MOE_ERR_CUDA;
   const long long grid = std::min<long long>((p.groups + kThreads - 1) / kThreads, kCtas * sms);
   void* args[] = {&p};
-  const void* kernel =
-      cfg->type == MOE_TYPE_FP32 ? kernel_of<float>(layout, residual != nullptr) : kernel_of<__nv_bfloat16>(layout, residual != nullptr);
+  const bool res = residual != nullptr;
+  const void* kernel = cfg->type == MOE_TYPE_FP32 ? kernel_of<float>(layout, res) : kernel_of<__nv_bfloat16>(layout, res);
   return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, stream, args) == cudaSuccess ? MOE_OK
                                                                                                               : MOE_ERR_CUDA;
 }

@@ -21,14 +21,19 @@
 // thread copies the pieces it reads itself, so the copies need no barrier).
 // Dropout's mask of the next row is drawn while that row is under way.
 //
-// What bounds it (BF16 with a branch, one GB300): the stream.  Forward 2048 x 7168 21.3 us
-// (5.5 TB/s; floor 17.3), 8192 x 7168 75.5 us (6.2 TB/s); the backward with its second
-// kernel 39.5 us (floor 21.6) and 106 us (5.6 TB/s).  Short inputs add a fixed part (launch, first
-// row, last stores; the backward's column sums and second kernel, 17 us).  Dropout adds the generator's
-// products, 4 cycles a warp each, beside the norm's own arithmetic: forward 27.9 and 90.8 us, backward 48.8 us.
+// What bounds it (BF16 with a branch, one GB300): the stream.  Forward 2048 x 7168
+// 21.4 us (5.5 TB/s; floor 17.3), 8192 x 7168 76 us (6.2 TB/s); the backward with
+// its second kernel 34.3 us (floor 21.6) and 100.5 us (5.8 TB/s).  Short inputs
+// add a fixed part (launch, first row, last stores; the backward's column sums
+// and second kernel, 12 us).  Dropout adds the generator's products, 4 cycles a
+// warp each, beside the norm's own arithmetic: forward 27.8 and 90.5 us, backward
+// 43.6 us.  Odd widths: 16384 x 1411 forward 37 us, with dropout 56, backward 54
+// and 72 (16384 x 1408: forward 31 and 37.6, backward 42.8).
 // Tried and slower: forward rows through a ring too (27.5 us, 88.7 us), 24 warps
-// (80 registers: one row in flight a CTA, 24.7 us), one piece a thread (25.6 us); backward with rows
-// in registers (56 us, spills), 28 warps without a row's normalised values kept (53.7 us).
+// (80 registers: one row in flight a CTA, 24.7 us), one piece a thread (25.6 us);
+// backward with rows in registers (56 us, spills), 28 warps without a row's
+// normalised values kept (53.7 us), column sums that leave element by element
+// (39.2 us).
 //
 // Widths that 8 does not divide: row t starts t D mod 8 elements past a
 // 16-byte boundary.  Each group's rows are a multiple of 8 apart, so for it
@@ -327,7 +332,8 @@ struct Group {
   // elements of the rows beside it, but none past the tensor's end.
   template <typename X>
   __device__ __forceinline__ bool vectors(const Tensor& s, long long row) const {
-    return !ODD || (s.vec && reinterpret_cast<const uint8_t*>(static_cast<const X*>(s.base) + row * s.ld - off + 8 * pieces) <= s.end);
+    const X* end = static_cast<const X*>(s.base) + row * s.ld - off + 8 * pieces;
+    return !ODD || (s.vec && reinterpret_cast<const uint8_t*>(end) <= s.end);
   }
   // Piece c, at src, of a row where they may not.
   template <typename X>
@@ -413,7 +419,8 @@ __device__ __forceinline__ void make_table(const LnParams& p, uint8_t* shared, i
       float v[8];
       if (src && off == 0 && 8 * c + 8 <= p.D) {
         if (p.params_f32) {
-          const float4 a = __ldg(static_cast<const float4*>(src) + 2 * c), b = __ldg(static_cast<const float4*>(src) + 2 * c + 1);
+          const float4 a = __ldg(static_cast<const float4*>(src) + 2 * c);
+          const float4 b = __ldg(static_cast<const float4*>(src) + 2 * c + 1);
           v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         } else {
           const uint4 u = __ldg(static_cast<const uint4*>(src) + c);
@@ -695,7 +702,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
 #pragma unroll
       for (int arr = 0; arr < 2; ++arr) {
         // in the layout's pieces, shifted like the rows
-        float4* out = reinterpret_cast<float4*>(p.partial) + (static_cast<long long>(arr) * gridDim.x + blockIdx.x) * 2 * planes;
+        float4* out = reinterpret_cast<float4*>(p.partial) +
+                      (static_cast<long long>(arr) * gridDim.x + blockIdx.x) * 2 * planes;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const int c = g.piece(i);
@@ -899,7 +907,8 @@ size_t moe_layer_norm_workspace_bytes(const moe_layer_norm_config* cfg) {
   const int sms = device_sms();
   if (sms <= 0) return 0;
   // two arrays of column sums a CTA
-  return 2 * static_cast<size_t>(std::min(cfg->tokens, std::max(8, sms))) * static_cast<size_t>((cfg->d_model + 14) / 8 * 8) * sizeof(float) + 256;
+  const size_t rows = static_cast<size_t>(std::min(cfg->tokens, std::max(8, sms)));
+  return 2 * rows * static_cast<size_t>((cfg->d_model + 14) / 8 * 8) * sizeof(float) + 256;
 }
 
 moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, const void* y, const void* weight, const float* stats,

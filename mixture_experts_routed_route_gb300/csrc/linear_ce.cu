@@ -26,16 +26,18 @@
 // Exponentials are in base 2 with one fused product, exp2(l k - m), k = scale
 // log2 e: the rounding is relative to the small difference.
 //
-// What bounds it (one GB300): large products the tensor cores under the power cap: forward
-// 2048 x 7168 x 131072 2.29 to 2.37 ms (1.65 PFLOP/s), 4096 x 2048 x 131072 1.38 to 1.45 ms; backward 4096 x 2048 x
-// 131072 3.8 to 4.2 ms, 2.1 to 2.3 PFLOP/s with the logits formed again (8 T V D; what it cannot do without
-// is 6 T V D), 1531 x 1408 x 50021 with 30 % ignored 343 us.  One token: the weight's
-// bytes, 88 us (6.1 TB/s; floor 79), backward 298 us (three times them; floor 237).  Small problems: the
-// chain of launches, about 6 us each beside their work (512 x 256 x 32768: forward 19 us, backward 49 us).
-// Larger pieces of the vocabulary are faster (launches, dh's sums): 4096 x 2048 x 131072 in pieces of
-// 16384 entries 4.18 ms, 32768 3.94, 65536 3.79; pieces that stay in L2 are not.
-// Tried without gain: sixteen epilogue warps in the backward's products, L2-sized pieces,
-// rotated starts of the contraction.
+// What bounds it (one GB300).  Large products: the tensor cores under the power
+// cap.  Forward 2048 x 7168 x 131072 2.29 to 2.46 ms (1.6 PFLOP/s), 4096 x 2048 x
+// 131072 1.38 to 1.45 ms; backward 4096 x 2048 x 131072 3.8 to 4.2 ms, 2.1 to 2.3
+// PFLOP/s with the logits formed again (8 T V D; what it cannot do without is 6 T
+// V D), 1531 x 1408 x 50021 with 30 % ignored 343 us.  One token: the weight's
+// bytes, 88 us (6.1 TB/s; floor 79), backward 298 us (three times them; floor
+// 237).  Small problems: the chain of launches, 6 to 9 us each beside their work
+// (512 x 256 x 32768: forward 19 us, backward 49 us).
+// Larger pieces of the vocabulary are faster (launches, dh's sums): 4096 x 2048 x
+// 131072 in pieces of 16384 entries 4.18 ms, 32768 3.94, 65536 3.79; pieces that
+// stay in L2 are not.  Tried without gain: sixteen epilogue warps in the
+// backward's products, rotated starts of the contraction.
 //
 // Warp roles: warp 0 TMA producer, warp 1 TMEM allocation and (rank 0) MMA
 // issue for the pair, the other 8 or 16 epilogue (lane quadrant w % 4, a part of
@@ -69,9 +71,9 @@ struct CeCfg {
 constexpr int kGroup = 8;          // row tiles that share the columns' operand before the next ones
 // Stages that the forward's accumulators sum before a new sum begins, in
 // registers: 1024 elements.  The tensor cores cut off, not round, at each of
-// their additions, so a logit of 7168 elements is low by 7.5e-6 of itself in one sum, by
-// 1.0e-6 in seven (8 stages a sum: 0.5e-6, but reading the accumulators twice as often costs
-// 4 % of the product; one sum: 3 % faster).
+// their additions, so a logit of 7168 elements is low by 7.5e-6 of itself in one
+// sum, by 1.0e-6 in seven (8 stages a sum: 0.5e-6, but reading the accumulators
+// twice as often costs 4 % of the product; one sum: 3 % faster).
 constexpr int kSegment = 16;
 // Few tokens: at most 64, 32 a group of four epilogue warps.
 constexpr int kFew = 64;
@@ -143,8 +145,8 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 // the pairs: what takes the least time by a stage's 0.27 us, a tile's 1.5 us
 // around its stages, and the parts' sums at 4 TB/s (written once a piece, read in
 // the end).  Chosen once a call for the rows that count, so on the device; every
-// lane of a warp gets the number (1531 x 1408 x 50021 with 30 % ignored: the product, planned for all
-// tokens, took 137 us).
+// lane of a warp gets the number (1531 x 1408 x 50021 with 30 % ignored: the
+// product planned for all tokens took 137 us, the call 358 instead of 343).
 __device__ __forceinline__ int dh_parts(const DhPlan& d, int count) {
   const int rows = (count + kTile - 1) / kTile * kTile, tiles = rows / kTile * ((d.D + kTile - 1) / kTile);
   const float sums = static_cast<float>(count) * static_cast<float>(d.D) * 2.0e-6f;
@@ -464,8 +466,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
       const int row = t.row0 + 128 * rank + 32 * q + lane;     // this thread's
       const int row_w = row - lane;
       const int cols = t.n / (E / 4), c0 = t.col0 + h * cols;  // this warp's columns
-      // Whether anything reads this warp's rows: those that count; of g, which the dW product reads 64 rows at a time, those
-      // up to a multiple of 64; of dW, the vocabulary's.
+      // Whether anything reads this warp's rows: those that count; of g, which the dW product reads 64 rows at a
+      // time, those up to a multiple of 64; of dW, the vocabulary's.
       const bool live = KIND == kDw ? p.v0 + row_w < p.V : row_w < (KIND == kGrad ? (w.m + 63) / 64 * 64 : w.m);
       // what the rows need, asked for a tile ahead
       const int target = next.target - (KIND == kGrad ? p.v0 : 0);
@@ -638,11 +640,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
 // Forward of at most N tokens: the vocabulary's rows are the products' rows, so
 // that the tensor cores take N columns instead of 256 and what is left is the
 // weight's one way from HBM.  A stage takes 512 bytes of a row at a time: with
-// 128, the rows' neighbouring lines are asked for too far apart for HBM's pages (1 x 2048 x
-// 131072 98.5 us, with 256 86.4, with 512 86.3).  Each CTA has a run of 32-row units, worked through
-// in tiles of 128 rows (the last one shorter, and no row loaded twice); a
-// thread keeps, for its place in the tiles, each token's running maximum and
-// sum of exponentials, which lanes exchange once at the end.
+// 128, the rows' neighbouring lines are asked for too far apart for HBM's pages
+// (1 x 2048 x 131072 98.5 us, with 256 86.4, with 512 86.3).  Each CTA has a run
+// of 32-row units, worked through in tiles of 128 rows (the last one shorter, and
+// no row loaded twice); a thread keeps, for its place in the tiles, each token's
+// running maximum and sum of exponentials, which lanes exchange once at the end.
 template <int N>
 __global__ void __launch_bounds__(64 + 4 * N, 1)
     ce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, const CeParams p) {
@@ -720,7 +722,8 @@ __global__ void __launch_bounds__(64 + 4 * N, 1)
           if (it >= static_cast<uint32_t>(ahead)) load_w(tile, ks, slot);
 #pragma unroll
           for (int j = 0; j < kFewSteps; ++j)
-            tma_load_2d(smem + slot * kBytes + kFewSteps * kOperand + j * kStep, &tmH, &full[slot], (ks * kFewSteps + j) * kBk, 0);
+            tma_load_2d(smem + slot * kBytes + kFewSteps * kOperand + j * kStep, &tmH, &full[slot],
+                        (ks * kFewSteps + j) * kBk, 0);
         }
         __syncwarp();
       }
@@ -944,7 +947,8 @@ __device__ __forceinline__ void pack_row(const RowParams& p, int i, int t) {
 // Up to 1024 tokens: every block finds the rows that count, the first writes them down, and all pack them.
 __global__ void __launch_bounds__(1024) ce_rows_once_kernel(const __grid_constant__ RowParams p) {
   __shared__ int counts[32], list[1024];
-  // in this order: the forward of few tokens reads the weight before its own wait, and everything before this call has ended then
+  // in this order: the forward of few tokens reads the weight before its own wait, and whatever ran before this call
+  // has ended then
   wait_previous();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int count = 0;
@@ -1024,7 +1028,8 @@ __global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, const int
   after_previous();
   const int n = count[0], splits = count[1], per = D / 4;
   const long long all = static_cast<long long>(T) * per, plane = static_cast<long long>((n + kTile - 1) / kTile * kTile) * D;
-  for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < all; k += static_cast<long long>(gridDim.x) * 256) {
+  const long long hop = static_cast<long long>(gridDim.x) * 256;
+  for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < all; k += hop) {
     const int t = static_cast<int>(k / per), c = static_cast<int>(k - static_cast<long long>(t) * per) * 4;
     const int i = inv[t];
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1034,12 +1039,14 @@ __global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, const int
         float4 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          v[j] = s + j < splits ? *reinterpret_cast<const float4*>(q + (s + j) * plane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          v[j] = s + j < splits ? *reinterpret_cast<const float4*>(q + (s + j) * plane)
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) a.x += v[j].x, a.y += v[j].y, a.z += v[j].z, a.w += v[j].w;
       }
     }
-    *reinterpret_cast<uint2*>(dh + static_cast<long long>(t) * D + c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    *reinterpret_cast<uint2*>(dh + static_cast<long long>(t) * D + c) =
+        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   }
 }
 
@@ -1128,8 +1135,9 @@ cudaError_t launch_gemm_as(const CUtensorMap& a, const CUtensorMap& b, const CUt
                           args);
 }
 // Sixteen epilogue warps where the forward's product is too short to hide eight
-// warps' exponentials and takes one segment (512 x 256 x 32768 22.8 and 20.2 us, 4096 x 512 x
-// 65536 224 and 210, 4096 x 1024 x 65536 373 and 366).  The backward's first product gained nothing.
+// warps' exponentials and takes one segment (512 x 256 x 32768 22.8 and 20.2 us,
+// 4096 x 512 x 65536 224 and 210, 4096 x 1024 x 65536 373 and 366).  The
+// backward's first product gained nothing.
 template <int KIND>
 cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
                         long long tiles, cudaStream_t stream) {
@@ -1141,11 +1149,12 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtens
 template <int N>
 cudaError_t launch_few(const void* weight, const void* packed, const CeParams& p, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
-  cudaError_t e =
-      once.once([&] { return cudaFuncSetAttribute(ce_few_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem); });
+  cudaError_t e = once.once(
+      [&] { return cudaFuncSetAttribute(ce_few_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem); });
   if (e != cudaSuccess) return e;
   CUtensorMap w, h;
-  if (!map_2d(&w, weight, p.V, p.D, 32, false) || !map_2d(&h, packed, p.rows_cap, p.D, N, false)) return cudaErrorInvalidValue;
+  if (!map_2d(&w, weight, p.V, p.D, 32, false) || !map_2d(&h, packed, p.rows_cap, p.D, N, false))
+    return cudaErrorInvalidValue;
   void* args[] = {&w, &h, const_cast<CeParams*>(&p)};
   return launch_dependent(reinterpret_cast<const void*>(ce_few_kernel<N>), dim3(sms), 64 + 4 * N, kFewSmem, stream, args);
 }
@@ -1251,8 +1260,8 @@ moe_status moe_linear_ce_forward(const moe_linear_ce_config* cfg, const void* h,
   const int* count = r.count;
   int cap = l.rows_cap;
   void* args[] = {&part, &hit, &list, &count, &parts, &cap, &k, &z, &loss, &lse};
-  if (launch_dependent(reinterpret_cast<const void*>(ce_join_kernel), dim3((cfg->tokens + 31) / 32), 1024, 0, stream, args) !=
-      cudaSuccess)
+  if (launch_dependent(reinterpret_cast<const void*>(ce_join_kernel), dim3((cfg->tokens + 31) / 32), 1024, 0, stream,
+                       args) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }
@@ -1321,8 +1330,10 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dh);
     const int* count = r.count;
     void* args[] = {&in, &count, &inv, &t, &d, &out};
-    if (launch_dependent(reinterpret_cast<const void*>(ce_dh_kernel), dim3(static_cast<unsigned>(std::min<long long>((static_cast<long long>(T) * (D / 4) + 255) / 256, 16 * sms))), 256, 0,
-                         stream, args) != cudaSuccess)
+    const long long blocks = (static_cast<long long>(T) * (D / 4) + 255) / 256;
+    if (launch_dependent(reinterpret_cast<const void*>(ce_dh_kernel),
+                         dim3(static_cast<unsigned>(std::min<long long>(blocks, 16 * sms))), 256, 0, stream,
+                         args) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
   return MOE_OK;
