@@ -19,7 +19,8 @@
 // row's own values have been used.  The backward, whose registers hold the
 // column sums, has its rows in flight in a ring in shared memory (cp.async; a
 // thread copies the pieces it reads itself, so the copies need no barrier).
-// Dropout's mask of the next row is drawn while that row is under way.
+// Dropout's mask of the next row is drawn while that row is under way; in the
+// backward, where a row's group leaves warps of its CTA over, by those.
 //
 // What bounds it (BF16 with a branch, one GB300): the stream.  Forward 2048 x 7168
 // 21.4 us (5.5 TB/s; floor 17.3), 8192 x 7168 76 us (6.2 TB/s); the backward with
@@ -27,13 +28,15 @@
 // add a fixed part (launch, first row, last stores; the backward's column sums
 // and second kernel, 12 us).  Dropout adds the generator's products, 4 cycles a
 // warp each, beside the norm's own arithmetic: forward 27.8 and 90.5 us, backward
-// 43.6 us.  Odd widths: 16384 x 1411 forward 37 us, with dropout 56, backward 54
+// 36.3 and 111 us.  Odd widths: 16384 x 1411 forward 37 us, with dropout 56, backward 54
 // and 72 (16384 x 1408: forward 31 and 37.6, backward 42.8).
 // Tried and slower: forward rows through a ring too (27.5 us, 88.7 us), 24 warps
 // (80 registers: one row in flight a CTA, 24.7 us), one piece a thread (25.6 us);
 // backward with rows in registers (56 us, spills), 28 warps without a row's
 // normalised values kept (53.7 us), column sums that leave element by element
-// (39.2 us).
+// (39.2 us); masks by warps of their own in the forward, which then has 64
+// registers (28.9 us), in the backward as finished words instead of raw numbers,
+// or for half of a row (40.3 and 42.5 us).
 //
 // Widths that 8 does not divide: row t starts t D mod 8 elements past a
 // 16-byte boundary.  Each group's rows are a multiple of 8 apart, so for it
@@ -73,6 +76,8 @@ struct LnParams {
   int T, D;
   int warps, groups;
   int stages, slot;      // backward: rows in flight per group, bytes of one
+  int drawers;           // backward: warps that draw the masks of the others' rows
+  int masks;             // where these are in shared memory, in bytes
   Tensor x, o, dy, dh;   // forward: x, branch; backward: x is y
   Tensor out0;           // y; dx
   Tensor out1;           // h; dbranch
@@ -246,6 +251,7 @@ template <int P, bool ODD>
 struct Group {
   const LnParams& p;
   int grp, wig, nt, t, bar;
+  int members;            // threads that meet at the barrier of sum_two
   int off, pieces;        // of its rows
   float* red;
   int turn = 0;
@@ -254,7 +260,7 @@ struct Group {
     const int warp = threadIdx.x >> 5;
     grp = warp / p.warps;
     wig = warp - grp * p.warps;
-    nt = p.warps * 32;
+    nt = members = p.warps * 32;
     t = threadIdx.x - grp * nt;
     bar = 1 + grp;
     red = red_all[grp];
@@ -323,7 +329,7 @@ struct Group {
     float* r = red + turn;
     turn ^= 64;
     if ((threadIdx.x & 15) == 0) r[2 * (threadIdx.x & 16) + wig] = v;
-    named_bar_sync(bar, nt);
+    named_bar_sync(bar, members);
     a = warp_sums(r);
     b = warp_sums(r + 32);
   }
@@ -395,6 +401,15 @@ struct Group {
     for (int i = 0; i < P; ++i) m[i] = keep_words(p.drop, philox(key, group0 + piece(i)));
   }
 };
+
+// Thread t of n draws its share of a row's mask: the generator's blocks as they
+// are, which the row's own threads compare with the threshold.
+__device__ __forceinline__ void draw_row(const LnParams& p, const PhiloxKey<true>& key, long long row, int pieces, int t,
+                                         int n, uint4* masks) {
+  const unsigned long long group0 = static_cast<unsigned long long>(row * p.D) >> 3;
+#pragma unroll 7
+  for (int c = t; c < pieces; c += n) masks[c] = philox(key, group0 + c);
+}
 
 // The columns' factors, one FP32 plane for each half of a piece (so that a
 // warp's 16-byte reads meet no bank twice): factor `which`, half of piece c.
@@ -598,7 +613,10 @@ struct Ring {
 };
 
 // ALL: dy is there, dx and dbranch are wanted (the common call).
-template <typename R, int P, bool ODD, bool DROP, bool ALL>
+// APART: one group, and the warps that it leaves draw the masks.  The mask of its
+// k-th row is in buffer k mod 2 when the group meets at that row's sums; the
+// buffer is written again after the next row's meeting, by which it was read.
+template <typename R, int P, bool ODD, bool DROP, bool ALL, bool APART = false>
 __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) float red_all[kMaxGroups][128];
@@ -607,7 +625,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
   const int planes = (p.D + 7 + (ODD ? 7 : 0)) >> 3;
   const long long step = static_cast<long long>(gridDim.x) * p.groups;
   long long row = g.grp * gridDim.x + blockIdx.x;
-  Ring<R, P, ODD, ALL> ring(p, g, shared + planes * 32, planes, row, step);
+  uint4* const first_mask = reinterpret_cast<uint4*>(shared + p.masks);
+  uint4* masks = first_mask;
+  const bool drawer = APART && g.grp > 0;
+  Ring<R, P, ODD, ALL> ring(p, g, shared + planes * 32, planes, drawer ? p.T : row, step);
   float mean = 0.0f, r = 0.0f;
   if (row < p.T) {
     mean = p.stats[row];
@@ -615,11 +636,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
   }
   PhiloxKey<false> key{};
   uint4 keep[P];
-  if (DROP) {
+  if (DROP && !APART) {
     key = philox_key<false>(p.drop);
     g.draw(key, row, keep);
   }
-  make_table<1>(p, shared, g.off, g.pieces, planes);
+  if (APART) g.members += 32 * p.drawers;
+  if (drawer) {
+    const PhiloxKey<true> all = philox_key<true>(p.drop);
+    const int t = threadIdx.x - 32 * p.warps, n = 32 * p.drawers;
+    row = blockIdx.x;
+    draw_row(p, all, row, g.pieces, t, n, masks);
+    make_table<1>(p, shared, g.off, g.pieces, planes);
+    for (int k = 1; row < p.T; ++k) {
+      named_bar_sync(1, g.members);
+      row += step;
+      if (row < p.T) draw_row(p, all, row, g.pieces, t, n, masks + (k & 1) * planes);
+    }
+  } else {
+    make_table<1>(p, shared, g.off, g.pieces, planes);
+  }
   const float inv_d = 1.0f / static_cast<float>(p.D), beta = p.beta * p.drop.scale;
   Pair sw[P][4], sb[P][4];   // sums over the group's rows of dh n and dh
 #pragma unroll
@@ -687,12 +722,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
       if (ALL || p.out1.base) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[j] = mul2(s[j], both(beta));
+        if (APART) keep[i] = keep_words(p.drop, masks[c]);
         if (DROP) g.store(p.out1, row, c, s, keep[i]);
         else g.template store<__nv_bfloat16>(p.out1, row, c, s);
       }
     }
     ring.send();
-    if (DROP) g.draw(key, row + step, keep);   // while the next row is on its way
+    if (APART) masks = first_mask + (masks == first_mask ? planes : 0);
+    if (DROP && !APART) g.draw(key, row + step, keep);   // while the next row is on its way
   }
   cp_wait<0>();
   __syncthreads();   // the rows' memory is free: it takes the groups' sums
@@ -796,6 +833,7 @@ struct Shape {
   int pieces, ctas, threads;
   int row_pieces;      // pieces of a row, at most
   bool odd;
+  bool apart;          // the masks are drawn by warps of their own
   size_t smem;
 };
 
@@ -820,14 +858,22 @@ Shape place(LnParams* p, bool fwd, int esz, int sms) {
   // no more groups than save a round of rows
   const int rounds = (p->T - 1) / (sms * most) + 1;
   p->groups = (p->T - 1) / (sms * rounds) + 1;
-  s.threads = p->warps * p->groups * 32;
+  // Backward with dropout where a single group leaves warps over: these draw the masks (2048 x 7168, two warps: 43.3 and
+  // 36.3 us, 150 rows 10.4 and 9.9; 4096 x 4352, seven: 56 and 46; one warp is not enough: 4096 x 7680 75 and 89).
+  const int spare = kBwdThreads / 32 - p->warps;
+  s.apart = !fwd && p->drop.rng && !s.odd && s.pieces == 2 && p->groups == 1 && p->warps > 1 && spare >= 2 &&
+            p->dy.base && p->out0.base && p->out1.base;
+  p->drawers = s.apart ? spare : 0;
+  s.threads = (p->warps * p->groups + p->drawers) * 32;
   // a group's rows have to be a multiple of 8 apart
   s.ctas = !ragged || p->T <= sms ? std::min(sms, p->T) : std::max(8, sms / 8 * 8);
   // the columns' factors; backward: the rows in flight, whose place the groups' sums take
   s.smem = 2 * all * 32;
   if (!fwd) {
-    p->stages = std::max(1, std::min(4, room / (p->groups * p->slot)));
-    s.smem = all * 32 + std::max(p->groups > 1 ? all * 64 : 0, p->groups * p->stages * p->slot);
+    const int masks = s.apart ? 2 * all * 16 : 0;
+    p->stages = std::max(1, std::min(4, (room - masks) / (p->groups * p->slot)));
+    p->masks = all * 32 + std::max(p->groups > 1 ? all * 64 : 0, p->groups * p->stages * p->slot);
+    s.smem = p->masks + masks;
   }
   return s;
 }
@@ -847,6 +893,10 @@ cudaError_t launch_as(bool fwd, const Shape& s, const LnParams& p, cudaStream_t 
   if (fwd)
     return p.o.base && p.out0.base ? launch(layer_norm_fwd_kernel<R, P, ODD, DROP, true>, f_all, s, p, stream)
                                    : launch(layer_norm_fwd_kernel<R, P, ODD, DROP, false>, f, s, p, stream);
+  if constexpr (P == 2 && !ODD && DROP) {
+    static PerDeviceOnce b_apart;
+    if (s.apart) return launch(layer_norm_bwd_kernel<R, P, ODD, DROP, true, true>, b_apart, s, p, stream);
+  }
   return p.dy.base && p.out0.base && p.out1.base ? launch(layer_norm_bwd_kernel<R, P, ODD, DROP, true>, b_all, s, p, stream)
                                                  : launch(layer_norm_bwd_kernel<R, P, ODD, DROP, false>, b, s, p, stream);
 }

@@ -127,6 +127,25 @@ def test_forward_and_backward(T, D, res, p):
         c.check_backward(y, block.layer_norm_backward(y, stats_of(y), c.dh, c.dy, **c.kw))
 
 
+@pytest.mark.parametrize("p", [0.3, 1.0])
+@pytest.mark.parametrize("res", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,D", [(7, 1024), (90, 4160), (305, 4104), (457, 5120), (609, 6152), (700, 7168), (500, 7176)])
+def test_rows_of_one_group_a_cta(T, D, res, p):
+    """Masks that go on from row to row, also between two calls whose generators differ."""
+    from mixture_experts_routed_route_gb300 import block
+    c = Case(T, D, res, torch.float32, p=p, pads=(0, 8, 0, 8, 0), seed=T)
+    stats = torch.empty((2, T), device="cuda")
+    y, h = block.layer_norm(c.x, c.branch, eps=EPS, stats=stats, **c.kw)
+    c.check_forward(y, h, stats)
+    st = stats_of(y)
+    grads = block.layer_norm_backward(y, st, c.dh, c.dy, **c.kw)
+    c.check_backward(y, grads)
+    other = dict(c.kw, site=SITE + 1)
+    block.layer_norm_backward(y, st, c.dh, c.dy, **other)
+    again = block.layer_norm_backward(y, st, c.dh, c.dy, **c.kw)
+    assert all(torch.equal(i, j) for i, j in zip(grads, again))
+
+
 @pytest.mark.parametrize("T,D", [(9, 72), (9, 75), (200, 2048)])
 def test_parts_left_out(T, D):
     """No branch, no weight, no bias, no dy, outputs of the caller's, rows of wider tensors."""
