@@ -19,24 +19,25 @@
 // row's own values have been used.  The backward, whose registers hold the
 // column sums, has its rows in flight in a ring in shared memory (cp.async; a
 // thread copies the pieces it reads itself, so the copies need no barrier).
-// Dropout's mask of the next row is drawn while that row is under way; in the
-// backward, where a row's group leaves warps of its CTA over, by those.
+// Dropout's mask of the next row is drawn while that row is under way; where a
+// wide row's group leaves warps of its CTA over, by those.
 //
 // What bounds it (BF16 with a branch, one GB300): the stream.  Forward 2048 x 7168
 // 21.4 us (5.5 TB/s; floor 17.3), 8192 x 7168 76 us (6.2 TB/s); the backward with
 // its second kernel 34.3 us (floor 21.6) and 100.5 us (5.8 TB/s).  Short inputs
 // add a fixed part (launch, first row, last stores; the backward's column sums
 // and second kernel, 12 us).  Dropout adds the generator's products, 4 cycles a
-// warp each, beside the norm's own arithmetic: forward 27.8 and 90.5 us, backward
-// 36.3 and 111 us.  Odd widths: 16384 x 1411 forward 37 us, with dropout 56, backward 54
+// warp each, beside the norm's own arithmetic: forward 26.3 and 92 us, backward
+// 36.5 and 112 us.  Odd widths: 16384 x 1411 forward 37 us, with dropout 56, backward 54
 // and 72 (16384 x 1408: forward 31 and 37.6, backward 42.8).
 // Tried and slower: forward rows through a ring too (27.5 us, 88.7 us), 24 warps
 // (80 registers: one row in flight a CTA, 24.7 us), one piece a thread (25.6 us);
 // backward with rows in registers (56 us, spills), 28 warps without a row's
 // normalised values kept (53.7 us), column sums that leave element by element
-// (39.2 us); masks by warps of their own in the forward, which then has 64
-// registers (28.9 us), in the backward as finished words instead of raw numbers,
-// or for half of a row (40.3 and 42.5 us).
+// (39.2 us); masks drawn apart for two groups in the forward, which leaves
+// 64 registers (28.9 us), with two or three rows in flight (27.2, 28.8 us), in the
+// backward as finished words instead of raw numbers, or for half of a row (40.3
+// and 42.5 us).
 //
 // Widths that 8 does not divide: row t starts t D mod 8 elements past a
 // 16-byte boundary.  Each group's rows are a multiple of 8 apart, so for it
@@ -64,6 +65,7 @@ constexpr int kMaxCols = 8192;
 constexpr int fwd_threads(bool odd, bool drop) { return odd && drop ? 512 : 896; }
 constexpr int kBwdThreads = 512;   // 128 registers: the column sums and a row's normalised values stay in them
 constexpr int kMaxGroups = 15;     // named barriers 1 .. 15
+constexpr int kSecondBarrier = 8;  // of one group's second sum, where it shares that with the warps that draw
 
 struct Tensor {
   void* base;      // NULL: not there
@@ -76,7 +78,7 @@ struct LnParams {
   int T, D;
   int warps, groups;
   int stages, slot;      // backward: rows in flight per group, bytes of one
-  int drawers;           // backward: warps that draw the masks of the others' rows
+  int drawers;           // warps that draw the masks of the others' rows
   int masks;             // where these are in shared memory, in bytes
   Tensor x, o, dy, dh;   // forward: x, branch; backward: x is y
   Tensor out0;           // y; dx
@@ -293,8 +295,9 @@ struct Group {
   }
 
   // Sums over the group in a fixed order: an xor tree in each warp, then a tree
-  // over the warps.  `red` holds two turns of 2 x 32 floats (zeros past the
-  // warps), so one barrier a sum is enough.
+  // over the warps.  `count` threads meet at the barrier `id`.
+  // `red` holds two turns of 2 x 32 floats (zeros past the warps), so one barrier
+  // a sum is enough.
   __device__ __forceinline__ float warp_sums(const float* r) const {
     const float4* q = reinterpret_cast<const float4*>(r);
     float s = (q[0].x + q[0].y) + (q[0].z + q[0].w);
@@ -305,16 +308,17 @@ struct Group {
            (((q[6].x + q[6].y) + (q[6].z + q[6].w)) + ((q[7].x + q[7].y) + (q[7].z + q[7].w)));
     return s;
   }
-  __device__ __forceinline__ float sum(float v) {
+  __device__ __forceinline__ float sum(float v, int id, int count) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (p.warps == 1) return v;
     float* r = red + turn;
     turn ^= 64;
     if ((threadIdx.x & 31) == 0) r[wig] = v;
-    named_bar_sync(bar, nt);
+    named_bar_sync(id, count);
     return warp_sums(r);
   }
+  __device__ __forceinline__ float sum(float v) { return sum(v, bar, nt); }
   // Two at once: the lower half of a warp carries a, the upper half b.
   __device__ __forceinline__ void sum_two(float& a, float& b) {
     const bool upper = threadIdx.x & 16;
@@ -459,14 +463,33 @@ __device__ __forceinline__ void make_table(const LnParams& p, uint8_t* shared, i
 // ALL: a branch is there and y is written (the common call): a test around a
 // row's loads or stores keeps the compiler from moving anything past it, which
 // costs 17 % (8192 x 7168 without dropout: 72.9 and 84.1 us).
-template <typename R, int P, bool ODD, bool DROP, bool ALL>
-__global__ void __launch_bounds__(fwd_threads(ODD, DROP), 1) layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
+// APART: one group, and other warps draw the masks.  That of its k-th row is in
+// buffer k mod 2 when the group meets at the second sum of the row before; the
+// buffer is written again after the meeting of row k itself, by which it was read.
+template <typename R, int P, bool ODD, bool DROP, bool ALL, bool APART = false>
+__global__ void __launch_bounds__(fwd_threads(ODD || APART, DROP), 1)
+    layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) float red_all[kMaxGroups][128];
   Group<P, ODD> g(p, red_all);
   wait_previous();
   const int planes = (p.D + 7 + (ODD ? 7 : 0)) >> 3;
   const long long step = static_cast<long long>(gridDim.x) * p.groups;
+  uint4* const first_mask = reinterpret_cast<uint4*>(shared + p.masks);
+  if (APART && g.grp > 0) {
+    const PhiloxKey<true> key = philox_key<true>(p.drop);
+    const int t = threadIdx.x - 32 * p.warps, n = 32 * p.drawers;
+    long long row = blockIdx.x;
+    draw_row(p, key, row, g.pieces, t, n, first_mask);
+    make_table<2>(p, shared, g.off, g.pieces, planes);
+    for (int k = 1; row < p.T; ++k) {
+      row += step;
+      if (row < p.T) draw_row(p, key, row, g.pieces, t, n, first_mask + (k & 1) * planes);
+      named_bar_sync(kSecondBarrier, g.nt + n);
+    }
+    return;
+  }
+  const uint4* masks = first_mask;
   long long row = g.grp * gridDim.x + blockIdx.x;
   const bool has_o = ALL || p.o.base != nullptr;
   Raw<R> x[P];
@@ -477,7 +500,7 @@ __global__ void __launch_bounds__(fwd_threads(ODD, DROP), 1) layer_norm_fwd_kern
     if (has_o) g.load(p.o, row, o);
   }
   PhiloxKey<false> key{};
-  if (DROP) {
+  if (DROP && !APART) {
     key = philox_key<false>(p.drop);
     g.draw(key, row, keep);
   }
@@ -495,6 +518,7 @@ __global__ void __launch_bounds__(fwd_threads(ODD, DROP), 1) layer_norm_fwd_kern
       for (int j = 0; j < 4; ++j) y[i][j] = mul2(y[i][j], both(p.alpha));
       if (has_o) {
         Pair b[4];
+        if (APART) keep[i] = keep_words(p.drop, masks[g.piece(i)]);
         if (DROP) o[i].keep(keep[i]);
         o[i].get(b);
 #pragma unroll
@@ -524,7 +548,8 @@ __global__ void __launch_bounds__(fwd_threads(ODD, DROP), 1) layer_norm_fwd_kern
 #pragma unroll
       for (int j = 0; j < 4; ++j) s = fma2(y[i][j], y[i][j], s);
     }
-    const float r = inv_sqrt(fmaf(g.sum(sum2(s)), inv_d, p.eps));
+    const float var = APART ? g.sum(sum2(s), kSecondBarrier + g.grp, g.nt + 32 * p.drawers) : g.sum(sum2(s));
+    const float r = inv_sqrt(fmaf(var, inv_d, p.eps));
     if (p.stats && g.t == 0) {
       p.stats[row] = mean;
       p.stats[p.T + row] = r;
@@ -540,7 +565,8 @@ __global__ void __launch_bounds__(fwd_threads(ODD, DROP), 1) layer_norm_fwd_kern
       for (int j = 0; j < 4; ++j) w[j] = fma2(mul2(y[i][j], both(r)), w[j], b[j]);
       g.template store<__nv_bfloat16>(p.out1, row, c, w);
     }
-    if (DROP) g.draw(key, row + step, keep);   // while the next row is on its way
+    if (APART) masks = first_mask + (masks == first_mask ? planes : 0);
+    if (DROP && !APART) g.draw(key, row + step, keep);   // while the next row is on its way
   }
 }
 
@@ -628,6 +654,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
   uint4* const first_mask = reinterpret_cast<uint4*>(shared + p.masks);
   uint4* masks = first_mask;
   const bool drawer = APART && g.grp > 0;
+  if (APART) g.members += 32 * p.drawers;
   Ring<R, P, ODD, ALL> ring(p, g, shared + planes * 32, planes, drawer ? p.T : row, step);
   float mean = 0.0f, r = 0.0f;
   if (row < p.T) {
@@ -640,7 +667,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) layer_norm_bwd_kernel(const __
     key = philox_key<false>(p.drop);
     g.draw(key, row, keep);
   }
-  if (APART) g.members += 32 * p.drawers;
   if (drawer) {
     const PhiloxKey<true> all = philox_key<true>(p.drop);
     const int t = threadIdx.x - 32 * p.warps, n = 32 * p.drawers;
@@ -858,19 +884,25 @@ Shape place(LnParams* p, bool fwd, int esz, int sms) {
   // no more groups than save a round of rows
   const int rounds = (p->T - 1) / (sms * most) + 1;
   p->groups = (p->T - 1) / (sms * rounds) + 1;
-  // Backward with dropout where a single group leaves warps over: these draw the masks (2048 x 7168, two warps: 43.3 and
-  // 36.3 us, 150 rows 10.4 and 9.9; 4096 x 4352, seven: 56 and 46; one warp is not enough: 4096 x 7680 75 and 89).
-  const int spare = kBwdThreads / 32 - p->warps;
-  s.apart = !fwd && p->drop.rng && !s.odd && s.pieces == 2 && p->groups == 1 && p->warps > 1 && spare >= 2 &&
-            p->dy.base && p->out0.base && p->out1.base;
+  // Dropout where a row takes so many of 16 warps that the CTA has one group, but leaves two: these draw the masks.
+  // Backward 2048 x 7168, two warps: 43.3 and 36.5 us, 150 rows 10.4 and 9.9; 4096 x 4352, seven: 56 and 46; one warp is
+  // not enough: 4096 x 7680 75 and 89.  Forward, which has two groups otherwise: 2048 x 7168 27.4 and 26.3 us, 300 rows 8.0
+  // and 6.3, 8192 90.4 and 91.8, 4096 x 6144 both 42.6, 4096 x 5120 37.6 and 38.7; FP32 4096 x 7168 67.0 and 60.9, 4096 x
+  // 5120 50.3 and 48.5, 4096 x 4352 41.2 and 42.6.
+  const int spare = 16 - p->warps;
+  s.apart = p->drop.rng && !s.odd && s.pieces == 2 && spare >= 2 && p->out0.base &&
+            (fwd ? p->o.base && p->warps > (esz == 4 ? 9 : 12)
+                 : p->warps > 1 && p->groups == 1 && p->dy.base && p->out1.base);
+  if (s.apart) p->groups = 1;
   p->drawers = s.apart ? spare : 0;
   s.threads = (p->warps * p->groups + p->drawers) * 32;
   // a group's rows have to be a multiple of 8 apart
   s.ctas = !ragged || p->T <= sms ? std::min(sms, p->T) : std::max(8, sms / 8 * 8);
   // the columns' factors; backward: the rows in flight, whose place the groups' sums take
-  s.smem = 2 * all * 32;
+  const int masks = s.apart ? 2 * all * 16 : 0;
+  p->masks = 2 * all * 32;
+  s.smem = p->masks + masks;
   if (!fwd) {
-    const int masks = s.apart ? 2 * all * 16 : 0;
     p->stages = std::max(1, std::min(4, (room - masks) / (p->groups * p->slot)));
     p->masks = all * 32 + std::max(p->groups > 1 ? all * 64 : 0, p->groups * p->stages * p->slot);
     s.smem = p->masks + masks;
@@ -890,13 +922,15 @@ cudaError_t launch(K kernel, PerDeviceOnce& once, const Shape& s, const LnParams
 template <typename R, int P, bool ODD, bool DROP>
 cudaError_t launch_as(bool fwd, const Shape& s, const LnParams& p, cudaStream_t stream) {
   static PerDeviceOnce f, b, f_all, b_all;
+  if constexpr (P == 2 && !ODD && DROP) {
+    static PerDeviceOnce f_apart, b_apart;
+    if (s.apart)
+      return fwd ? launch(layer_norm_fwd_kernel<R, P, ODD, DROP, true, true>, f_apart, s, p, stream)
+                 : launch(layer_norm_bwd_kernel<R, P, ODD, DROP, true, true>, b_apart, s, p, stream);
+  }
   if (fwd)
     return p.o.base && p.out0.base ? launch(layer_norm_fwd_kernel<R, P, ODD, DROP, true>, f_all, s, p, stream)
                                    : launch(layer_norm_fwd_kernel<R, P, ODD, DROP, false>, f, s, p, stream);
-  if constexpr (P == 2 && !ODD && DROP) {
-    static PerDeviceOnce b_apart;
-    if (s.apart) return launch(layer_norm_bwd_kernel<R, P, ODD, DROP, true, true>, b_apart, s, p, stream);
-  }
   return p.dy.base && p.out0.base && p.out1.base ? launch(layer_norm_bwd_kernel<R, P, ODD, DROP, true>, b_all, s, p, stream)
                                                  : launch(layer_norm_bwd_kernel<R, P, ODD, DROP, false>, b, s, p, stream);
 }
