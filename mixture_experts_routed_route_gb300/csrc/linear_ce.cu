@@ -22,7 +22,7 @@
 //                   one store or one reduce-add by TMA a piece
 //   dW     g^T h:   both operands read MN-major
 // g is the one rounding between the accumulators and the results: 2^-8 at most,
-// relative, as much as the results' own.
+// relative, as much as the results' own (2^-16 where up to 64 rows count).
 // Exponentials are in base 2 with one fused product, exp2(l k - m), k = scale
 // log2 e: the rounding is relative to the small difference.
 //
@@ -31,7 +31,7 @@
 // 131072 1.38 to 1.45 ms; backward 4096 x 2048 x 131072 3.8 to 4.2 ms, 2.1 to 2.3
 // PFLOP/s with the logits formed again (8 T V D; what it cannot do without is 6 T
 // V D), 1531 x 1408 x 50021 with 30 % ignored 343 us.  One token: the weight's
-// bytes, 88 us (6.1 TB/s; floor 79), backward 298 us (three times them; floor
+// bytes, 88 us (6.1 TB/s; floor 79), backward 305 us (three times them; floor
 // 237).  Small problems: the chain of launches, 6 to 9 us each beside their work
 // (512 x 256 x 32768: forward 19 us, backward 49 us).
 // Larger pieces of the vocabulary are faster (launches, dh's sums): 4096 x 2048 x
@@ -77,6 +77,8 @@ constexpr int kGroup = 8;          // row tiles that share the columns' operand 
 constexpr int kSegment = 16;
 // Few tokens: at most 64, 32 a group of four epilogue warps.
 constexpr int kFew = 64;
+// Backward of at most so many rows that count: g in two parts, see product_rows.
+constexpr int kTwice = 64;
 constexpr int kFewSteps = 4;       // contraction steps of 64 a stage, which is also a segment
 constexpr int kFewSmem = 230 * 1000;
 static_assert(kFewSmem <= 232448, "shared memory per CTA");
@@ -92,7 +94,7 @@ struct DhPlan {
 };
 
 struct CeParams {
-  const int* count;      // rows that count, parts of dh
+  const int* count;      // rows of the products, parts of dh, rows that count
   int rows_cap;          // their capacity, a multiple of 256
   int D, V;
   int v0, vn;            // piece of the vocabulary: first, number (backward)
@@ -444,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
     const uint32_t tempty0 = cluster_addr(tempty, 0);
     uint32_t tc = 0;
     int side = 0;
+    const int whole = KIND == kGrad ? p.count[2] : 0;
     bool dead = false;   // forward: a wait ran out of time; the tiles' barriers are still met
     struct {
       int target;
@@ -473,6 +476,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
       const int target = next.target - (KIND == kGrad ? p.v0 : 0);
       const float lse2 = next.lse2;
       const float2 coef = next.coef;
+      const bool second = row >= whole;   // grad: what the rounding of the first row's g leaves over
+      const bool seconds = KIND == kGrad && row_w + 31 >= whole && whole < w.m;
       if (tile + ncl < w.total) row_values(tile + ncl);
       if constexpr (KIND == kLse) {
         float top = kLowest, sum = 0.0f;
@@ -588,6 +593,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (c + j >= w.n) x[j] = 0.0f;
+            }
+            if (seconds) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] -= second ? __bfloat162float(__float2bfloat16_rn(x[j])) : 0.0f;
             }
           }
           if (ci % kHalves == 0) {   // the stores that read the buffer before are done
@@ -844,7 +853,7 @@ struct RowParams {
   long long ignore;
   const __nv_bfloat16* h;
   long long ldh;
-  int* count;            // rows that count, parts of dh
+  int* count;            // rows of the products, parts of dh, rows that count
   DhPlan dh;             // backward
   int* list;             // [rows_cap] token of each packed row, -1 past them
   int* target;           // [rows_cap], -1 past them
@@ -860,6 +869,17 @@ struct RowParams {
   float* lse2;           // [rows_cap]
   float2* coef;          // [rows_cap]
 };
+
+// Rows of the products.  The backward rounds g to BF16.  Of a few rows each
+// result is one or a few products, so that a row's rounding shows in all of them
+// (11 rows: results off by up to 0.0034 in norm, their own rounding 0.0017).  Few
+// rows are therefore there twice: the first rows' g is rounded, the second rows' g
+// is what that left over, to 2^-16 of g.  The tiles are no more (1 x 2048 x 131072
+// 300 and 305 us, 64 rows 297 and 307; 128 rows of 2048 x 32768 would take 119
+// instead of 99, and their roundings average out).
+__device__ __forceinline__ int product_rows(const RowParams& p, int count) {
+  return p.coef && count <= kTwice ? 2 * count : count;
+}
 
 // A turn of 1024 tokens from t0, of which `base` rows that count come before:
 // the packed row of this thread's token (-1: it does not count) and the number
@@ -887,12 +907,19 @@ __device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, i
   base += all;
   if (write) {
     if (on) {
-      p.list[at] = t;
-      p.target[at] = static_cast<int>(target);
+      float lse = 0.0f, d = 0.0f;
       if (p.coef) {
-        const float lse = p.lse_in[t], d = p.dloss[t] * p.scale;
-        p.lse2[at] = lse * kLog2e;
-        p.coef[at] = make_float2(d * fmaf(2.0f * p.z, lse, 1.0f), d);
+        lse = p.lse_in[t];
+        d = p.dloss[t] * p.scale;
+      }
+      // one turn: the second rows as well
+      for (int i = at; i < (p.T <= 1024 ? product_rows(p, all) : at + 1); i += all) {
+        p.list[i] = t;
+        p.target[i] = static_cast<int>(target);
+        if (p.coef) {
+          p.lse2[i] = lse * kLog2e;
+          p.coef[i] = make_float2(d * fmaf(2.0f * p.z, lse, 1.0f), d);
+        }
       }
     } else if (t < p.T && p.loss) {
       p.loss[t] = target == p.ignore ? 0.0f : NAN;
@@ -903,17 +930,29 @@ __device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, i
   return on ? at : -1;
 }
 
-// After the last turn: the number of rows, and what stands for none up to a multiple of 256.
+// After the last turn: the number of rows, the second ones, and what stands for
+// none up to a multiple of 256.
 __device__ __forceinline__ void row_end(const RowParams& p, int count) {
+  const int rows = product_rows(p, count);
   if (threadIdx.x < 32) {
-    const int parts = p.inv ? dh_parts(p.dh, count) : 1;
+    const int parts = p.inv ? dh_parts(p.dh, rows) : 1;
     if (threadIdx.x == 0) {
-      p.count[0] = count;
+      p.count[0] = rows;
       p.count[1] = parts;
+      p.count[2] = count;
     }
   }
-  const int end = (count + kTile - 1) / kTile * kTile;
-  for (int i = count + threadIdx.x; i < end; i += 1024) {
+  if (p.T > 1024 && rows > count) {
+    __syncthreads();   // the rows are written down
+    for (int i = count + threadIdx.x; i < rows; i += 1024) {
+      p.list[i] = p.list[i - count];
+      p.target[i] = p.target[i - count];
+      p.lse2[i] = p.lse2[i - count];
+      p.coef[i] = p.coef[i - count];
+    }
+  }
+  const int end = (rows + kTile - 1) / kTile * kTile;
+  for (int i = rows + threadIdx.x; i < end; i += 1024) {
     p.list[i] = -1;
     p.target[i] = -1;
     if (p.coef) {
@@ -956,8 +995,8 @@ __global__ void __launch_bounds__(1024) ce_rows_once_kernel(const __grid_constan
   if (at >= 0) list[at] = threadIdx.x;
   if (blockIdx.x == 0) row_end(p, count);
   __syncthreads();
-  const int end = (count + kTile - 1) / kTile * kTile;
-  for (int i = blockIdx.x; i < end; i += gridDim.x) pack_row(p, i, i < count ? list[i] : -1);
+  const int rows = product_rows(p, count), end = (rows + kTile - 1) / kTile * kTile;
+  for (int i = blockIdx.x; i < end; i += gridDim.x) pack_row(p, i, i < rows ? list[i < count ? i : i - count] : -1);
 }
 
 // More tokens: one block finds the rows, 1024 tokens a turn, and others pack them.
@@ -1027,6 +1066,8 @@ __global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, const int
                                                     __nv_bfloat16* dh) {
   after_previous();
   const int n = count[0], splits = count[1], per = D / 4;
+  const int parts = n > count[2] ? 2 * splits : splits;              // of the second rows as well
+  const long long second = static_cast<long long>(count[2]) * D;
   const long long all = static_cast<long long>(T) * per, plane = static_cast<long long>((n + kTile - 1) / kTile * kTile) * D;
   const long long hop = static_cast<long long>(gridDim.x) * 256;
   for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < all; k += hop) {
@@ -1035,12 +1076,13 @@ __global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, const int
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i >= 0) {
       const float* q = part + static_cast<long long>(i) * D + c;
-      for (int s = 0; s < splits; s += 4) {
+      for (int s = 0; s < parts; s += 4) {
         float4 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          v[j] = s + j < splits ? *reinterpret_cast<const float4*>(q + (s + j) * plane)
-                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          v[j] = s + j < parts ? *reinterpret_cast<const float4*>(q + (s + j < splits ? (s + j) * plane
+                                                                                      : (s + j - splits) * plane + second))
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) a.x += v[j].x, a.y += v[j].y, a.z += v[j].z, a.w += v[j].w;
       }
@@ -1091,7 +1133,7 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
   l.dh_rows = std::max<int64_t>(l.rows_cap, std::min<int64_t>(64ll * l.rows_cap, (32 << 20) / c->d_model / kTile * kTile));
   const size_t rows = l.rows_cap, D = c->d_model;
   size_t at = 0;
-  l.count = take(&at, 8);
+  l.count = take(&at, 12);
   l.list = take(&at, rows * 4);
   l.target = take(&at, rows * 4);
   l.packed = take(&at, rows * D * 2);

@@ -113,6 +113,28 @@ def test_backward(T, D, V):
     assert error_bits() == 0
 
 
+@pytest.mark.parametrize("T,ignored", [(1, 0), (11, 0), (63, 0), (64, 0), (300, 236), (2000, 1995), (65, 0)])
+def test_few_rows_lose_nothing_between_the_products(T, ignored):
+    """Up to 64 rows that count: g is there to 2^-16, so a result is off by its own rounding and 2^-16 of the
+    magnitudes beside what an FP32 g of these logits would be off by; one row more, and g is rounded to BF16."""
+    from mixture_experts_routed_route_gb300 import loss
+    c = Case(T, 256, 5000, ignored, seed=T)
+    lse = c.lse32()
+    dh, dw = loss.linear_cross_entropy_backward(c.h, c.weight, c.targets, lse, c.d_loss, **c.kw)
+    c.check_backward(lse, dh, dw)
+    if T - ignored > 64:
+        return
+    l, el = c.logits()
+    ls, d = lse[c.on].double()[:, None], c.d_loss[c.on].double()[:, None]
+    p = torch.exp(l - ls)
+    g = d * (p - torch.zeros_like(p).scatter_(1, c.targets[c.on].long()[:, None], 1.0))
+    eg = d * p * (el + 2.0 ** -15 + 64 * E) * 1.1 + (2.0 ** -16 + 8 * 2.0 ** -24) * g.abs()
+    h, w = c.h.double()[c.on], c.weight.double()
+    for got, ref, mag in ((dh[c.on], g @ w, (eg + (5000 + 64) * E * g.abs()) @ w.abs()),
+                          (dw, g.t() @ h, (eg + (2 * T + 64) * E * g.abs()).t() @ h.abs())):
+        assert bool(((got.double() - ref).abs() <= mag + U * (ref.abs() + mag)).all())
+
+
 def test_one_gradient_alone():
     from mixture_experts_routed_route_gb300 import loss
     c = Case(200, 128, 3000, 20)
