@@ -435,13 +435,16 @@ _norm_bytes = {}
 
 
 def _layer_norm_workspace(cfg, dev):
-    """moe_layer_norm_workspace_bytes, remembered by what it depends on."""
+    """moe_layer_norm_workspace_bytes, remembered by what it depends on (0, of a
+    configuration that the library refuses for whatever reason, is not)."""
     key = cfg.tokens, cfg.d_model, dev.index
     nb = _norm_bytes.get(key)
     if nb is None:
-        if len(_norm_bytes) >= 1024:
-            _norm_bytes.clear()
-        nb = _norm_bytes[key] = _LIB.moe_layer_norm_workspace_bytes(_byref(cfg))
+        nb = _LIB.moe_layer_norm_workspace_bytes(_byref(cfg))
+        if nb:
+            if len(_norm_bytes) >= 1024:
+                _norm_bytes.clear()
+            _norm_bytes[key] = nb
     return _empty(nb, dtype=torch.uint8, device=dev)
 
 
