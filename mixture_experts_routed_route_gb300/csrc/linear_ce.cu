@@ -1145,7 +1145,8 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
     l.g = take(&at, rows * 2 * l.piece);
   } else {
     l.hit = take(&at, rows * 4);
-    l.part = take(&at, rows * 8 * std::max(l.col_tiles, few(c->tokens) ? sms : 0));
+    // a column a tile, or for few tokens one a CTA; room for either, so that fewer tokens never want more
+    l.part = take(&at, 8 * std::max(rows * l.col_tiles, c->tokens ? static_cast<size_t>(kTile) * sms : 0));
   }
   l.bytes = at;
   return l;
