@@ -59,11 +59,11 @@ constexpr int kStage = 2 * kOperand;
 enum CeKind { kLse, kGrad, kDh, kDw };
 
 // E epilogue warps, 4 KB each to turn their values around (the forward: the
-// warps' maxima and sums of a row).
+// warps' maxima and sums of a row); a stage less makes room for sixteen of them.
 template <int KIND, int E>
 struct CeCfg {
   static constexpr int kThreads = 64 + 32 * E;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = KIND == kGrad && E == 16 ? 5 : 6;
   static constexpr int kTurn = KIND == kLse ? 16384 : E * 4096;
   static constexpr int kSmem = 1024 + kStages * kStage + kTurn + 256;
   static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -73,7 +73,12 @@ constexpr int kGroup = 8;          // row tiles that share the columns' operand 
 // registers: 1024 elements.  The tensor cores cut off, not round, at each of
 // their additions, so a logit of 7168 elements is low by 7.5e-6 of itself in one
 // sum, by 1.0e-6 in seven (8 stages a sum: 0.5e-6, but reading the accumulators
-// twice as often costs 4 % of the product; one sum: 3 % faster).
+// twice as often costs 4 % of the product; one sum: 3 % faster).  The backward
+// forms the same sums as the forward of as many tokens: softmax - 1 of a
+// confident token, a difference of nearly equal numbers, is then good to what
+// lse's FP32 holds (one sum: off by as much as itself at a logit of 40 and
+// probability 0.9997; faster by 1 to 4 %: 1531 x 1408 x 50021 344 and 358 us,
+// 2048 x 7168 x 131072 6.93 and 6.99 ms, 1 x 2048 x 131072 304 and 314 us).
 constexpr int kSegment = 16;
 // Few tokens: at most 64, 32 a group of four epilogue warps.
 constexpr int kFew = 64;
@@ -99,6 +104,7 @@ struct CeParams {
   int D, V;
   int v0, vn;            // piece of the vocabulary: first, number (backward)
   int first;             // dh: store (else add)
+  int segment;           // grad: stages that one sum of a logit takes, as in the forward
   float k;               // scale log2 e
   const int* target;     // [rows_cap], -1 past the rows
   float2* part;          // lse: [column tiles, or CTAs][rows_cap]: maximum of l k, sum of exp2(l k - maximum)
@@ -218,6 +224,15 @@ __device__ __forceinline__ CeTile ce_tile(const CeWork<KIND>& w, int tile) {
   return t;
 }
 
+// 16 columns of the warp's 32 lanes: where 32 would not fit beside a row's sums.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // One 16-byte piece of a warp's 32 rows x 128 bytes, in the 128-byte swizzle.
 __device__ __forceinline__ void stage16(uint8_t* ws, int lane, int piece, uint4 v) {
   *reinterpret_cast<uint4*>(ws + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
@@ -287,11 +302,13 @@ __device__ __forceinline__ void join_chunk(float (&x)[32], int c, int n, int row
   sum += a + b;
 }
 
-template <int KIND, int E>
+// SUMS: the gradient's logits are summed in segments, p.segment stages each.
+template <int KIND, int E, bool SUMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmC, const CeParams p) {
   constexpr bool kAMn = KIND == kDw, kBMn = KIND == kDh || KIND == kDw;
+  static_assert(!SUMS || (KIND == kGrad && E == 16), "tiles of 256 columns, 64 a thread");
   constexpr int kStages = CeCfg<KIND, E>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -397,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
         uint32_t d_tmem = tmem + acc * 256;
         int first = 0;
         for (int ks = 0; ks < t.ks; ++ks, ++it) {
-          if (KIND == kLse && ks - first == kSegment) {   // the next segment, in the other accumulator
+          if ((KIND == kLse || SUMS) && ks - first == (SUMS ? p.segment : kSegment)) {   // the next segment, in the other accumulator
             if (lane == 0) tc_commit_pair_mc(&tfull[acc], 3);
             __syncwarp();
             first = ks;
@@ -447,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
     uint32_t tc = 0;
     int side = 0;
     const int whole = KIND == kGrad ? p.count[2] : 0;
-    bool dead = false;   // forward: a wait ran out of time; the tiles' barriers are still met
+    bool dead = false;   // a wait ran out of time (forward: the tiles' barriers are still met)
     struct {
       int target;
       float lse2;
@@ -551,36 +568,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
         }
         side ^= 1;
       } else {
-        const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-        ++tc;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err))) break;
-        tc_fence_after();
-        const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
-        if (!live) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
-          continue;
-        }
-#pragma unroll 1
-        for (int ci = 0; ci < cols / 32; ++ci) {
-          uint32_t v[32];
-          tmem_ld32(tbase + 32 * ci, v);
-          tmem_ld_wait();
-          if (ci == cols / 32 - 1) {   // every column has been read: the accumulator is free
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
-          }
+        // 32 columns of a row, chunk ci of the warp's, on their way out
+        auto put_chunk = [&](float (&x)[32], int ci) {
           const int c = c0 + 32 * ci;
           constexpr int kHalves = KIND == kDh ? 1 : 2;   // chunks of 32 columns in 128 bytes
-          float x[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
-          if (KIND != kGrad && t.ks == 0) {   // an empty contraction
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = 0.0f;
-          }
           if constexpr (KIND == kGrad) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = coef.x * exp2_fast(fmaf(x[j], p.k, -lse2));
@@ -633,6 +624,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
               bulk_commit();
             }
           }
+        };
+        // the accumulator whose turn it is: complete (false: a wait ran out of time), its first column, free again
+        auto next_sum = [&] {
+          const bool there =
+              __all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[tc & 1], (tc >> 1) & 1, abort_flag, p.err));
+          tc_fence_after();
+          return there;
+        };
+        auto sum_at = [&] { return tmem + (tc & 1) * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16); };
+        auto sum_read = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * (tc & 1));
+        };
+        if (!live) {
+          for (int ks = 0; ks == 0 || (SUMS && ks < t.ks); ks += p.segment, ++tc) {
+            dead = !next_sum();
+            if (dead) break;
+            sum_read();
+          }
+          if (dead) break;
+        } else if constexpr (!SUMS) {
+          if (!next_sum()) break;
+          const uint32_t tbase = sum_at();
+#pragma unroll 1
+          for (int ci = 0; ci < cols / 32; ++ci) {
+            uint32_t v[32];
+            tmem_ld32(tbase + 32 * ci, v);
+            tmem_ld_wait();
+            if (ci == cols / 32 - 1) sum_read();   // every column has been read: the accumulator is free
+            float x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+            if (KIND != kGrad && t.ks == 0) {   // an empty contraction
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+            }
+            put_chunk(x, ci);
+          }
+          ++tc;
+        } else {
+          // this thread's columns: sums of the segments
+          constexpr int kChunks = 32 / E;
+          float x[kChunks][32];
+          for (int ks = 0; ks < t.ks; ks += p.segment, ++tc) {
+            dead = !next_sum();
+            if (dead) break;
+            const uint32_t tbase = sum_at();
+#pragma unroll
+            for (int ci = 0; ci < kChunks; ++ci) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 16) {
+                uint32_t v[16];
+                tmem_ld16(tbase + 32 * ci + i, v);
+                tmem_ld_wait();
+                if (i == 16 && ci == kChunks - 1) sum_read();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  x[ci][i + j] = ks == 0 ? __uint_as_float(v[j]) : x[ci][i + j] + __uint_as_float(v[j]);
+              }
+            }
+          }
+          if (dead) break;
+          // the accumulators are free: the next tile's products run beside this
+#pragma unroll
+          for (int ci = 0; ci < kChunks; ++ci) put_chunk(x[ci], ci);
         }
       }
     }
@@ -1162,30 +1219,34 @@ bool map_2d(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int b
                       box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int KIND, int E>
+template <int KIND, int E, bool SUMS = false>
 cudaError_t launch_gemm_as(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
                            long long tiles, cudaStream_t stream) {
   using C = CeCfg<KIND, E>;
   static PerDeviceOnce once;
   cudaError_t e = once.once([&] {
-    return cudaFuncSetAttribute(ce_gemm_kernel<KIND, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(ce_gemm_kernel<KIND, E, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<CUtensorMap*>(&a), const_cast<CUtensorMap*>(&b), const_cast<CUtensorMap*>(&c),
                   const_cast<CeParams*>(&p)};
   const int grid = 2 * static_cast<int>(std::max<long long>(1, std::min<long long>(pairs, tiles)));
-  return launch_dependent(reinterpret_cast<const void*>(ce_gemm_kernel<KIND, E>), dim3(grid), C::kThreads, C::kSmem, stream,
-                          args);
+  return launch_dependent(reinterpret_cast<const void*>(ce_gemm_kernel<KIND, E, SUMS>), dim3(grid), C::kThreads, C::kSmem,
+                          stream, args);
 }
 // Sixteen epilogue warps where the forward's product is too short to hide eight
 // warps' exponentials and takes one segment (512 x 256 x 32768 22.8 and 20.2 us,
 // 4096 x 512 x 65536 224 and 210, 4096 x 1024 x 65536 373 and 366).  The
-// backward's first product gained nothing.
+// backward's first product gained nothing in one sum; in several, sixteen warps
+// have 64 columns a thread to keep and spill little (64 x 2048 x 131072 318 us,
+// eight warps 323 to 341; 2048 x 7168 x 131072 6.99 and 7.08 ms).
 template <int KIND>
 cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
                         long long tiles, cudaStream_t stream) {
   if constexpr (KIND == kLse)
     if (p.D <= kSegment * kBk) return launch_gemm_as<KIND, 16>(a, b, c, p, pairs, tiles, stream);
+  if constexpr (KIND == kGrad)
+    if (p.D > p.segment * kBk) return launch_gemm_as<KIND, 16, true>(a, b, c, p, pairs, tiles, stream);
   return launch_gemm_as<KIND, 8>(a, b, c, p, pairs, tiles, stream);
 }
 
@@ -1343,6 +1404,7 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
   r.coef = at<float2>(workspace, l.coef);
   p.lse2 = r.lse2;
   p.coef = r.coef;
+  p.segment = few(T) ? kFewSteps : kSegment;
   r.dh = {D, static_cast<int>(l.piece / kBk), sms / 2, static_cast<int>(l.dh_rows)};
   __nv_bfloat16* g = at<__nv_bfloat16>(workspace, l.g);
   float* part = at<float>(workspace, l.dh);
