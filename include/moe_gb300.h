@@ -884,8 +884,10 @@ MOE_API moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, con
  * forward's inputs and lse:
  *   dh       bf16 [T, D] contiguous, or NULL; zeros in rows that do not count
  *   dweight  bf16 [V, D], overwritten, or NULL; zeros with T = 0
- * It forms the logits again, a piece of the vocabulary at a time; the gradient
- * of the logits is rounded to BF16 (at most 2^-8 relative) between the products.
+ * It forms the logits again, a piece of the vocabulary at a time, in the sums of
+ * the forward of as many tokens; the gradient of the logits is rounded to BF16
+ * (at most 2^-8 relative) between the products, without a weight that all tokens
+ * share (d_loss of a mean); where at most 64 tokens count, in two parts.
  *
  * workspace: 256-byte aligned, contents need not be kept or cleared, at least
  * moe_linear_ce_workspace_bytes(cfg, backward, piece) for pieces of `piece`

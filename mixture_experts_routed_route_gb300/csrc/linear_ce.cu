@@ -22,7 +22,14 @@
 //                   one store or one reduce-add by TMA a piece
 //   dW     g^T h:   both operands read MN-major
 // g is the one rounding between the accumulators and the results: 2^-8 at most,
-// relative, as much as the results' own (2^-16 where up to 64 rows count).
+// relative, as much as the results' own; where up to 64 rows count, what it
+// leaves over takes part as well.  A factor that g's rows share (the 1 / N of a
+// mean) is kept out of it, the `unit` m: g is formed as g / m and the results are
+// multiplied by m in FP32.  With it inside, the target's g, near -dl scale in
+// every row, is rounded the same way in all of them: of 255 to 2040 rows of equal
+// weight all results were too large or too small by up to 0.0039.  m is the
+// significand, 1 <= m < 2, of the largest finite |dl scale|, so that no exponent
+// moves.
 // Exponentials are in base 2 with one fused product, exp2(l k - m), k = scale
 // log2 e: the rounding is relative to the small difference.
 //
@@ -111,6 +118,7 @@ struct CeParams {
   float* hit;            // lse: l_target (before the scale)
   const float* lse2;     // grad: lse log2 e
   const float2* coef;    // grad: scale dl (1 + 2 z lse), scale dl
+  const float* unit;     // backward: what g leaves out, and its reciprocal
   uint32_t* err;
 };
 
@@ -464,6 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
     uint32_t tc = 0;
     int side = 0;
     const int whole = KIND == kGrad ? p.count[2] : 0;
+    const float unit = KIND == kGrad ? p.unit[1] : KIND == kDw ? p.unit[0] : 1.0f;
     bool dead = false;   // a wait ran out of time (forward: the tiles' barriers are still met)
     struct {
       int target;
@@ -492,7 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
       // what the rows need, asked for a tile ahead
       const int target = next.target - (KIND == kGrad ? p.v0 : 0);
       const float lse2 = next.lse2;
-      const float2 coef = next.coef;
+      const float2 coef = make_float2(next.coef.x * unit, next.coef.y * unit);
       const bool second = row >= whole;   // grad: what the rounding of the first row's g leaves over
       const bool seconds = KIND == kGrad && row_w + 31 >= whole && whole < w.m;
       if (tile + ncl < w.total) row_values(tile + ncl);
@@ -589,6 +598,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
 #pragma unroll
               for (int j = 0; j < 32; ++j) x[j] -= second ? __bfloat162float(__float2bfloat16_rn(x[j])) : 0.0f;
             }
+          }
+          if constexpr (KIND == kDw) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] *= unit;
           }
           if (ci % kHalves == 0) {   // the stores that read the buffer before are done
             if (lane == 0) bulk_wait_read<0>();
@@ -911,6 +924,7 @@ struct RowParams {
   const __nv_bfloat16* h;
   long long ldh;
   int* count;            // rows of the products, parts of dh, rows that count
+  float* unit;           // backward: the factor that g leaves out, and its reciprocal
   DhPlan dh;             // backward
   int* list;             // [rows_cap] token of each packed row, -1 past them
   int* target;           // [rows_cap], -1 past them
@@ -941,9 +955,9 @@ __device__ __forceinline__ int product_rows(const RowParams& p, int count) {
 // A turn of 1024 tokens from t0, of which `base` rows that count come before:
 // the packed row of this thread's token (-1: it does not count) and the number
 // of rows after the turn.  counts: the warps', a turn's own.  write: put
-// down what the products need of the row; tokens that do not count get their results: loss 0
-// (NaN for a target outside the vocabulary), lse 0.
-__device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, int* counts, bool write) {
+// down what the products need of the row, and keep in `most` the bits of this thread's largest finite |dl scale|;
+// tokens that do not count get their results: loss 0 (NaN for a target outside the vocabulary), lse 0.
+__device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, int* counts, bool write, uint32_t& most) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = t0 + threadIdx.x;
   long long target = p.ignore;
@@ -968,6 +982,8 @@ __device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, i
       if (p.coef) {
         lse = p.lse_in[t];
         d = p.dloss[t] * p.scale;
+        const uint32_t bits = __float_as_uint(d) & 0x7FFFFFFFu;
+        if (bits < 0x7F800000u) most = max(most, bits);
       }
       // one turn: the second rows as well
       for (int i = at; i < (p.T <= 1024 ? product_rows(p, all) : at + 1); i += all) {
@@ -987,10 +1003,24 @@ __device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, i
   return on ? at : -1;
 }
 
-// After the last turn: the number of rows, the second ones, and what stands for
-// none up to a multiple of 256.
-__device__ __forceinline__ void row_end(const RowParams& p, int count) {
+// After the last turn: the number of rows, the unit, the second rows, and what
+// stands for none up to a multiple of 256.
+__device__ __forceinline__ void row_end(const RowParams& p, int count, uint32_t most) {
+  __shared__ uint32_t tops[32];
   const int rows = product_rows(p, count);
+  if (p.coef) {
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = most;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      most = __reduce_max_sync(0xFFFFFFFFu, tops[threadIdx.x]);
+      const float m = __uint_as_float((most & 0x007FFFFFu) | 0x3F800000u);
+      if (threadIdx.x == 0) {
+        p.unit[0] = m;
+        p.unit[1] = 1.0f / m;
+      }
+    }
+  }
   if (threadIdx.x < 32) {
     const int parts = p.inv ? dh_parts(p.dh, rows) : 1;
     if (threadIdx.x == 0) {
@@ -1048,9 +1078,10 @@ __global__ void __launch_bounds__(1024) ce_rows_once_kernel(const __grid_constan
   wait_previous();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int count = 0;
-  const int at = row_turn(p, 0, count, counts, blockIdx.x == 0);
+  uint32_t most = 0;
+  const int at = row_turn(p, 0, count, counts, blockIdx.x == 0, most);
   if (at >= 0) list[at] = threadIdx.x;
-  if (blockIdx.x == 0) row_end(p, count);
+  if (blockIdx.x == 0) row_end(p, count, most);
   __syncthreads();
   const int rows = product_rows(p, count), end = (rows + kTile - 1) / kTile * kTile;
   for (int i = blockIdx.x; i < end; i += gridDim.x) pack_row(p, i, i < rows ? list[i < count ? i : i - count] : -1);
@@ -1061,8 +1092,9 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const __grid_constant__ R
   __shared__ int counts[2][32];
   wait_previous();
   int base = 0;
-  for (int t0 = 0, turn = 0; t0 < p.T; t0 += 1024, turn ^= 1) row_turn(p, t0, base, counts[turn], true);
-  row_end(p, base);
+  uint32_t most = 0;
+  for (int t0 = 0, turn = 0; t0 < p.T; t0 += 1024, turn ^= 1) row_turn(p, t0, base, counts[turn], true, most);
+  row_end(p, base, most);
 }
 __global__ void __launch_bounds__(256) ce_pack_kernel(const __grid_constant__ RowParams p) {
   after_previous();
@@ -1117,11 +1149,12 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* part, const
   }
 }
 
-// dh: the sum of the splits' FP32 rows, rounded; zeros for tokens that do not
-// count.  A thread takes four columns and asks for four splits at a time.
-__global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, const int* count, const int* inv, int T, int D,
-                                                    __nv_bfloat16* dh) {
+// dh: the sum of the splits' FP32 rows, times the unit, rounded; zeros for tokens
+// that do not count.  A thread takes four columns and asks for four splits at a time.
+__global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, const int* count, const float* unit, const int* inv,
+                                                    int T, int D, __nv_bfloat16* dh) {
   after_previous();
+  const float m = *unit;
   const int n = count[0], splits = count[1], per = D / 4;
   const int parts = n > count[2] ? 2 * splits : splits;              // of the second rows as well
   const long long second = static_cast<long long>(count[2]) * D;
@@ -1145,7 +1178,7 @@ __global__ void __launch_bounds__(256) ce_dh_kernel(const float* part, const int
       }
     }
     *reinterpret_cast<uint2*>(dh + static_cast<long long>(t) * D + c) =
-        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        make_uint2(pack_bf16x2(a.x * m, a.y * m), pack_bf16x2(a.z * m, a.w * m));
   }
 }
 
@@ -1174,7 +1207,7 @@ struct Layout {
   int rows_cap, col_tiles;
   int64_t dh_rows;        // of partial sums
   int64_t piece;          // vocabulary entries a piece, a multiple of 256
-  size_t count, list, target, inv, lse2, coef, hit, part, packed, g, dh, bytes;
+  size_t count, unit, list, target, inv, lse2, coef, hit, part, packed, g, dh, bytes;
 };
 size_t take(size_t* at, size_t n) {
   const size_t r = *at;
@@ -1190,7 +1223,8 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
   l.dh_rows = std::max<int64_t>(l.rows_cap, std::min<int64_t>(64ll * l.rows_cap, (32 << 20) / c->d_model / kTile * kTile));
   const size_t rows = l.rows_cap, D = c->d_model;
   size_t at = 0;
-  l.count = take(&at, 12);
+  l.count = take(&at, 12);   // 256 bytes: the unit behind it
+  l.unit = l.count + 16;
   l.list = take(&at, rows * 4);
   l.target = take(&at, rows * 4);
   l.packed = take(&at, rows * D * 2);
@@ -1404,6 +1438,8 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
   r.coef = at<float2>(workspace, l.coef);
   p.lse2 = r.lse2;
   p.coef = r.coef;
+  r.unit = at<float>(workspace, l.unit);
+  p.unit = r.unit;
   p.segment = few(T) ? kFewSteps : kSegment;
   r.dh = {D, static_cast<int>(l.piece / kBk), sms / 2, static_cast<int>(l.dh_rows)};
   __nv_bfloat16* g = at<__nv_bfloat16>(workspace, l.g);
@@ -1434,7 +1470,8 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
     const int* inv = r.inv;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dh);
     const int* count = r.count;
-    void* args[] = {&in, &count, &inv, &t, &d, &out};
+    const float* unit = r.unit;
+    void* args[] = {&in, &count, &unit, &inv, &t, &d, &out};
     const long long blocks = (static_cast<long long>(T) * (D / 4) + 255) / 256;
     if (launch_dependent(reinterpret_cast<const void*>(ce_dh_kernel),
                          dim3(static_cast<unsigned>(std::min<long long>(blocks, 16 * sms))), 256, 0, stream,
