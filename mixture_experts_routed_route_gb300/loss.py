@@ -53,6 +53,7 @@ def workspace(T, D, V, *, backward=True, piece=None, device="cuda"):
     """A workspace for calls on up to T tokens: of the forward or the backward,
     which works in pieces of `piece` vocabulary entries (default: as many as
     512 MiB hold; a larger workspace means larger pieces)."""
+    _need(0 <= T < _MOST and 0 < D < _MOST and 0 < V < _MOST, "sizes: expected T >= 0, D and V >= 1, all below 2^31")
     cfg = abi.moe_linear_ce_config(T, D, V, 8, 1.0, 0.0, -100, 0)
     device = torch.device(device)
     with torch.cuda.device(device):
