@@ -428,7 +428,8 @@ __device__ __forceinline__ void table_load(const uint8_t* shared, int planes, in
   q[2] = pair_of(b.x, b.y);
   q[3] = pair_of(b.z, b.w);
 }
-// Fill it (all threads; ends with a barrier).
+// Fill it (all threads; ends with a barrier).  Plain loads: what ran before may have written the parameters while this
+// kernel was in place already, so they are not constant for as long as it is there.
 template <int N>
 __device__ __forceinline__ void make_table(const LnParams& p, uint8_t* shared, int off, int pieces, int planes) {
   for (int c = threadIdx.x; c < pieces; c += blockDim.x) {
@@ -438,11 +439,11 @@ __device__ __forceinline__ void make_table(const LnParams& p, uint8_t* shared, i
       float v[8];
       if (src && off == 0 && 8 * c + 8 <= p.D) {
         if (p.params_f32) {
-          const float4 a = __ldg(static_cast<const float4*>(src) + 2 * c);
-          const float4 b = __ldg(static_cast<const float4*>(src) + 2 * c + 1);
+          const float4 a = static_cast<const float4*>(src)[2 * c];
+          const float4 b = static_cast<const float4*>(src)[2 * c + 1];
           v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         } else {
-          const uint4 u = __ldg(static_cast<const uint4*>(src) + c);
+          const uint4 u = static_cast<const uint4*>(src)[c];
           v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
           v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
         }
