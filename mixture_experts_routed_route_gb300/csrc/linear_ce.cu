@@ -84,8 +84,8 @@ constexpr int kGroup = 8;          // row tiles that share the columns' operand 
 // forms the same sums as the forward of as many tokens: softmax - 1 of a
 // confident token, a difference of nearly equal numbers, is then good to what
 // lse's FP32 holds (one sum: off by as much as itself at a logit of 40 and
-// probability 0.9997; faster by 1 to 4 %: 1531 x 1408 x 50021 344 and 358 us,
-// 2048 x 7168 x 131072 6.93 and 6.99 ms, 1 x 2048 x 131072 304 and 314 us).
+// probability 0.9997; faster by 1 to 2 %: 1531 x 1408 x 50021 346 and 354 us,
+// 2048 x 7168 x 131072 6.93 and 6.99 ms, 1 x 2048 x 131072 304 and 312 us).
 constexpr int kSegment = 16;
 // Few tokens: at most 64, 32 a group of four epilogue warps.
 constexpr int kFew = 64;
@@ -316,6 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
     ce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmC, const CeParams p) {
   constexpr bool kAMn = KIND == kDw, kBMn = KIND == kDh || KIND == kDw;
+  constexpr bool kSums = SUMS || (KIND == kLse && E == 8);   // a tile may take several accumulators
   static_assert(!SUMS || (KIND == kGrad && E == 16), "tiles of 256 columns, 64 a thread");
   constexpr int kStages = CeCfg<KIND, E>::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -413,49 +414,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
       const uint32_t idesc0 = idesc_bf16(0, 256) | (kAMn ? kIdescAMnMajor : 0u) | (kBMn ? (1u << 16) : 0u);
       uint32_t it = 0, tc = 0;
       bool ok = true;
-      for (int tile = cid; ok && tile < w.total; tile += ncl, ++tc) {
+      for (int tile = cid; ok && tile < w.total; tile += ncl) {
         const CeTile t = ce_tile<KIND, E>(w, tile);
         const uint32_t idesc = idesc0 | ((static_cast<uint32_t>(t.n) >> 3) << 17);
-        uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) break;
-        tc_fence_after();
-        uint32_t d_tmem = tmem + acc * 256;
-        int first = 0;
-        for (int ks = 0; ks < t.ks; ++ks, ++it) {
-          if ((KIND == kLse || SUMS) && ks - first == (SUMS ? p.segment : kSegment)) {   // the next segment, in the other accumulator
-            if (lane == 0) tc_commit_pair_mc(&tfull[acc], 3);
-            __syncwarp();
-            first = ks;
-            ++tc;
-            acc = tc & 1, aph = (tc >> 1) & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            d_tmem = tmem + acc * 256;
-          }
-          const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait<true>(&full[slot], ph, abort_flag, p.err))) {
-            ok = false;
-            break;
-          }
+        // Sums of a tile, each in the accumulator whose turn it is; a loop of its own around the stages, which a test in
+        // each of them slows down
+        int ks = 0;
+        for (bool more = true; more; more = kSums && ks < t.ks) {
+          const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err));
+          if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t sa = smem_u32(smem + slot * kStage), sb = sa + kOperand;
+          const uint32_t d_tmem = tmem + acc * 256;
+          const int first = ks, end = kSums ? min(t.ks, ks + (SUMS ? p.segment : kSegment)) : t.ks;
+          for (; ks < end; ++ks, ++it) {
+            const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(&full[slot], ph, abort_flag, p.err));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t sa = smem_u32(smem + slot * kStage), sb = sa + kOperand;
 #pragma unroll
-            for (int j = 0; j < kBk / 16; ++j) {
-              const uint64_t ad = kAMn ? sdesc_mn_bf16(sa + j * 2048) : sdesc_k_sw128(sa + j * 32);
-              const uint64_t bd = kBMn ? sdesc_mn_bf16(sb + j * 2048) : sdesc_k_sw128(sb + j * 32);
-              mma_bf16_pair(d_tmem, ad, bd, idesc, ((ks - first) | j) ? 1u : 0u);
+              for (int j = 0; j < kBk / 16; ++j) {
+                const uint64_t ad = kAMn ? sdesc_mn_bf16(sa + j * 2048) : sdesc_k_sw128(sa + j * 32);
+                const uint64_t bd = kBMn ? sdesc_mn_bf16(sb + j * 2048) : sdesc_k_sw128(sb + j * 32);
+                mma_bf16_pair(d_tmem, ad, bd, idesc, ((ks - first) | j) ? 1u : 0u);
+              }
+              tc_commit_pair_mc(&empty[slot], 3);
             }
-            tc_commit_pair_mc(&empty[slot], 3);
+            __syncwarp();
           }
+          if (!ok) break;
+          if (lane == 0) tc_commit_pair_mc(&tfull[acc], 3);
           __syncwarp();
+          ++tc;
         }
-        if (!ok) break;
-        if (lane == 0) tc_commit_pair_mc(&tfull[acc], 3);
-        __syncwarp();
       }
       if (lane == 0 && it > 0) {
         tc_commit_pair(drain);
@@ -489,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
         }
       }
     };
-    if (cid < w.total) row_values(cid);
+    if (!SUMS && cid < w.total) row_values(cid);
     for (int tile = cid; tile < w.total; tile += ncl) {
       const CeTile t = ce_tile<KIND, E>(w, tile);
       const int row = t.row0 + 128 * rank + 32 * q + lane;     // this thread's
@@ -498,13 +491,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
       // Whether anything reads this warp's rows: those that count; of g, which the dW product reads 64 rows at a
       // time, those up to a multiple of 64; of dW, the vocabulary's.
       const bool live = KIND == kDw ? p.v0 + row_w < p.V : row_w < (KIND == kGrad ? (w.m + 63) / 64 * 64 : w.m);
-      // what the rows need, asked for a tile ahead
+      // what the rows need, asked for a tile ahead (in segments: while the first sum is formed)
+      if (SUMS) row_values(tile);
       const int target = next.target - (KIND == kGrad ? p.v0 : 0);
       const float lse2 = next.lse2;
       const float2 coef = make_float2(next.coef.x * unit, next.coef.y * unit);
       const bool second = row >= whole;   // grad: what the rounding of the first row's g leaves over
       const bool seconds = KIND == kGrad && row_w + 31 >= whole && whole < w.m;
-      if (tile + ncl < w.total) row_values(tile + ncl);
+      if (!SUMS && tile + ncl < w.total) row_values(tile + ncl);
       if constexpr (KIND == kLse) {
         float top = kLowest, sum = 0.0f;
         if (dead) {
@@ -1273,7 +1267,8 @@ cudaError_t launch_gemm_as(const CUtensorMap& a, const CUtensorMap& b, const CUt
 // 4096 x 512 x 65536 224 and 210, 4096 x 1024 x 65536 373 and 366).  The
 // backward's first product gained nothing in one sum; in several, sixteen warps
 // have 64 columns a thread to keep and spill little (64 x 2048 x 131072 318 us,
-// eight warps 323 to 341; 2048 x 7168 x 131072 6.99 and 7.08 ms).
+// eight warps 323 to 341, before the tensor cores' loop was split in sums, which
+// took it to 311; 2048 x 7168 x 131072 6.99 and 7.08 ms).
 template <int KIND>
 cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
                         long long tiles, cudaStream_t stream) {
