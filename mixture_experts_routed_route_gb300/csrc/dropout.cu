@@ -5,9 +5,10 @@
 //
 // A thread takes groups of eight elements, which share one block of the
 // generator, one after the other, the next one's loads ahead of this one's mask.
-// What bounds it: 32 x 32 -> 64 bit products take 4 cycles a warp, and 19 of them
-// a group are 76 cycles where BF16's bytes take 70 (16384 x 7168: 77 us, 6.1 TB/s;
-// floor 69); in FP32 the stream alone (135 us, 6.9 TB/s).  On the way there, BF16:
+// What bounds it: the stream (16384 x 7168 in BF16 77 us, 6.1 TB/s, floor 69; FP32
+// 135 us, 6.9 TB/s).  Beside it the generator's 32 x 32 -> 64 bit products, 19 a
+// group at 4 cycles a warp and scheduler, take 29 us, and 60 % of the issue slots
+// are busy in BF16.  On the way there, BF16:
 // four groups a thread at a time with 98 registers took 133 us (22 % of the warps:
 // products and logic, which run in different pipes, hardly overlapped); the first
 // round's product with the site is formed once a thread, and dropped places are

@@ -26,10 +26,14 @@
 // 21.4 us (5.5 TB/s; floor 17.3), 8192 x 7168 76 us (6.2 TB/s); the backward with
 // its second kernel 34.3 us (floor 21.6) and 100.5 us (5.8 TB/s).  Short inputs
 // add a fixed part (launch, first row, last stores; the backward's column sums
-// and second kernel, 12 us).  Dropout adds the generator's products, 4 cycles a
-// warp each, beside the norm's own arithmetic: forward 26.3 and 92 us, backward
-// 36.5 and 112 us.  Odd widths: 16384 x 1411 forward 37 us, with dropout 56, backward 54
-// and 72 (16384 x 1408: forward 31 and 37.6, backward 42.8).
+// and second kernel, 12 us).  With dropout: forward 26.3 and 92 us, backward 36.5
+// and 112 us.  The generator's products alone would be under 4 us of 2048 x 7168
+// (4 cycles a warp and scheduler each), and half of the issue slots are idle: it
+// is that a row's mask and sums stand between two barriers, one row a CTA at a
+// time.  Odd widths: 16384 x 1411 forward 37 us, with dropout 56, backward 54 and
+// 72 (16384 x 1408: forward 31 and 37.6, backward 42.8).  Odd widths above 8185
+// take four pieces a thread and spill: 4096 x 8191 forward 93 and 102 us, backward
+// 194 and 227 (4096 x 8184: 57 and 69, 73 and 89).
 // Tried and slower: forward rows through a ring too (27.5 us, 88.7 us), 24 warps
 // (80 registers: one row in flight a CTA, 24.7 us), one piece a thread (25.6 us);
 // backward with rows in registers (56 us, spills), 28 warps without a row's

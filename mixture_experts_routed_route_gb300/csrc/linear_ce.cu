@@ -35,12 +35,14 @@
 //
 // What bounds it (one GB300).  Large products: the tensor cores under the power
 // cap.  Forward 2048 x 7168 x 131072 2.29 to 2.46 ms (1.6 PFLOP/s), 4096 x 2048 x
-// 131072 1.38 to 1.45 ms; backward 4096 x 2048 x 131072 3.8 to 4.2 ms, 2.1 to 2.3
-// PFLOP/s with the logits formed again (8 T V D; what it cannot do without is 6 T
-// V D), 1531 x 1408 x 50021 with 30 % ignored 343 us.  One token: the weight's
-// bytes, 88 us (6.1 TB/s; floor 79), backward 305 us (three times them; floor
-// 237).  Small problems: the chain of launches, 6 to 9 us each beside their work
-// (512 x 256 x 32768: forward 19 us, backward 49 us).
+// 131072 1.38 to 1.45 ms; backward 4096 x 2048 x 131072 3.9 to 4.2 ms, 1.57 to
+// 1.69 PFLOP/s (three products, 6 T V D; floor 3.43 ms), 2048 x 7168 x 131072 7.0
+// ms (1.65), 1531 x 1408 x 50021 with 30 % ignored 354 us (1.28; floor 235: the
+// last of five row tiles holds 48 rows, the last of six column tiles 128).  One
+// token: the weight's bytes, 88 us (6.1 TB/s; floor 79), backward 312 us (the
+// weight read twice and its gradient written; floor 158: read once).  Small
+// problems: the chain of launches, 6 to 9 us each beside their work (512 x 256 x
+// 32768: forward 19 us, backward 51 us; floors 4.5 and 13.4).
 // Larger pieces of the vocabulary are faster (launches, dh's sums): 4096 x 2048 x
 // 131072 in pieces of 16384 entries 4.18 ms, 32768 3.94, 65536 3.79; pieces that
 // stay in L2 are not.  Tried without gain: sixteen epilogue warps in the
@@ -79,8 +81,9 @@ constexpr int kGroup = 8;          // row tiles that share the columns' operand 
 // Stages that the forward's accumulators sum before a new sum begins, in
 // registers: 1024 elements.  The tensor cores cut off, not round, at each of
 // their additions, so a logit of 7168 elements is low by 7.5e-6 of itself in one
-// sum, by 1.0e-6 in seven (8 stages a sum: 0.5e-6, but reading the accumulators
-// twice as often costs 4 % of the product; one sum: 3 % faster).  The backward
+// sum, by 1.0e-6 in seven (2.4e-6 where every product has the same sign; 8 stages
+// a sum: 0.5e-6, but reading the accumulators twice as often costs 4 % of the
+// product; one sum: 3 % faster).  The backward
 // forms the same sums as the forward of as many tokens: softmax - 1 of a
 // confident token, a difference of nearly equal numbers, is then good to what
 // lse's FP32 holds (one sum: off by as much as itself at a logit of 40 and
@@ -939,9 +942,12 @@ struct RowParams {
 // result is one or a few products, so that a row's rounding shows in all of them
 // (11 rows: results off by up to 0.0034 in norm, their own rounding 0.0017).  Few
 // rows are therefore there twice: the first rows' g is rounded, the second rows' g
-// is what that left over, to 2^-16 of g.  The tiles are no more (1 x 2048 x 131072
-// 300 and 305 us, 64 rows 297 and 307; 128 rows of 2048 x 32768 would take 119
-// instead of 99, and their roundings average out).
+// is what that left over, to 2^-16 of g (the logits' own error aside).  The tiles
+// are no more (1 x 2048 x 131072 300 and 305 us, 64 rows 297 and 307; 128 rows of
+// 2048 x 32768 would take 119 instead of 99).  More rows are off by 0.0017 in norm
+// where they share a weight, which the unit keeps out of g, and by 0.0023 where
+// weights differ from row to row: a target's g of its own weight is then rounded
+// by up to 2^-8, in rows of equal weight alike.
 __device__ __forceinline__ int product_rows(const RowParams& p, int count) {
   return p.coef && count <= kTwice ? 2 * count : count;
 }

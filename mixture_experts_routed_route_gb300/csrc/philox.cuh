@@ -8,8 +8,8 @@
 // e / 8 high word, site, step): half e % 2 of word (e % 8) / 2.  It is kept if
 // those 16 bits, as a number, are at least the threshold p 2^16.
 // 16 bits an element: one block serves the 8 elements a thread handles at a
-// time, 2.5 wide products an element.  With 32 bits it would be five, about as
-// many as the SMs issue while the elements stream from HBM.
+// time, 2.5 wide products an element, which take the SMs 29 us for the 16384 x
+// 7168 elements that stream from HBM in 69 (BF16).  With 32 bits it would be five.
 #pragma once
 
 #include "common.cuh"
