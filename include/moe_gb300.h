@@ -879,13 +879,17 @@ MOE_API moe_status moe_layer_norm_backward(const moe_layer_norm_config* cfg, con
  *   targets  int32 or int64 [T] (target_bytes 4 or 8)
  *   loss, lse  float [T]
  * Operands are BF16, products are summed in FP32, and so are the softmax's sums.
+ * (The tensor cores cut off instead of rounding; sums there are kept to 1024
+ * elements or fewer, and losses are as close as with FP32 products that round.)
  *
  * moe_linear_ce_backward: from d_loss (float [T], gradient of each loss) and the
  * forward's inputs and lse:
  *   dh       bf16 [T, D] contiguous, or NULL; zeros in rows that do not count
  *   dweight  bf16 [V, D], overwritten, or NULL; zeros with T = 0
- * It forms the logits again, a piece of the vocabulary at a time, in the sums of
- * the forward of as many tokens; the gradient of the logits is rounded to BF16
+ * It forms the logits again, a piece of the vocabulary at a time; each target's,
+ * as in the forward, with FP32 products and sums apart from the tensor cores, so
+ * that softmax - 1 of a confident token is as good as lse; the gradient of the
+ * logits is rounded to BF16
  * (at most 2^-8 relative) between the products, without a weight that all tokens
  * share (d_loss of a mean); where at most 64 tokens count, in two parts.
  *

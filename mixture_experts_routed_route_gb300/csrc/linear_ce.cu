@@ -34,15 +34,15 @@
 // log2 e: the rounding is relative to the small difference.
 //
 // What bounds it (one GB300).  Large products: the tensor cores under the power
-// cap.  Forward 2048 x 7168 x 131072 2.29 to 2.46 ms (1.6 PFLOP/s), 4096 x 2048 x
-// 131072 1.38 to 1.45 ms; backward 4096 x 2048 x 131072 3.9 to 4.2 ms, 1.57 to
+// cap.  Forward 2048 x 7168 x 131072 2.13 to 2.3 ms (1.7 PFLOP/s), 4096 x 2048 x
+// 131072 1.25 ms; backward 4096 x 2048 x 131072 3.9 to 4.2 ms, 1.57 to
 // 1.69 PFLOP/s (three products, 6 T V D; floor 3.43 ms), 2048 x 7168 x 131072 7.0
-// ms (1.65), 1531 x 1408 x 50021 with 30 % ignored 354 us (1.28; floor 235: the
+// ms (1.65), 1531 x 1408 x 50021 with 30 % ignored 347 us (1.3; floor 235: the
 // last of five row tiles holds 48 rows, the last of six column tiles 128).  One
-// token: the weight's bytes, 88 us (6.1 TB/s; floor 79), backward 312 us (the
+// token: the weight's bytes, 90 us (6.0 TB/s; floor 79), backward 303 us (the
 // weight read twice and its gradient written; floor 158: read once).  Small
 // problems: the chain of launches, 6 to 9 us each beside their work (512 x 256 x
-// 32768: forward 19 us, backward 51 us; floors 4.5 and 13.4).
+// 32768: forward 19 us, backward 50 us; floors 4.5 and 13.4).
 // Larger pieces of the vocabulary are faster (launches, dh's sums): 4096 x 2048 x
 // 131072 in pieces of 16384 entries 4.18 ms, 32768 3.94, 65536 3.79; pieces that
 // stay in L2 are not.  Tried without gain: sixteen epilogue warps in the
@@ -68,35 +68,31 @@ constexpr int kStage = 2 * kOperand;
 enum CeKind { kLse, kGrad, kDh, kDw };
 
 // E epilogue warps, 4 KB each to turn their values around (the forward: the
-// warps' maxima and sums of a row); a stage less makes room for sixteen of them.
+// warps' maxima and sums of a row).
 template <int KIND, int E>
 struct CeCfg {
   static constexpr int kThreads = 64 + 32 * E;
-  static constexpr int kStages = KIND == kGrad && E == 16 ? 5 : 6;
+  static constexpr int kStages = 6;
   static constexpr int kTurn = KIND == kLse ? 16384 : E * 4096;
   static constexpr int kSmem = 1024 + kStages * kStage + kTurn + 256;
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 constexpr int kGroup = 8;          // row tiles that share the columns' operand before the next ones
-// Stages that the forward's accumulators sum before a new sum begins, in
-// registers: 1024 elements.  The tensor cores cut off, not round, at each of
-// their additions, so a logit of 7168 elements is low by 7.5e-6 of itself in one
-// sum, by 1.0e-6 in seven (2.4e-6 where every product has the same sign; 8 stages
-// a sum: 0.5e-6, but reading the accumulators twice as often costs 4 % of the
-// product; one sum: 3 % faster).  The backward
-// forms the same sums as the forward of as many tokens: softmax - 1 of a
-// confident token, a difference of nearly equal numbers, is then good to what
-// lse's FP32 holds (one sum: off by as much as itself at a logit of 40 and
-// probability 0.9997; faster by 1 to 2 %: 1531 x 1408 x 50021 346 and 354 us,
-// 2048 x 7168 x 131072 6.93 and 6.99 ms, 1 x 2048 x 131072 304 and 312 us).
-constexpr int kSegment = 16;
+// The tensor cores cut off, not round, at each of their additions, so a logit of
+// 7168 elements is low by 7.5e-6 of itself in one sum (by 17e-6 where all products
+// have one sign).  In the forward logits are therefore summed in segments, whose
+// sums are added up in registers (segment_of; few tokens: 64 elements each, which
+// costs them nothing), and of each row the one logit whose error does not show as
+// a share of its result, the target's, is formed apart in both directions:
+// pack_rows.  The backward's other logits are one sum: g is off by 1e-4 of itself
+// at a logit of 10, its rounding 2^-9.
 // Few tokens: at most 64, 32 a group of four epilogue warps.
 constexpr int kFew = 64;
 // Backward of at most so many rows that count: g in two parts, see product_rows.
 constexpr int kTwice = 64;
-constexpr int kFewSteps = 4;       // contraction steps of 64 a stage, which is also a segment
-constexpr int kFewSmem = 230 * 1000;
-static_assert(kFewSmem <= 232448, "shared memory per CTA");
+constexpr int kFewSteps = 4;       // contraction steps of 64 a stage; each is a sum of its own
+constexpr int kFewSmem = 228 * 1000;   // beside 3 KB that are static
+static_assert(kFewSmem + 3 * 1024 <= 232448, "shared memory per CTA");
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 constexpr float kLowest = -1.0e30f;
 
@@ -114,11 +110,11 @@ struct CeParams {
   int D, V;
   int v0, vn;            // piece of the vocabulary: first, number (backward)
   int first;             // dh: store (else add)
-  int segment;           // grad: stages that one sum of a logit takes, as in the forward
+  int segment;           // lse: stages that one sum of a logit takes
   float k;               // scale log2 e
   const int* target;     // [rows_cap], -1 past the rows
   float2* part;          // lse: [column tiles, or CTAs][rows_cap]: maximum of l k, sum of exp2(l k - maximum)
-  float* hit;            // lse: l_target (before the scale)
+  const float* hit;      // lse, grad: [rows_cap], l_target (before the scale) in FP32
   const float* lse2;     // grad: lse log2 e
   const float2* coef;    // grad: scale dl (1 + 2 z lse), scale dl
   const float* unit;     // backward: what g leaves out, and its reciprocal
@@ -244,6 +240,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 // One 16-byte piece of a warp's 32 rows x 128 bytes, in the 128-byte swizzle.
 __device__ __forceinline__ void stage16(uint8_t* ws, int lane, int piece, uint4 v) {
   *reinterpret_cast<uint4*>(ws + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
@@ -273,16 +275,14 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
   return r;
 }
 
-// Element i of 32 registers.
-__device__ __forceinline__ float pick(const float (&x)[32], int i) {
-  float v[16];
+// Where a row's target is among its 32 logits, columns c .. c + 31: the logit in FP32.
+__device__ __forceinline__ void take_target(float (&x)[32], int c, int row, int target, const CeParams& p) {
+  if (static_cast<unsigned>(target - c) < 32u) {
+    const float l = p.hit[row];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = (i & 16) ? x[16 + j] : x[j];
-#pragma unroll
-  for (int w = 8; w > 0; w >>= 1)
-#pragma unroll
-    for (int j = 0; j < w; ++j) v[j] = (i & w) ? v[w + j] : v[j];
-  return v[0];
+    for (int j = 0; j < 32; ++j)
+      if (target - c == j) x[j] = l;
+  }
 }
 
 // 32 logits of a row, columns c .. c + 31 of n, join its maximum and sum of exponentials.
@@ -293,7 +293,7 @@ __device__ __forceinline__ void join_chunk(float (&x)[32], int c, int n, int row
     for (int j = 0; j < 32; ++j)
       if (c + j >= n) x[j] = -INFINITY;
   }
-  if (static_cast<unsigned>(target - c) < 32u) p.hit[row] = pick(x, target - c);
+  take_target(x, c, row, target, p);
   float m = x[0];
 #pragma unroll
   for (int j = 1; j < 31; j += 2) m = max3(m, x[j], x[j + 1]);
@@ -313,14 +313,13 @@ __device__ __forceinline__ void join_chunk(float (&x)[32], int c, int n, int row
   sum += a + b;
 }
 
-// SUMS: the gradient's logits are summed in segments, p.segment stages each.
+// SUMS: logits are summed in segments, p.segment stages each.
 template <int KIND, int E, bool SUMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmC, const CeParams p) {
   constexpr bool kAMn = KIND == kDw, kBMn = KIND == kDh || KIND == kDw;
-  constexpr bool kSums = SUMS || (KIND == kLse && E == 8);   // a tile may take several accumulators
-  static_assert(!SUMS || (KIND == kGrad && E == 16), "tiles of 256 columns, 64 a thread");
+  static_assert(!SUMS || (KIND == kLse && E == 16), "tiles of 256 columns, 64 a thread");
   constexpr int kStages = CeCfg<KIND, E>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -423,13 +422,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
         // Sums of a tile, each in the accumulator whose turn it is; a loop of its own around the stages, which a test in
         // each of them slows down
         int ks = 0;
-        for (bool more = true; more; more = kSums && ks < t.ks) {
+        for (bool more = true; more; more = SUMS && ks < t.ks) {
           const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(&tempty[acc], aph ^ 1, abort_flag, p.err));
           if (!ok) break;
           tc_fence_after();
           const uint32_t d_tmem = tmem + acc * 256;
-          const int first = ks, end = kSums ? min(t.ks, ks + (SUMS ? p.segment : kSegment)) : t.ks;
+          const int first = ks, end = SUMS ? min(t.ks, ks + p.segment) : t.ks;
           for (; ks < end; ++ks, ++it) {
             const uint32_t slot = it % kStages, ph = (it / kStages) & 1;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(&full[slot], ph, abort_flag, p.err));
@@ -469,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
     int side = 0;
     const int whole = KIND == kGrad ? p.count[2] : 0;
     const float unit = KIND == kGrad ? p.unit[1] : KIND == kDw ? p.unit[0] : 1.0f;
-    bool dead = false;   // a wait ran out of time (forward: the tiles' barriers are still met)
+    bool dead = false;   // forward: a wait ran out of time; the tiles' barriers are still met
     struct {
       int target;
       float lse2;
@@ -485,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
         }
       }
     };
-    if (!SUMS && cid < w.total) row_values(cid);
+    if (cid < w.total) row_values(cid);
     for (int tile = cid; tile < w.total; tile += ncl) {
       const CeTile t = ce_tile<KIND, E>(w, tile);
       const int row = t.row0 + 128 * rank + 32 * q + lane;     // this thread's
@@ -494,70 +493,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
       // Whether anything reads this warp's rows: those that count; of g, which the dW product reads 64 rows at a
       // time, those up to a multiple of 64; of dW, the vocabulary's.
       const bool live = KIND == kDw ? p.v0 + row_w < p.V : row_w < (KIND == kGrad ? (w.m + 63) / 64 * 64 : w.m);
-      // what the rows need, asked for a tile ahead (in segments: while the first sum is formed)
-      if (SUMS) row_values(tile);
+      // what the rows need, asked for a tile ahead
       const int target = next.target - (KIND == kGrad ? p.v0 : 0);
       const float lse2 = next.lse2;
       const float2 coef = make_float2(next.coef.x * unit, next.coef.y * unit);
       const bool second = row >= whole;   // grad: what the rounding of the first row's g leaves over
       const bool seconds = KIND == kGrad && row_w + 31 >= whole && whole < w.m;
-      if (!SUMS && tile + ncl < w.total) row_values(tile + ncl);
+      if (tile + ncl < w.total) row_values(tile + ncl);
+      // the accumulator whose turn it is: complete (false: a wait ran out of time), its first column, free again
+      auto next_sum = [&] {
+        const bool there =
+            __all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[tc & 1], (tc >> 1) & 1, abort_flag, p.err));
+        tc_fence_after();
+        return there;
+      };
+      auto sum_at = [&] { return tmem + (tc & 1) * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16); };
+      auto sum_read = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * (tc & 1));
+      };
+// this thread's columns: the sums of the segments, added up (false: a wait ran out of time)
+      constexpr int kChunks = 32 / E;
+      auto sum_up = [&](float (&x)[kChunks][32]) {
+        for (int ks = 0; ks < t.ks; ks += p.segment, ++tc) {
+          if (!next_sum()) return false;
+          const uint32_t tbase = sum_at();
+#pragma unroll
+          for (int ci = 0; ci < kChunks; ++ci) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 16) {
+              uint32_t v[16];
+              tmem_ld16(tbase + 32 * ci + i, v);
+              tmem_ld_wait();
+              if (i == 16 && ci == kChunks - 1) sum_read();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                x[ci][i + j] = ks == 0 ? __uint_as_float(v[j]) : x[ci][i + j] + __uint_as_float(v[j]);
+            }
+          }
+        }
+        return true;
+      };
       if constexpr (KIND == kLse) {
         float top = kLowest, sum = 0.0f;
-        if (dead) {
-          // nothing is waited for, but the barrier below is met
-        } else if (E == 16 || t.ks <= kSegment) {   // one segment
-          const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-          ++tc;
-          dead = !__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err));
-          tc_fence_after();
-          const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
+        if constexpr (!SUMS) {
+          dead = dead || !next_sum();
+          const uint32_t tbase = sum_at();
 #pragma unroll 1
           for (int ci = 0; ci < (dead ? 0 : cols / 32); ++ci) {
             uint32_t v[32];
             tmem_ld32(tbase + 32 * ci, v);
             tmem_ld_wait();
-            if (ci == cols / 32 - 1) {   // every column has been read: the accumulator is free
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
-            }
+            if (ci == cols / 32 - 1) sum_read();   // every column has been read: the accumulator is free
             float x[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
             join_chunk(x, c0 + 32 * ci, w.n, row, target, p, top, sum);
           }
-        } else if constexpr (E == 8) {
-          // this thread's 128 columns: sums of the segments
-          float x[4][32];
-          for (int ks = 0; ks < t.ks; ks += kSegment, ++tc) {
-            const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-            dead = !__all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[acc], aph, abort_flag, p.err));
-            if (dead) break;
-            tc_fence_after();
-            const uint32_t tbase = tmem + acc * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16);
-            const bool last = ks + kSegment >= t.ks;
+          ++tc;
+        } else {
+          float x[kChunks][32];
+          dead = dead || !sum_up(x);
 #pragma unroll
-            for (int ci = 0; ci < 4; ++ci) {
-              if (ci >= 2 && cols == 64) continue;
-              uint32_t v[32];
-              tmem_ld32(tbase + 32 * ci, v);
-              tmem_ld_wait();
-              if (ci == (cols == 64 ? 1 : 3)) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
-              }
-              if (ks == 0) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[ci][j] = __uint_as_float(v[j]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[ci][j] += __uint_as_float(v[j]);
-              }
-              if (last) join_chunk(x[ci], c0 + 32 * ci, w.n, row, target, p, top, sum);
-            }
-          }
+          for (int ci = 0; ci < kChunks; ++ci)
+            if (!dead) join_chunk(x[ci], c0 + 32 * ci, w.n, row, target, p, top, sum);
         }
         // the warps that share the rows
         red[side][h][32 * q + lane] = make_float2(top, sum);
@@ -579,6 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
           const int c = c0 + 32 * ci;
           constexpr int kHalves = KIND == kDh ? 1 : 2;   // chunks of 32 columns in 128 bytes
           if constexpr (KIND == kGrad) {
+            take_target(x, c, row, target, p);
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = coef.x * exp2_fast(fmaf(x[j], p.k, -lse2));
             if (static_cast<unsigned>(target - c) < 32u) {
@@ -635,72 +636,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
             }
           }
         };
-        // the accumulator whose turn it is: complete (false: a wait ran out of time), its first column, free again
-        auto next_sum = [&] {
-          const bool there =
-              __all_sync(0xFFFFFFFFu, mbar_wait<true>(&tfull[tc & 1], (tc >> 1) & 1, abort_flag, p.err));
-          tc_fence_after();
-          return there;
-        };
-        auto sum_at = [&] { return tmem + (tc & 1) * 256 + h * cols + (static_cast<uint32_t>(q * 32) << 16); };
-        auto sum_read = [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * (tc & 1));
-        };
+        if (!next_sum()) break;
+        const uint32_t tbase = sum_at();
         if (!live) {
-          for (int ks = 0; ks == 0 || (SUMS && ks < t.ks); ks += p.segment, ++tc) {
-            dead = !next_sum();
-            if (dead) break;
-            sum_read();
-          }
-          if (dead) break;
-        } else if constexpr (!SUMS) {
-          if (!next_sum()) break;
-          const uint32_t tbase = sum_at();
-#pragma unroll 1
-          for (int ci = 0; ci < cols / 32; ++ci) {
-            uint32_t v[32];
-            tmem_ld32(tbase + 32 * ci, v);
-            tmem_ld_wait();
-            if (ci == cols / 32 - 1) sum_read();   // every column has been read: the accumulator is free
-            float x[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
-            if (KIND != kGrad && t.ks == 0) {   // an empty contraction
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = 0.0f;
-            }
-            put_chunk(x, ci);
-          }
+          sum_read();
           ++tc;
-        } else {
-          // this thread's columns: sums of the segments
-          constexpr int kChunks = 32 / E;
-          float x[kChunks][32];
-          for (int ks = 0; ks < t.ks; ks += p.segment, ++tc) {
-            dead = !next_sum();
-            if (dead) break;
-            const uint32_t tbase = sum_at();
-#pragma unroll
-            for (int ci = 0; ci < kChunks; ++ci) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 16) {
-                uint32_t v[16];
-                tmem_ld16(tbase + 32 * ci + i, v);
-                tmem_ld_wait();
-                if (i == 16 && ci == kChunks - 1) sum_read();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  x[ci][i + j] = ks == 0 ? __uint_as_float(v[j]) : x[ci][i + j] + __uint_as_float(v[j]);
-              }
-            }
-          }
-          if (dead) break;
-          // the accumulators are free: the next tile's products run beside this
-#pragma unroll
-          for (int ci = 0; ci < kChunks; ++ci) put_chunk(x[ci], ci);
+          continue;
         }
+#pragma unroll 1
+        for (int ci = 0; ci < cols / 32; ++ci) {
+          uint32_t v[32];
+          tmem_ld32(tbase + 32 * ci, v);
+          tmem_ld_wait();
+          if (ci == cols / 32 - 1) sum_read();   // every column has been read: the accumulator is free
+          float x[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+          if (KIND != kGrad && t.ks == 0) {   // an empty contraction
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+          }
+          put_chunk(x, ci);
+        }
+        ++tc;
       }
     }
     if (KIND != kLse && lane == 0) bulk_wait<0>();
@@ -736,6 +694,7 @@ __global__ void __launch_bounds__(64 + 4 * N, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ int targets[N];
+  __shared__ float hits[N];
   __shared__ float2 red[4][N];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -773,12 +732,15 @@ __global__ void __launch_bounds__(64 + 4 * N, 1)
     tma_prefetch(&tmH);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 2 * N);
+    tmem_alloc(tmem_slot, 2 * kFewSteps * N);
     tmem_relinquish();
   }
   after_previous();
   const int count = min(*p.count, N);
-  if (threadIdx.x < N) targets[threadIdx.x] = p.target[threadIdx.x];
+  if (threadIdx.x < N) {
+    targets[threadIdx.x] = p.target[threadIdx.x];
+    hits[threadIdx.x] = p.hit[threadIdx.x];   // anything past the rows that count, where the target is -1
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -827,9 +789,9 @@ __global__ void __launch_bounds__(64 + 4 * N, 1)
         if (lane == 0) {
           const uint32_t sa = smem_u32(smem + slot * kBytes), sb = sa + kFewSteps * kOperand;
 #pragma unroll
-          for (int j = 0; j < kFewSteps * kBk / 16; ++j)
-            mma_bf16(tmem + acc * N, sdesc_k_sw128(sa + (j >> 2) * kOperand + (j & 3) * 32),
-                     sdesc_k_sw128(sb + (j >> 2) * kStep + (j & 3) * 32), idesc, j ? 1u : 0u);
+          for (int j = 0; j < kFewSteps * kBk / 16; ++j)   // a sum each 64 elements
+            mma_bf16(tmem + (acc * kFewSteps + (j >> 2)) * N, sdesc_k_sw128(sa + (j >> 2) * kOperand + (j & 3) * 32),
+                     sdesc_k_sw128(sb + (j >> 2) * kStep + (j & 3) * 32), idesc, (j & 3) ? 1u : 0u);
           tc_commit(&empty[slot]);
           tc_commit(&tfull[acc]);
         }
@@ -859,11 +821,20 @@ __global__ void __launch_bounds__(64 + 4 * N, 1)
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], aph, abort_flag, p.err));
         if (!ok) break;
         tc_fence_after();
-        uint32_t v[32];
-        tmem_ld32(tmem + acc * N + j0 + (static_cast<uint32_t>(q * 32) << 16), v);
-        tmem_ld_wait();
+        const uint32_t at = tmem + acc * kFewSteps * N + j0 + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = ks == 0 ? __uint_as_float(v[j]) : x[j] + __uint_as_float(v[j]);
+        for (int i = 0; i < 32; i += 8) {   // the stage's sums in pairs
+          uint32_t v[kFewSteps][8];
+#pragma unroll
+          for (int k = 0; k < kFewSteps; ++k) tmem_ld8(at + k * N + i, v[k]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float s = (__uint_as_float(v[0][j]) + __uint_as_float(v[1][j])) +
+                            (__uint_as_float(v[2][j]) + __uint_as_float(v[3][j]));
+            x[i + j] = ks == 0 ? s : x[i + j] + s;
+          }
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[acc]);
@@ -872,7 +843,7 @@ __global__ void __launch_bounds__(64 + 4 * N, 1)
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         if (j0 + j >= count) break;
-        if (targets[j0 + j] == row) p.hit[j0 + j] = x[j];
+        if (targets[j0 + j] == row) x[j] = hits[j0 + j];
         const float m = fmaxf(top[j], x[j] * p.k);
         sum[j] = fmaf(sum[j], exp2_fast(top[j] - m), exp2_fast(fmaf(x[j], p.k, -m)));
         top[j] = m;
@@ -907,7 +878,7 @@ __global__ void __launch_bounds__(64 + 4 * N, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 2 * N);
+  if (warp == 1) tmem_dealloc(tmem, 2 * kFewSteps * N);
 }
 
 // ----------------------------------------------------- rows that count
@@ -936,6 +907,8 @@ struct RowParams {
   float scale, z;
   float* lse2;           // [rows_cap]
   float2* coef;          // [rows_cap]
+  const __nv_bfloat16* weight;
+  float* hit;            // [rows_cap] logit of each row's target
 };
 
 // Rows of the products.  The backward rounds g to BF16.  Of a few rows each
@@ -953,11 +926,11 @@ __device__ __forceinline__ int product_rows(const RowParams& p, int count) {
 }
 
 // A turn of 1024 tokens from t0, of which `base` rows that count come before:
-// the packed row of this thread's token (-1: it does not count) and the number
-// of rows after the turn.  counts: the warps', a turn's own.  write: put
+// the packed row of this thread's token (-1: it does not count) and its target,
+// and the number of rows after the turn.  counts: the warps', a turn's own.  write: put
 // down what the products need of the row, and keep in `most` the bits of this thread's largest finite |dl scale|;
 // tokens that do not count get their results: loss 0 (NaN for a target outside the vocabulary), lse 0.
-__device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, int* counts, bool write, uint32_t& most) {
+__device__ __forceinline__ int2 row_turn(const RowParams& p, int t0, int& base, int* counts, bool write, uint32_t& most) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = t0 + threadIdx.x;
   long long target = p.ignore;
@@ -1000,7 +973,7 @@ __device__ __forceinline__ int row_turn(const RowParams& p, int t0, int& base, i
     }
     if (t < p.T && p.inv) p.inv[t] = on ? at : -1;
   }
-  return on ? at : -1;
+  return on ? make_int2(at, static_cast<int>(target)) : make_int2(-1, -1);
 }
 
 // After the last turn: the number of rows, the unit, the second rows, and what
@@ -1049,42 +1022,84 @@ __device__ __forceinline__ void row_end(const RowParams& p, int count, uint32_t 
   }
 }
 
-// Row i of the packed copy of h, token t's (-1: zeros).
-__device__ __forceinline__ void pack_row(const RowParams& p, int i, int t) {
-  uint4* out = reinterpret_cast<uint4*>(p.packed + static_cast<long long>(i) * p.D);
-  const __nv_bfloat16* in = p.h + static_cast<long long>(max(t, 0)) * p.ldh;
-  for (int c = threadIdx.x; c < p.D / 8; c += blockDim.x) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (t >= 0) {
-      if (p.ldh % 8 == 0) {
-        v = reinterpret_cast<const uint4*>(in)[c];
-      } else {
-        const unsigned short* s = reinterpret_cast<const unsigned short*>(in) + 8 * c;
-        v.x = s[0] | static_cast<uint32_t>(s[1]) << 16;
-        v.y = s[2] | static_cast<uint32_t>(s[3]) << 16;
-        v.z = s[4] | static_cast<uint32_t>(s[5]) << 16;
-        v.w = s[6] | static_cast<uint32_t>(s[7]) << 16;
+// Rows 0 .. end - 1 of the packed copy of h, row i that of the token row_at(i).x (-1: zeros), with its logit of the
+// target row_at(i).y in FP32.  Where a token is confident, lse - l_target and softmax - 1 are differences of nearly equal numbers that show
+// what the tensor cores cut off: at a logit of 40 and probability 0.9997 a sum of 7168 elements there was off by as much
+// as the gradient.  It is the one entry of a row that cancels, so its logit alone is formed apart, the same way in both
+// directions, while the row and the target's weights are at hand (1.3 us of a call on one token, 2 of one on 1072 rows).
+// A row takes as many of the block's threads as it has pieces of eight elements (a power of two, warps at least), and the
+// rows go round the blocks first.
+template <typename RowAt>
+__device__ __forceinline__ void pack_rows(const RowParams& p, int end, RowAt row_at) {
+  __shared__ float sums[32];
+  const int pieces = p.D / 8, block = blockDim.x;
+  const int size = min(block, max(32, pieces > 1 ? 1 << (32 - __clz(pieces - 1)) : 1));
+  const int groups = block / size, group = threadIdx.x / size, at = threadIdx.x - group * size;
+  for (int i0 = blockIdx.x; i0 < end; i0 += gridDim.x * groups) {
+    const int i = i0 + group * gridDim.x;
+    const int2 row = i < end ? row_at(i) : make_int2(-1, -1);
+    const int t = row.x;
+    float s = 0.0f;
+    if (i < end) {
+      const __nv_bfloat16* in = p.h + static_cast<long long>(max(t, 0)) * p.ldh;
+      uint4* out = reinterpret_cast<uint4*>(p.packed + static_cast<long long>(i) * p.D);
+      const uint4* w = reinterpret_cast<const uint4*>(p.weight + static_cast<long long>(max(row.y, 0)) * p.D);
+      for (int c = at; c < pieces; c += size) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (t >= 0) {
+          if (p.ldh % 8 == 0) {
+            v = reinterpret_cast<const uint4*>(in)[c];
+          } else {
+            const unsigned short* e = reinterpret_cast<const unsigned short*>(in) + 8 * c;
+            v.x = e[0] | static_cast<uint32_t>(e[1]) << 16;
+            v.y = e[2] | static_cast<uint32_t>(e[3]) << 16;
+            v.z = e[4] | static_cast<uint32_t>(e[5]) << 16;
+            v.w = e[6] | static_cast<uint32_t>(e[7]) << 16;
+          }
+          const uint4 u = w[c];
+          float d = bf16_lo(v.x) * bf16_lo(u.x);
+          d = fmaf(bf16_hi(v.x), bf16_hi(u.x), d);
+          d = fmaf(bf16_lo(v.y), bf16_lo(u.y), d);
+          d = fmaf(bf16_hi(v.y), bf16_hi(u.y), d);
+          d = fmaf(bf16_lo(v.z), bf16_lo(u.z), d);
+          d = fmaf(bf16_hi(v.z), bf16_hi(u.z), d);
+          d = fmaf(bf16_lo(v.w), bf16_lo(u.w), d);
+          s += fmaf(bf16_hi(v.w), bf16_hi(u.w), d);
+        }
+        out[c] = v;
       }
     }
-    out[c] = v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (size > 32) {   // the row's warps, in their order
+      if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+      __syncthreads();
+      if (at == 0) {
+        s = 0.0f;
+        for (int k = 0; k < size / 32; ++k) s += sums[(threadIdx.x >> 5) + k];
+      }
+      __syncthreads();   // before the next rows' sums
+    }
+    if (at == 0 && t >= 0) p.hit[i] = s;
   }
 }
 
 // Up to 1024 tokens: every block finds the rows that count, the first writes them down, and all pack them.
 __global__ void __launch_bounds__(1024) ce_rows_once_kernel(const __grid_constant__ RowParams p) {
-  __shared__ int counts[32], list[1024];
+  __shared__ int counts[32];
+  __shared__ int2 list[1024];
   // in this order: the forward of few tokens reads the weight before its own wait, and whatever ran before this call
   // has ended then
   wait_previous();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int count = 0;
   uint32_t most = 0;
-  const int at = row_turn(p, 0, count, counts, blockIdx.x == 0, most);
-  if (at >= 0) list[at] = threadIdx.x;
+  const int2 mine = row_turn(p, 0, count, counts, blockIdx.x == 0, most);
+  if (mine.x >= 0) list[mine.x] = make_int2(threadIdx.x, mine.y);
   if (blockIdx.x == 0) row_end(p, count, most);
   __syncthreads();
   const int rows = product_rows(p, count), end = (rows + kTile - 1) / kTile * kTile;
-  for (int i = blockIdx.x; i < end; i += gridDim.x) pack_row(p, i, i < rows ? list[i < count ? i : i - count] : -1);
+  pack_rows(p, end, [&](int i) { return i < rows ? list[i < count ? i : i - count] : make_int2(-1, -1); });
 }
 
 // More tokens: one block finds the rows, 1024 tokens a turn, and others pack them.
@@ -1099,7 +1114,7 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const __grid_constant__ R
 __global__ void __launch_bounds__(256) ce_pack_kernel(const __grid_constant__ RowParams p) {
   after_previous();
   const int count = *p.count, end = (count + kTile - 1) / kTile * kTile;
-  for (int i = blockIdx.x; i < end; i += gridDim.x) pack_row(p, i, p.list[i]);
+  pack_rows(p, end, [&](int i) { return make_int2(p.list[i], p.target[i]); });
 }
 
 // loss and lse of the packed rows from the tiles' maxima and sums: 32 rows a
@@ -1228,6 +1243,7 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
   l.list = take(&at, rows * 4);
   l.target = take(&at, rows * 4);
   l.packed = take(&at, rows * D * 2);
+  l.hit = take(&at, rows * 4);
   if (backward) {
     l.inv = take(&at, rows * 4);
     l.lse2 = take(&at, rows * 4);
@@ -1235,7 +1251,6 @@ Layout lay_out(const moe_linear_ce_config* c, bool backward, int64_t piece, int 
     l.dh = take(&at, static_cast<size_t>(l.dh_rows) * D * 4);
     l.g = take(&at, rows * 2 * l.piece);
   } else {
-    l.hit = take(&at, rows * 4);
     // a column a tile, or for few tokens one a CTA; room for either, so that fewer tokens never want more
     l.part = take(&at, 8 * std::max(rows * l.col_tiles, c->tokens ? static_cast<size_t>(kTile) * sms : 0));
   }
@@ -1268,21 +1283,27 @@ cudaError_t launch_gemm_as(const CUtensorMap& a, const CUtensorMap& b, const CUt
   return launch_dependent(reinterpret_cast<const void*>(ce_gemm_kernel<KIND, E, SUMS>), dim3(grid), C::kThreads, C::kSmem,
                           stream, args);
 }
-// Sixteen epilogue warps where the forward's product is too short to hide eight
-// warps' exponentials and takes one segment (512 x 256 x 32768 22.8 and 20.2 us,
-// 4096 x 512 x 65536 224 and 210, 4096 x 1024 x 65536 373 and 366).  The
-// backward's first product gained nothing in one sum; in several, sixteen warps
-// have 64 columns a thread to keep and spill little (64 x 2048 x 131072 318 us,
-// eight warps 323 to 341, before the tensor cores' loop was split in sums, which
-// took it to 311; 2048 x 7168 x 131072 6.99 and 7.08 ms).
+// Stages of 64 elements that one sum of a logit takes in the forward of more than
+// kFew tokens: short enough that the loss is as good as torch's FP32 products make
+// it (error in norm against 64 bits, and theirs: D 512 0.5e-6 and 0.5e-6, 1024 0.5
+// and 0.75, 1408 0.85 and 0.9, 2048 1.0 and 1.2, 7168 1.0 and 2.5).  512 instead of
+// 1024 elements a sum: 4096 x 1024 x 65536 416 and 390 us, 4096 x 2048 x 131072
+// 1.30 and 1.23 ms.
+int segment_of(int D) { return D <= 1024 ? 8 : 16; }
+
+// Sixteen epilogue warps in the forward: eight do not hide the exponentials of a
+// short product (512 x 256 x 32768 22.8 and 20.2 us, 4096 x 512 x 65536 224 and
+// 210), and would have 128 columns of sums a thread to keep instead of 64, which
+// spills (2048 x 7168 x 131072 2.39 and 2.25 ms).  The backward's products gained
+// nothing.
 template <int KIND>
 cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CeParams& p, int pairs,
                         long long tiles, cudaStream_t stream) {
   if constexpr (KIND == kLse)
-    if (p.D <= kSegment * kBk) return launch_gemm_as<KIND, 16>(a, b, c, p, pairs, tiles, stream);
-  if constexpr (KIND == kGrad)
-    if (p.D > p.segment * kBk) return launch_gemm_as<KIND, 16, true>(a, b, c, p, pairs, tiles, stream);
-  return launch_gemm_as<KIND, 8>(a, b, c, p, pairs, tiles, stream);
+    return p.D > p.segment * kBk ? launch_gemm_as<KIND, 16, true>(a, b, c, p, pairs, tiles, stream)
+                                 : launch_gemm_as<KIND, 16>(a, b, c, p, pairs, tiles, stream);
+  else
+    return launch_gemm_as<KIND, 8>(a, b, c, p, pairs, tiles, stream);
 }
 
 template <int N>
@@ -1315,8 +1336,8 @@ X* at(void* base, size_t off) {
 }
 
 // What the calls share: rows packed, parameters of the products.
-void fill(const moe_linear_ce_config* c, const Layout& l, const void* h, const void* targets, void* ws, uint32_t* err,
-          RowParams* r, CeParams* p) {
+void fill(const moe_linear_ce_config* c, const Layout& l, const void* h, const void* weight, const void* targets, void* ws,
+          uint32_t* err, RowParams* r, CeParams* p) {
   r->T = c->tokens;
   r->D = c->d_model;
   r->V = c->vocab;
@@ -1330,12 +1351,16 @@ void fill(const moe_linear_ce_config* c, const Layout& l, const void* h, const v
   r->list = at<int>(ws, l.list);
   r->target = at<int>(ws, l.target);
   r->packed = at<__nv_bfloat16>(ws, l.packed);
+  r->weight = static_cast<const __nv_bfloat16*>(weight);
+  r->hit = at<float>(ws, l.hit);
   r->scale = c->logit_scale;
   r->z = c->z_weight;
   p->count = r->count;
   p->rows_cap = l.rows_cap;
   p->D = c->d_model;
   p->V = c->vocab;
+  p->segment = segment_of(c->d_model);
+  p->hit = r->hit;
   p->k = c->logit_scale * kLog2e;
   p->target = r->target;
   p->err = err;
@@ -1372,11 +1397,10 @@ moe_status moe_linear_ce_forward(const moe_linear_ce_config* cfg, const void* h,
   if (workspace_bytes < l.bytes) return MOE_ERR_CAPACITY;
   RowParams r{};
   CeParams p{};
-  fill(cfg, l, h, targets, workspace, device_error_word, &r, &p);
+  fill(cfg, l, h, weight, targets, workspace, device_error_word, &r, &p);
   r.loss = loss;
   r.lse = lse;
   p.part = at<float2>(workspace, l.part);
-  p.hit = at<float>(workspace, l.hit);
   if (launch_rows(r, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   int parts = l.col_tiles;
   if (few(cfg->tokens)) {
@@ -1431,7 +1455,7 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
   l = lay_out(cfg, true, (l.col_tiles + pieces - 1) / pieces * kTile, sms);
   RowParams r{};
   CeParams p{};
-  fill(cfg, l, h, targets, workspace, device_error_word, &r, &p);
+  fill(cfg, l, h, weight, targets, workspace, device_error_word, &r, &p);
   r.lse_in = lse;
   r.dloss = d_loss;
   r.inv = at<int>(workspace, l.inv);
@@ -1441,7 +1465,6 @@ moe_status moe_linear_ce_backward(const moe_linear_ce_config* cfg, const void* h
   p.coef = r.coef;
   r.unit = at<float>(workspace, l.unit);
   p.unit = r.unit;
-  p.segment = few(T) ? kFewSteps : kSegment;
   r.dh = {D, static_cast<int>(l.piece / kBk), sms / 2, static_cast<int>(l.dh_rows)};
   __nv_bfloat16* g = at<__nv_bfloat16>(workspace, l.g);
   float* part = at<float>(workspace, l.dh);
