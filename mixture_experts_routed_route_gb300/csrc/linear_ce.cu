@@ -513,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * (tc & 1));
       };
-// this thread's columns: the sums of the segments, added up (false: a wait ran out of time)
+      // this thread's columns: the sums of the segments, added up (false: a wait ran out of time)
       constexpr int kChunks = 32 / E;
       auto sum_up = [&](float (&x)[kChunks][32]) {
         for (int ks = 0; ks < t.ks; ks += p.segment, ++tc) {
@@ -574,8 +574,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
         }
         side ^= 1;
       } else {
-        // 32 columns of a row, chunk ci of the warp's, on their way out
-        auto put_chunk = [&](float (&x)[32], int ci) {
+        if (!next_sum()) break;
+        const uint32_t tbase = sum_at();
+        if (!live) {
+          sum_read();
+          ++tc;
+          continue;
+        }
+#pragma unroll 1
+        for (int ci = 0; ci < cols / 32; ++ci) {
+          uint32_t v[32];
+          tmem_ld32(tbase + 32 * ci, v);
+          tmem_ld_wait();
+          if (ci == cols / 32 - 1) sum_read();   // every column has been read: the accumulator is free
+          float x[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+          if (KIND != kGrad && t.ks == 0) {   // an empty contraction
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+          }
           const int c = c0 + 32 * ci;
           constexpr int kHalves = KIND == kDh ? 1 : 2;   // chunks of 32 columns in 128 bytes
           if constexpr (KIND == kGrad) {
@@ -635,28 +653,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CeCfg<KIND, E>::kThr
               bulk_commit();
             }
           }
-        };
-        if (!next_sum()) break;
-        const uint32_t tbase = sum_at();
-        if (!live) {
-          sum_read();
-          ++tc;
-          continue;
-        }
-#pragma unroll 1
-        for (int ci = 0; ci < cols / 32; ++ci) {
-          uint32_t v[32];
-          tmem_ld32(tbase + 32 * ci, v);
-          tmem_ld_wait();
-          if (ci == cols / 32 - 1) sum_read();   // every column has been read: the accumulator is free
-          float x[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
-          if (KIND != kGrad && t.ks == 0) {   // an empty contraction
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = 0.0f;
-          }
-          put_chunk(x, ci);
         }
         ++tc;
       }
